@@ -290,6 +290,148 @@ kvq_status kvq_decode_attention_noalloc(const kvq_config* cfg, const kvq_cache* 
                                         const uint16_t* q, int32_t q_heads, float scale,
                                         float* out, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Paged cache: a pool of pages that sequences of any length share, written
+ * token by token, in 4-bit codes with one fp16 scale per token and kv head.
+ * A token's codes are final when they are written (no residual, no flush), so
+ * sequences grow, end and share pages without moving data.
+ *
+ * Flag sets of kvq_config for these calls (bits must be 4, head_dim 64 or 128):
+ *   0             per-token absmax of x (the codes and scales of the naive mode)
+ *   KVQ_HADAMARD  the same of the rotated vector R x, R = H diag(signs) / sqrt(d)
+ * The rotation spreads outlier channels over the vector, which is what the
+ * per-channel scales of the block cache are for; norm separation would change
+ * nothing, since the token's scale takes the norm with it.
+ *
+ * Stored per token, head and tensor:
+ *   y     = x or R x in fp32 (butterflies of strides 1, 2, .., d/2 in that
+ *           order, then one multiplication by 1/sqrt(d))
+ *   sigma = fp16(min(max|y| / 7, 65504)),  r = 1 / sigma in fp32 (0 if sigma is 0)
+ *   codes = rint(y r) clamped to +-7 (half to even, from the exact product),
+ *           kept as e = q + 8, channel 2j in the low nibble of byte j
+ * Inputs beyond +-65504 and infinities are taken as +-65504, NaN as 0.
+ */
+
+/*
+ * The pool.  Caller-allocated; index [2] selects K (0) or V (1).
+ *   codes[i] uint8 [n_pages][kv_heads][page_tokens][head_dim / 2]
+ *   tok[i]   fp16  [n_pages][kv_heads][page_tokens]     the scales
+ * page_tokens in {16, 32, 64, 128}; n_pages * kv_heads * page_tokens < 2^31.
+ * What the slots hold that no sequence has reached does not matter.
+ */
+typedef struct {
+    int32_t n_pages, kv_heads, head_dim, page_tokens;
+    uint8_t* codes[2];
+    uint16_t* tok[2];
+} kvq_pages;
+
+/*
+ * Which rows of a call's tensors are which tokens.  Device arrays:
+ *   start int32 [n_seqs + 1]  not decreasing; rows start[s] .. start[s+1] - 1
+ *                             are the LAST tokens of sequence s, in order
+ *   len   int32 [n_seqs]      tokens of sequence s, those rows included
+ *   table int32 [n_seqs][table_stride], of each row the first max_pages are
+ *         used: token t of sequence s is slot t % page_tokens of page
+ *         table[s][t / page_tokens]
+ * Row start[s] + i is thus token len[s] - (start[s+1] - start[s]) + i.  Rows
+ * whose token is negative (more rows than tokens) are padding, and so are
+ * rows before start[0], from start[n_seqs] on, and past the call's `rows`.
+ * A generation step has one row a sequence, a prompt or a part of one many;
+ * both may be in one batch, and a sequence may have no rows.
+ * max_rows (host): the most rows one sequence has; 0 = not known.  It only
+ * chooses between kernels: too small a value costs time, never results.
+ * Page numbers outside [0, n_pages) and tokens past max_pages pages are never
+ * followed: the token is left out, and bit 2 of the word that
+ * kvq_pages_read_errors reads is set.
+ */
+typedef struct {
+    int32_t n_seqs, max_pages, table_stride, max_rows;
+    const int32_t* start;
+    const int32_t* len;
+    const int32_t* table;
+} kvq_batch;
+
+enum { KVQ_F16 = 0, KVQ_BF16 = 1, KVQ_F32 = 2 };
+
+/*
+ * A tensor [rows][heads][head_dim] on the device: element (r, h, c) is at
+ * data + r * row_stride + h * head_stride + c, strides in elements (so K, V
+ * and queries may be slices of one fused projection).  data is 16-byte
+ * aligned and the strides are multiples of 16 bytes; a stride may be 0 or
+ * negative in an input, not in an output.
+ */
+typedef struct {
+    void* data;
+    int64_t row_stride, head_stride;
+    int32_t dtype;    /* KVQ_F16, KVQ_BF16, or KVQ_F32 for kvq_pages_read's outputs */
+    int32_t reserved; /* must be 0 */
+} kvq_rows;
+
+/*
+ * Quantize the rows of k and v (fp16 or bf16, `rows` rows of kv_heads heads)
+ * into their slots.  Padding rows are not stored; no other slot is touched.
+ * Rows of one call must not share a slot: where two sequences' tables send two
+ * rows of a call to one slot, what that slot holds afterwards is undefined
+ * (other slots are not affected).
+ * rows == 0 or n_seqs == 0 enqueue nothing.
+ * Errors: INVALID_ARG; UNSUPPORTED (flags, bits, head_dim, page_tokens,
+ * dtype, sizes past the limits above, rows * kv_heads >= 2^31); CUDA.
+ */
+kvq_status kvq_pages_write(const kvq_config* cfg, const kvq_pages* pages, const kvq_batch* batch,
+                           const kvq_rows* k, const kvq_rows* v, int64_t rows, void* stream);
+
+/*
+ * Rebuild the rows' K and V from the cache: sigma q, or R^T (sigma q) under
+ * KVQ_HADAMARD, in fp32, rounded once to the output's type (fp16 saturates at
+ * +-65504).  k_out or v_out may be NULL.  Rows start[s] .. are the sequence's
+ * last tokens, so start = the running sum of len reads whole sequences, and a
+ * smaller len ends the range earlier.  Rows whose token is negative, or whose page is
+ * refused, become zeros; rows before start[0] and from start[n_seqs] on are left as they were.
+ * Errors: as kvq_pages_write.
+ */
+kvq_status kvq_pages_read(const kvq_config* cfg, const kvq_pages* pages, const kvq_batch* batch,
+                          const kvq_rows* k_out, const kvq_rows* v_out, int64_t rows, void* stream);
+
+/* Workspace bytes of kvq_pages_attention for batches of at most this n_seqs,
+   `rows` and max_rows (partial softmax states of the sequence splits; it depends on the
+   current device's SM count); 0 on invalid arguments.  Contents need no
+   initialization; calls that share a workspace must not overlap in time. */
+size_t kvq_pages_attention_workspace_bytes(const kvq_config* cfg, const kvq_pages* pages, const kvq_batch* batch,
+                                           int64_t rows, int32_t q_heads);
+
+/*
+ * Attention of the rows' queries over their sequences in the paged cache:
+ *   out[r, j] = sum_t softmax_t(scale * q[r, j] . k_hat[t, g]) v_hat[t, g]
+ * with g = j / (q_heads / kv_heads), over the tokens t of the row's sequence
+ * that the row sees: all up to and with its own token (causal != 0), or all
+ * len[s] of them (causal == 0); with window > 0 (causal only) the last
+ * `window` of these.  The rows' own tokens are written before (kvq_pages_write).
+ *   q     fp16 or bf16, `rows` rows of q_heads heads, q_heads a multiple of kv_heads
+ *   scale softmax scale; <= 0 selects 1/sqrt(head_dim)
+ *   out   the type of q (fp16 saturates at +-65504); must not overlap q
+ *   lse   fp32 [rows][q_heads], the natural logarithm of the sum of
+ *         exp(scale * q . k_hat), or NULL
+ * A row that sees no token (padding inside a sequence, an empty sequence)
+ * gives zeros and lse -inf; rows of no sequence are left as they were.
+ * Scores, softmax statistics and sums are fp32; the rotated query is kept to
+ * 22 bits and a token's probability times its value scale is rounded to fp16.
+ * Errors: INVALID_ARG; WORKSPACE; UNSUPPORTED (as kvq_pages_write; rows *
+ * q_heads >= 2^31; q_heads / kv_heads > 256); CUDA.
+ */
+kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, const kvq_batch* batch,
+                               const kvq_rows* q, int32_t q_heads, int64_t rows, float scale, int32_t causal,
+                               int32_t window, const kvq_rows* out, float* lse, void* ws, size_t ws_bytes,
+                               void* stream);
+
+/*
+ * Read (and, if clear != 0, reset) the sticky error word of the paged calls on
+ * the current device: bits 0 and 1 as in kvq_read_device_errors (which covers
+ * the other calls), bit 2 = a page number or token outside its range was left
+ * out.  HOST call; synchronizes the device.
+ * Errors: INVALID_ARG (host_out NULL); CUDA.
+ */
+kvq_status kvq_pages_read_errors(uint32_t* host_out, int32_t clear);
+
 /*
  * Read (and, if clear != 0, reset) the sticky device error word of the
  * current device: bit 0 = a kernel gave up waiting for a TMA tile, bit 1 = a

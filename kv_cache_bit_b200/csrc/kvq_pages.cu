@@ -1,0 +1,279 @@
+// kvq_pages.cu -- host side of the paged 4-bit cache (kvq_pages_* of
+// include/kvq.h): argument checks and launches.  A translation unit of its
+// own, with its own copy of the device error word of kvq_device.cuh, which
+// kvq_pages_read_errors reads.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include <nvtx3/nvToolsExt.h>
+
+#include "kvq.h"
+#include "kvq_pages.cuh"
+#include "kvq_pages_attn.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int64_t kMaxIndex = int64_t(1) << 31;
+constexpr int kMaxGroup = 256;  // query heads per kv head
+
+struct NvtxRange {
+    explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
+    ~NvtxRange() { nvtxRangePop(); }
+    NvtxRange(const NvtxRange&) = delete;
+    NvtxRange& operator=(const NvtxRange&) = delete;
+};
+
+bool ok_ptr(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool ok_ints(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+kvq_status launch_status() { return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA; }
+
+// Configuration, pool and batch; the checks every paged call shares.
+kvq_status check_paged(const kvq_config* cfg, const kvq_pages* p, const kvq_batch* b, int64_t rows) {
+    if (cfg == nullptr || p == nullptr || b == nullptr) return KVQ_ERR_INVALID_ARG;
+    if (cfg->reserved != 0 || rows < 0) return KVQ_ERR_INVALID_ARG;
+    if (cfg->signs != nullptr && !ok_ptr(cfg->signs)) return KVQ_ERR_INVALID_ARG;
+    if (cfg->bits != 4 || (cfg->head_dim != 64 && cfg->head_dim != 128)) return KVQ_ERR_UNSUPPORTED;
+    if (cfg->flags != 0 && cfg->flags != KVQ_HADAMARD) return KVQ_ERR_UNSUPPORTED;
+    if (p->n_pages < 1 || p->kv_heads < 1 || p->head_dim != cfg->head_dim) return KVQ_ERR_INVALID_ARG;
+    const int t = p->page_tokens;
+    if (t != 16 && t != 32 && t != 64 && t != 128) return KVQ_ERR_UNSUPPORTED;
+    for (int i = 0; i < 2; ++i)
+        if (!ok_ptr(p->codes[i]) || !ok_ptr(p->tok[i])) return KVQ_ERR_INVALID_ARG;
+    if ((int64_t)p->n_pages * p->kv_heads >= kMaxIndex / t) return KVQ_ERR_UNSUPPORTED;
+    if (b->n_seqs < 0 || b->max_rows < 0) return KVQ_ERR_INVALID_ARG;
+    if (b->n_seqs > 0) {
+        if (b->max_pages < 1 || b->table_stride < b->max_pages) return KVQ_ERR_INVALID_ARG;
+        if (!ok_ints(b->start) || !ok_ints(b->len) || !ok_ints(b->table)) return KVQ_ERR_INVALID_ARG;
+        if ((int64_t)b->max_pages * t >= kMaxIndex) return KVQ_ERR_UNSUPPORTED;
+    }
+    return KVQ_OK;
+}
+
+// A rows tensor; strides of dimensions of one element are not looked at.
+kvq_status check_rows(const kvq_rows* x, int64_t rows, int heads, int d, bool output, bool f32) {
+    if (x == nullptr || !ok_ptr(x->data) || x->reserved != 0) return KVQ_ERR_INVALID_ARG;
+    if (x->dtype != KVQ_F16 && x->dtype != KVQ_BF16 && !(f32 && x->dtype == KVQ_F32)) return KVQ_ERR_UNSUPPORTED;
+    const int64_t unit = x->dtype == KVQ_F32 ? 4 : 8;  // elements of 16 bytes
+    const int64_t rs = rows > 1 ? x->row_stride : 0, hs = heads > 1 ? x->head_stride : 0;
+    if (rs % unit != 0 || hs % unit != 0) return KVQ_ERR_INVALID_ARG;
+    if (rs > (INT64_MAX >> 36) || rs < -(INT64_MAX >> 36) || hs > (INT64_MAX >> 36) || hs < -(INT64_MAX >> 36))
+        return KVQ_ERR_INVALID_ARG;
+    if (output) {  // no two elements in one place: rows inside heads or heads inside rows
+        if ((rows > 1 && rs < d) || (heads > 1 && hs < d)) return KVQ_ERR_INVALID_ARG;
+        if (rows > 1 && heads > 1 && rs < (heads - 1) * hs + d && hs < (rows - 1) * rs + d) return KVQ_ERR_INVALID_ARG;
+    }
+    return KVQ_OK;
+}
+
+// Bytes [lo, hi) from the first to the last element.
+void extent(const kvq_rows* x, int64_t rows, int heads, int d, intptr_t* lo, intptr_t* hi) {
+    const int64_t size = x->dtype == KVQ_F32 ? 4 : 2;
+    const int64_t r = (rows - 1) * x->row_stride * (rows > 1), h = (heads - 1) * x->head_stride * (heads > 1);
+    const intptr_t at = reinterpret_cast<intptr_t>(x->data);
+    *lo = at + size * ((r < 0 ? r : 0) + (h < 0 ? h : 0));
+    *hi = at + size * ((r > 0 ? r : 0) + (h > 0 ? h : 0) + d);
+}
+
+Batch batch_of(const kvq_batch* b) {
+    return Batch{b->start, b->len, b->table, b->n_seqs, b->max_pages, b->table_stride};
+}
+
+Pool pool_of(const kvq_pages* p) {
+    Pool o;
+    for (int i = 0; i < 2; ++i) {
+        o.codes[i] = p->codes[i];
+        o.tok[i] = reinterpret_cast<__half*>(p->tok[i]);
+    }
+    o.n_pages = p->n_pages;
+    o.H = p->kv_heads;
+    o.page_log2 = p->page_tokens == 16 ? 4 : p->page_tokens == 32 ? 5 : p->page_tokens == 64 ? 6 : 7;
+    return o;
+}
+
+float rsqd_of(int d) { return (float)(1.0 / std::sqrt((double)d)); }
+
+// Compile-time dispatch over (head_dim, element type, rotation).
+template <int D, typename T, typename Fn>
+kvq_status dispatch_had(bool had, Fn& fn) {
+    return had ? fn.template run<D, T, true>() : fn.template run<D, T, false>();
+}
+
+template <typename Fn>
+kvq_status dispatch(int d, int dtype, bool had, Fn& fn) {
+    if (dtype == KVQ_F16) return d == 64 ? dispatch_had<64, __half>(had, fn) : dispatch_had<128, __half>(had, fn);
+    return d == 64 ? dispatch_had<64, __nv_bfloat16>(had, fn) : dispatch_had<128, __nv_bfloat16>(had, fn);
+}
+
+struct WriteLaunch {
+    WriteArgs a;
+    unsigned grid;
+    cudaStream_t st;
+    template <int D, typename T, bool HAD>
+    kvq_status run() {
+        pages_write_kernel<D, T, HAD><<<dim3(grid, 2), kWriteThreads, 0, st>>>(a);
+        return launch_status();
+    }
+};
+
+struct ReadLaunch {
+    ReadArgs a;
+    unsigned grid;
+    cudaStream_t st;
+    template <int D, typename T, bool HAD>
+    kvq_status run() {
+        pages_read_kernel<D, T, HAD><<<dim3(grid, a.only >= 0 ? 1 : 2), kWriteThreads, 0, st>>>(a);
+        return launch_status();
+    }
+};
+
+struct AttnLaunch {
+    AttnArgs a;
+    cudaStream_t st;
+    template <int D, typename T, bool HAD>
+    kvq_status run() {
+        pages_attn_simple_kernel<D, T, HAD><<<dim3(a.rows, a.Hq), 128, 0, st>>>(a);
+        return launch_status();
+    }
+};
+
+kvq_status check_attention(const kvq_config* cfg, const kvq_pages* p, const kvq_batch* b, int64_t rows, int q_heads) {
+    const kvq_status s = check_paged(cfg, p, b, rows);
+    if (s != KVQ_OK) return s;
+    if (q_heads < p->kv_heads || q_heads % p->kv_heads != 0) return KVQ_ERR_INVALID_ARG;
+    if (q_heads / p->kv_heads > kMaxGroup || q_heads > 65535 || rows >= kMaxIndex / q_heads)
+        return KVQ_ERR_UNSUPPORTED;
+    return KVQ_OK;
+}
+
+}  // namespace
+}  // namespace kvq
+
+using namespace kvq;
+
+extern "C" {
+
+kvq_status kvq_pages_write(const kvq_config* cfg, const kvq_pages* pages, const kvq_batch* batch, const kvq_rows* k,
+                           const kvq_rows* v, int64_t rows, void* stream) {
+    NvtxRange nvtx_range("kvq_pages_write");
+    kvq_status s = check_paged(cfg, pages, batch, rows);
+    if (s != KVQ_OK) return s;
+    const int H = pages->kv_heads, d = cfg->head_dim;
+    if (rows >= kMaxIndex / H / 4) return KVQ_ERR_UNSUPPORTED;  // lanes are counted in 32 bits
+    if ((s = check_rows(k, rows, H, d, false, false)) != KVQ_OK) return s;
+    if ((s = check_rows(v, rows, H, d, false, false)) != KVQ_OK) return s;
+    if (k->dtype != v->dtype) return KVQ_ERR_INVALID_ARG;
+    if (rows == 0 || batch->n_seqs == 0) return KVQ_OK;
+    WriteLaunch L;
+    L.a.b = batch_of(batch);
+    L.a.p = pool_of(pages);
+    const kvq_rows* x[2] = {k, v};
+    for (int i = 0; i < 2; ++i) {
+        L.a.x[i] = x[i]->data;
+        L.a.row_stride[i] = rows > 1 ? x[i]->row_stride : 0;
+        L.a.head_stride[i] = H > 1 ? x[i]->head_stride : 0;
+    }
+    L.a.signs = cfg->signs;
+    L.a.rows = (int)rows;
+    L.a.rsqd = rsqd_of(d);
+    L.grid = (unsigned)((rows * H * 4 + kWriteThreads - 1) / kWriteThreads);
+    L.st = static_cast<cudaStream_t>(stream);
+    return dispatch(d, k->dtype, cfg->flags == KVQ_HADAMARD, L);
+}
+
+kvq_status kvq_pages_read(const kvq_config* cfg, const kvq_pages* pages, const kvq_batch* batch, const kvq_rows* k_out,
+                          const kvq_rows* v_out, int64_t rows, void* stream) {
+    NvtxRange nvtx_range("kvq_pages_read");
+    kvq_status s = check_paged(cfg, pages, batch, rows);
+    if (s != KVQ_OK) return s;
+    const int H = pages->kv_heads, d = cfg->head_dim;
+    if (rows >= kMaxIndex / H / 4) return KVQ_ERR_UNSUPPORTED;
+    if (k_out == nullptr && v_out == nullptr) return KVQ_ERR_INVALID_ARG;
+    const kvq_rows* x[2] = {k_out, v_out};
+    for (int i = 0; i < 2; ++i)
+        if (x[i] != nullptr && (s = check_rows(x[i], rows, H, d, true, true)) != KVQ_OK) return s;
+    if (k_out != nullptr && v_out != nullptr && (k_out->dtype != v_out->dtype || k_out->data == v_out->data))
+        return KVQ_ERR_INVALID_ARG;
+    if (rows == 0 || batch->n_seqs == 0) return KVQ_OK;
+    ReadLaunch L;
+    L.a.b = batch_of(batch);
+    L.a.p = pool_of(pages);
+    for (int i = 0; i < 2; ++i) {
+        L.a.out[i] = x[i] ? x[i]->data : nullptr;
+        L.a.row_stride[i] = x[i] && rows > 1 ? x[i]->row_stride : 0;
+        L.a.head_stride[i] = x[i] && H > 1 ? x[i]->head_stride : 0;
+    }
+    L.a.signs = cfg->signs;
+    L.a.rows = (int)rows;
+    L.a.only = k_out == nullptr ? 1 : v_out == nullptr ? 0 : -1;
+    L.a.rsqd = rsqd_of(d);
+    L.grid = (unsigned)((rows * H * 4 + kWriteThreads - 1) / kWriteThreads);
+    L.st = static_cast<cudaStream_t>(stream);
+    const bool had = cfg->flags == KVQ_HADAMARD;
+    const int dtype = (k_out ? k_out : v_out)->dtype;
+    if (dtype == KVQ_F32) return d == 64 ? dispatch_had<64, float>(had, L) : dispatch_had<128, float>(had, L);
+    return dispatch(d, dtype, had, L);
+}
+
+size_t kvq_pages_attention_workspace_bytes(const kvq_config* cfg, const kvq_pages* pages, const kvq_batch* batch,
+                                           int64_t rows, int32_t q_heads) {
+    if (check_attention(cfg, pages, batch, rows, q_heads) != KVQ_OK) return 0;
+    return 16;
+}
+
+kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, const kvq_batch* batch,
+                               const kvq_rows* q, int32_t q_heads, int64_t rows, float scale, int32_t causal,
+                               int32_t window, const kvq_rows* out, float* lse, void* ws, size_t ws_bytes,
+                               void* stream) {
+    NvtxRange nvtx_range("kvq_pages_attention");
+    kvq_status s = check_attention(cfg, pages, batch, rows, q_heads);
+    if (s != KVQ_OK) return s;
+    const int d = cfg->head_dim;
+    if ((s = check_rows(q, rows, q_heads, d, false, false)) != KVQ_OK) return s;
+    if ((s = check_rows(out, rows, q_heads, d, true, false)) != KVQ_OK) return s;
+    if (q->dtype != out->dtype || window < 0 || (window > 0 && causal == 0)) return KVQ_ERR_INVALID_ARG;
+    if (lse != nullptr && !ok_ints(lse)) return KVQ_ERR_INVALID_ARG;
+    if (!(scale <= 3.0e38f)) return KVQ_ERR_INVALID_ARG;  // infinite or NaN
+    if (rows == 0 || batch->n_seqs == 0) return KVQ_OK;
+    intptr_t ql, qh, ol, oh;
+    extent(q, rows, q_heads, d, &ql, &qh);
+    extent(out, rows, q_heads, d, &ol, &oh);
+    if (ql < oh && ol < qh) return KVQ_ERR_INVALID_ARG;
+    const size_t need = kvq_pages_attention_workspace_bytes(cfg, pages, batch, rows, q_heads);
+    if (!ok_ptr(ws) || ws_bytes < need) return KVQ_ERR_WORKSPACE;
+    AttnLaunch L;
+    L.a.b = batch_of(batch);
+    L.a.p = pool_of(pages);
+    L.a.q = q->data;
+    L.a.out = out->data;
+    L.a.lse = lse;
+    L.a.q_row = rows > 1 ? q->row_stride : 0;
+    L.a.q_head = q_heads > 1 ? q->head_stride : 0;
+    L.a.o_row = rows > 1 ? out->row_stride : 0;
+    L.a.o_head = q_heads > 1 ? out->head_stride : 0;
+    L.a.signs = cfg->signs;
+    L.a.rows = (int)rows;
+    L.a.Hq = q_heads;
+    L.a.G = q_heads / pages->kv_heads;
+    L.a.causal = causal != 0;
+    L.a.window = window;
+    L.a.scale = scale > 0.0f ? scale : rsqd_of(d);
+    L.a.rsqd = rsqd_of(d);
+    L.st = static_cast<cudaStream_t>(stream);
+    return dispatch(d, q->dtype, cfg->flags == KVQ_HADAMARD, L);
+}
+
+kvq_status kvq_pages_read_errors(uint32_t* host_out, int32_t clear) {
+    if (host_out == nullptr) return KVQ_ERR_INVALID_ARG;
+    if (cudaMemcpyFromSymbol(host_out, g_error_word, sizeof(uint32_t)) != cudaSuccess) return KVQ_ERR_CUDA;
+    if (clear) {
+        const uint32_t zero = 0;
+        if (cudaMemcpyToSymbol(g_error_word, &zero, sizeof(uint32_t)) != cudaSuccess) return KVQ_ERR_CUDA;
+    }
+    return KVQ_OK;
+}
+
+}  // extern "C"

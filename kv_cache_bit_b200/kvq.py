@@ -24,7 +24,8 @@ BLOCK_TOKENS = 128
 EXPORTS = ["kvq_row_bytes", "kvq_tok_params", "kvq_off_words", "kvq_make_signs", "kvq_quantize_block", "kvq_append_token",
            "kvq_decode_workspace_bytes", "kvq_decode_attention", "kvq_decode_attention_noalloc", "kvq_dequantize",
            "kvq_select_signs_workspace_bytes", "kvq_select_signs", "kvq_read_device_errors",
-           "kvq_status_string"]
+           "kvq_pages_write", "kvq_pages_read", "kvq_pages_attention_workspace_bytes", "kvq_pages_attention",
+           "kvq_pages_read_errors", "kvq_status_string"]
 
 
 class kvq_config(ctypes.Structure):
@@ -37,6 +38,22 @@ class kvq_cache(ctypes.Structure):
                 ("capacity", ctypes.c_int32), ("len", ctypes.c_int64),
                 ("codes", ctypes.c_void_p * 2), ("tok", ctypes.c_void_p * 2), ("chan", ctypes.c_void_p * 2),
                 ("off", ctypes.c_void_p * 2), ("resid", ctypes.c_void_p * 2)]
+
+
+class kvq_pages(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("codes", ctypes.c_void_p * 2), ("tok", ctypes.c_void_p * 2)]
+
+
+class kvq_batch(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("table_stride", ctypes.c_int32),
+                ("max_rows", ctypes.c_int32), ("start", ctypes.c_void_p), ("len", ctypes.c_void_p),
+                ("table", ctypes.c_void_p)]
+
+
+class kvq_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 def _load():
@@ -75,6 +92,18 @@ def _load():
                                    ctypes.c_size_t, P]
     L.kvq_read_device_errors.restype = ctypes.c_int
     L.kvq_read_device_errors.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int32]
+    C, G, B, R = (ctypes.POINTER(t) for t in (kvq_config, kvq_pages, kvq_batch, kvq_rows))
+    L.kvq_pages_write.restype = ctypes.c_int
+    L.kvq_pages_write.argtypes = [C, G, B, R, R, ctypes.c_int64, P]
+    L.kvq_pages_read.restype = ctypes.c_int
+    L.kvq_pages_read.argtypes = [C, G, B, R, R, ctypes.c_int64, P]
+    L.kvq_pages_attention_workspace_bytes.restype = ctypes.c_size_t
+    L.kvq_pages_attention_workspace_bytes.argtypes = [C, G, B, ctypes.c_int64, ctypes.c_int32]
+    L.kvq_pages_attention.restype = ctypes.c_int
+    L.kvq_pages_attention.argtypes = [C, G, B, R, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_int32,
+                                      ctypes.c_int32, R, P, P, ctypes.c_size_t, P]
+    L.kvq_pages_read_errors.restype = ctypes.c_int
+    L.kvq_pages_read_errors.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int32]
     L.kvq_status_string.restype = ctypes.c_char_p
     L.kvq_status_string.argtypes = [ctypes.c_int]
     return L
@@ -189,6 +218,107 @@ def kvq_read_device_errors(clear: bool = True) -> int:
     return v.value
 
 
+# ------------------------------------------------------------------ paged cache
+
+KVQ_F16, KVQ_BF16, KVQ_F32 = 0, 1, 2
+PAGE_TOKENS = (16, 32, 64, 128)
+_DTYPES = {}
+
+
+def _paged(call: str, cfg: "Config", pages: "PagedCache", batch: "Batch", *tensors) -> int:
+    """Number of rows of the [rows, heads, head_dim] tensors, after the checks
+    that only their Python side can make (the library sees bare pointers)."""
+    rows = None
+    device = pages.device
+    if batch.device != device or (cfg.signs_dev is not None and cfg.signs_dev.device != device):
+        raise KvqError(KVQ_ERR_INVALID_ARG, call + ": configuration, cache and batch on one device")
+    for x, heads in tensors:
+        if x is None:
+            continue
+        if x.device != device or x.dim() != 3 or x.shape[2] != cfg.head_dim or x.stride(2) != 1:
+            raise KvqError(KVQ_ERR_INVALID_ARG, call + ": tensors are [rows, heads, head_dim] on the cache's device")
+        if (heads and x.shape[1] != heads) or rows not in (None, x.shape[0]):
+            raise KvqError(KVQ_ERR_INVALID_ARG, call + ": heads or rows of the tensors differ")
+        rows = x.shape[0]
+    return rows
+
+
+def _rows(x, call: str):
+    """kvq_rows of a [rows, heads, head_dim] tensor (None: a null pointer)."""
+    if x is None:
+        return None
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float16: KVQ_F16, torch.bfloat16: KVQ_BF16, torch.float32: KVQ_F32})
+    kind = _DTYPES.get(x.dtype)
+    if kind is None:
+        raise KvqError(KVQ_ERR_UNSUPPORTED, call)
+    # (a tensor without rows has no address; nothing is read through this one)
+    return kvq_rows(x.data_ptr() or 16, x.stride(0), x.stride(1), kind, 0)
+
+
+def _on(pages: "PagedCache", stream, call: str, fn, *args):
+    """fn(*args, stream) with the cache's device current; stream None: the
+    current stream of that device."""
+    import torch
+    index = pages.device.index
+    if stream is None:
+        stream = torch.cuda.current_stream(index).cuda_stream
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        return _check(fn(*args, stream), call)
+    with torch.cuda.device(index):
+        return _check(fn(*args, stream), call)
+
+
+def kvq_pages_write(cfg: "Config", pages: "PagedCache", batch: "Batch", k, v, stream=None):
+    """Quantize rows k, v [rows, kv_heads, head_dim] (fp16 or bf16, any row and
+    head strides of whole 16 bytes) into their slots; see include/kvq.h."""
+    name = "kvq_pages_write"
+    rows = _paged(name, cfg, pages, batch, (k, pages.c.kv_heads), (v, pages.c.kv_heads))
+    _on(pages, stream, name, lib.kvq_pages_write, cfg.c, pages.c, batch.c, _rows(k, name), _rows(v, name), rows)
+
+
+def kvq_pages_read(cfg: "Config", pages: "PagedCache", batch: "Batch", k_out, v_out, stream=None):
+    """Rebuild the batch's rows into k_out and v_out [rows, kv_heads, head_dim]
+    (fp16, bf16 or fp32; one of them may be None)."""
+    name = "kvq_pages_read"
+    rows = _paged(name, cfg, pages, batch, (k_out, pages.c.kv_heads), (v_out, pages.c.kv_heads))
+    _on(pages, stream, name, lib.kvq_pages_read, cfg.c, pages.c, batch.c, _rows(k_out, name), _rows(v_out, name),
+        rows or 0)
+
+
+def kvq_pages_attention_workspace_bytes(cfg: "Config", pages: "PagedCache", batch: "Batch", rows: int,
+                                        q_heads: int) -> int:
+    import torch
+    with torch.cuda.device(pages.device):
+        return lib.kvq_pages_attention_workspace_bytes(cfg.c, pages.c, batch.c, rows, q_heads)
+
+
+def kvq_pages_attention(cfg: "Config", pages: "PagedCache", batch: "Batch", q, out, lse=None, scale: float = 0.0,
+                        causal: bool = True, window: int = 0, ws=None, stream=None):
+    """Attention of queries q [rows, q_heads, head_dim] over their sequences
+    into out (q's type and shape) and, if given, lse fp32 [rows, q_heads].
+    ws: uint8 tensor of kvq_pages_attention_workspace_bytes()."""
+    name = "kvq_pages_attention"
+    rows = _paged(name, cfg, pages, batch, (q, 0), (out, 0))
+    heads = q.shape[1]
+    if out.shape[1] != heads or ws is None or ws.device != pages.device or not ws.is_contiguous():
+        raise KvqError(KVQ_ERR_INVALID_ARG, name + ": out of q's shape, a contiguous workspace on the cache's device")
+    if lse is not None and (lse.device != pages.device or tuple(lse.shape) != (rows, heads) or
+                            str(lse.dtype) != "torch.float32" or not lse.is_contiguous()):
+        raise KvqError(KVQ_ERR_INVALID_ARG, name + ": lse is a contiguous float32 [rows, q_heads]")
+    _on(pages, stream, name, lib.kvq_pages_attention, cfg.c, pages.c, batch.c, _rows(q, name), heads, rows, scale,
+        1 if causal else 0, window, _rows(out, name), _ptr(lse) or None, _ptr(ws), ws.numel() * ws.element_size())
+
+
+def kvq_pages_read_errors(clear: bool = True) -> int:
+    v = ctypes.c_uint32(0)
+    _check(lib.kvq_pages_read_errors(ctypes.byref(v), 1 if clear else 0), "kvq_pages_read_errors")
+    return v.value
+
+
 # ------------------------------------------------------------------ plumbing
 
 class Config:
@@ -278,3 +408,82 @@ class KVCache:
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for group in (self.codes, self.tok, self.chan, self.off, self.resid)
                    for t in group if t is not None)
+
+
+@dataclass
+class PagedCache:
+    """Caller-side memory of a kvq_pages pool (torch tensors on the GPU):
+    codes[2] uint8 [n_pages, kv_heads, page_tokens, head_dim / 2] and tok[2]
+    float16 [n_pages, kv_heads, page_tokens], K then V."""
+    c: kvq_pages
+    codes: list
+    tok: list
+
+    @classmethod
+    def allocate(cls, cfg: Config, n_pages: int, kv_heads: int, page_tokens: int, device="cuda") -> "PagedCache":
+        import torch
+        if page_tokens not in PAGE_TOKENS or cfg.bits != 4 or kvq_row_bytes(cfg.head_dim, 4) == 0:
+            raise KvqError(KVQ_ERR_UNSUPPORTED, "PagedCache.allocate")
+        shape = (n_pages, kv_heads, page_tokens)
+        codes = [torch.zeros((*shape, cfg.head_dim // 2), dtype=torch.uint8, device=device) for _ in range(2)]
+        tok = [torch.zeros(shape, dtype=torch.float16, device=device) for _ in range(2)]
+        return cls.wrap(cfg, codes, tok)
+
+    @classmethod
+    def wrap(cls, cfg: Config, codes, tok) -> "PagedCache":
+        """A pool over tensors that the caller has."""
+        import torch
+        n, h, t, half = codes[0].shape
+        for x, y in zip(codes, tok):
+            if (x.dtype, y.dtype) != (torch.uint8, torch.float16) or x.device != y.device or \
+                    x.device != codes[0].device or tuple(x.shape) != (n, h, t, half) or half * 2 != cfg.head_dim or \
+                    tuple(y.shape) != (n, h, t) or not x.is_contiguous() or not y.is_contiguous():
+                raise KvqError(KVQ_ERR_INVALID_ARG, "PagedCache.wrap")
+        c = kvq_pages(n, h, cfg.head_dim, t, (ctypes.c_void_p * 2)(*[_ptr(x) for x in codes]),
+                      (ctypes.c_void_p * 2)(*[_ptr(x) for x in tok]))
+        return cls(c, list(codes), list(tok))
+
+    @property
+    def device(self):
+        return self.codes[0].device
+
+    def snapshot(self) -> dict:
+        """A host copy of the pool (checkpoint); the batch's tables and
+        lengths are the caller's."""
+        return {"codes": [t.cpu() for t in self.codes], "tok": [t.cpu() for t in self.tok]}
+
+    def restore(self, snap: dict) -> None:
+        """Load a snapshot taken from a pool of the same shape (resume)."""
+        for name in ("codes", "tok"):
+            for dst, src in zip(getattr(self, name), snap[name]):
+                if dst.shape != src.shape:
+                    raise KvqError(KVQ_ERR_INVALID_ARG, "PagedCache.restore: snapshot of another pool shape")
+        for name in ("codes", "tok"):
+            for dst, src in zip(getattr(self, name), snap[name]):
+                dst.copy_(src)
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in (*self.codes, *self.tok))
+
+
+class Batch:
+    """kvq_batch over int32 device tensors: start [n_seqs + 1], length [n_seqs]
+    and the page table [n_seqs, pages] (rows may be further apart than their
+    pages, as in a slice of a larger table).  Their contents may change between
+    calls, and between a graph's replays."""
+
+    def __init__(self, start, length, table, max_rows: int = 0):
+        import torch
+        n = length.shape[0]
+        ok = all(x.dtype == torch.int32 and x.device == table.device for x in (start, length, table))
+        if not ok or start.dim() != 1 or length.dim() != 1 or table.dim() != 2 or start.shape[0] != n + 1 or \
+                table.shape[0] != n or (n and not (start.is_contiguous() and length.is_contiguous())) or \
+                (table.shape[1] > 1 and table.stride(1) != 1):
+            raise KvqError(KVQ_ERR_INVALID_ARG, "Batch")
+        self.start, self.length, self.table = start, length, table
+        stride = table.stride(0) if n > 1 else table.shape[1]
+        self.c = kvq_batch(n, table.shape[1], stride, max_rows, _ptr(start), _ptr(length), _ptr(table))
+
+    @property
+    def device(self):
+        return self.table.device
