@@ -17,7 +17,7 @@ NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 # translation unit -> the headers of csrc/ that only it includes
 UNITS = {"kvq_api.cu": ("kvq_decode_mma.cuh", "kvq_decode_simple.cuh", "kvq_quant.cuh", "kvq_quant_rows.cuh"),
-         "kvq_pages.cu": ("kvq_pages.cuh", "kvq_pages_attn.cuh")}
+         "kvq_pages.cu": ("kvq_pages.cuh", "kvq_pages_attn.cuh", "kvq_pages_step.cuh")}
 
 
 def sources():
@@ -27,7 +27,7 @@ def sources():
 TEST_LIB = os.path.join(OUT_DIR, "libkvq_waittest.so")
 
 _FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
-          "-I", os.path.join(ROOT, "include"), "--expt-relaxed-constexpr"]
+          "-I", os.path.join(ROOT, "include"), "--expt-relaxed-constexpr", "--split-compile=0"]
 
 
 def _deps(unit):

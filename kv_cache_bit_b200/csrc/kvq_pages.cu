@@ -12,6 +12,7 @@
 #include "kvq.h"
 #include "kvq_pages.cuh"
 #include "kvq_pages_attn.cuh"
+#include "kvq_pages_step.cuh"
 
 namespace kvq {
 namespace {
@@ -130,15 +131,89 @@ struct ReadLaunch {
     }
 };
 
-struct AttnLaunch {
-    AttnArgs a;
-    cudaStream_t st;
-    template <int D, typename T, bool HAD>
-    kvq_status run() {
-        pages_attn_simple_kernel<D, T, HAD><<<dim3(a.rows, a.Hq), 128, 0, st>>>(a);
-        return launch_status();
+// Launch as a programmatic dependent of the kernel ahead of it in the stream:
+// the kernels wait for that one (grid_dep_wait) before they read anything.
+template <typename A>
+kvq_status launch(void (*kernel)(A), const A& args, dim3 grid, int threads, int smem, cudaStream_t st) {
+    cudaLaunchConfig_t c = {};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = at;
+    c.numAttrs = 1;
+    if (cudaLaunchKernelEx(&c, kernel, args) != cudaSuccess) {
+        cudaGetLastError();
+        return KVQ_ERR_CUDA;
     }
+    return launch_status();
+}
+
+// Once per process and kernel would do; the attribute is per device, and the
+// call costs well under a microsecond.
+bool allow_smem(const void* kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess &&
+           cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                cudaSharedmemCarveoutMaxShared) == cudaSuccess;
+}
+
+// SMs of the current device.
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        return 148;
+    }
+    return n;
+}
+
+// Generation-step kernel: CTAs of a single wave, and query rows an item.
+template <int NQ>
+struct StepShape {
+    static constexpr int kWarps = NQ == 16 ? 4 : 8, kPerSm = NQ == 16 ? 3 : 2;
 };
+
+struct AttnWorkspace {
+    size_t meta, ml, part, bytes;
+};
+AttnWorkspace attn_workspace(int sms, int d) {
+    const size_t small = size_t(sms) * StepShape<8>::kPerSm, large = size_t(sms) * StepShape<16>::kPerSm;
+    const size_t ctas = large > small ? large : small;
+    const size_t queries = small * 8 > large * 16 ? small * 8 : large * 16;
+    AttnWorkspace w;
+    w.meta = 0;
+    w.ml = ctas * 16;
+    w.part = w.ml + 2 * queries * 8;
+    w.bytes = w.part + 2 * queries * d * 4;
+    return w;
+}
+
+template <int D, int NQ, bool HAD>
+kvq_status launch_step(StepArgs g, int sms, cudaStream_t st) {
+    using Sh = StepShape<NQ>;
+    constexpr int smem = (int)sizeof(StepSmem<D, NQ, HAD, Sh::kWarps>);
+    static_assert(smem * Sh::kPerSm + Sh::kPerSm * 1024 <= 228 * 1024, "shared memory of the CTAs on one SM");
+    const auto kernel = pages_step_kernel<D, NQ, HAD, Sh::kWarps, Sh::kPerSm>;
+    if (!allow_smem(reinterpret_cast<const void*>(kernel), smem)) return KVQ_ERR_CUDA;
+    g.min_units = Sh::kWarps;
+    const int grid = sms * Sh::kPerSm;
+    kvq_status s = launch<StepArgs>(kernel, g, dim3(grid), Sh::kWarps * 32, smem, st);
+    if (s != KVQ_OK) return s;
+    return launch<AttnArgs>(pages_merge_kernel<D, NQ, HAD>, g.a, dim3(grid, NQ), 128, 0, st);
+}
+
+template <int D, bool HAD>
+kvq_status launch_attn(const StepArgs& g, long long queries, int sms, cudaStream_t st) {
+    if constexpr (HAD) {
+        if (queries <= 4) return launch_step<D, 4, HAD>(g, sms, st);
+    }
+    if (queries <= 8) return launch_step<D, 8, HAD>(g, sms, st);
+    return launch_step<D, 16, HAD>(g, sms, st);
+}
 
 kvq_status check_attention(const kvq_config* cfg, const kvq_pages* p, const kvq_batch* b, int64_t rows, int q_heads) {
     const kvq_status s = check_paged(cfg, p, b, rows);
@@ -221,7 +296,7 @@ kvq_status kvq_pages_read(const kvq_config* cfg, const kvq_pages* pages, const k
 size_t kvq_pages_attention_workspace_bytes(const kvq_config* cfg, const kvq_pages* pages, const kvq_batch* batch,
                                            int64_t rows, int32_t q_heads) {
     if (check_attention(cfg, pages, batch, rows, q_heads) != KVQ_OK) return 0;
-    return 16;
+    return attn_workspace(sm_count(), cfg->head_dim).bytes;
 }
 
 kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, const kvq_batch* batch,
@@ -244,26 +319,39 @@ kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, co
     if (ql < oh && ol < qh) return KVQ_ERR_INVALID_ARG;
     const size_t need = kvq_pages_attention_workspace_bytes(cfg, pages, batch, rows, q_heads);
     if (!ok_ptr(ws) || ws_bytes < need) return KVQ_ERR_WORKSPACE;
-    AttnLaunch L;
-    L.a.b = batch_of(batch);
-    L.a.p = pool_of(pages);
-    L.a.q = q->data;
-    L.a.out = out->data;
-    L.a.lse = lse;
-    L.a.q_row = rows > 1 ? q->row_stride : 0;
-    L.a.q_head = q_heads > 1 ? q->head_stride : 0;
-    L.a.o_row = rows > 1 ? out->row_stride : 0;
-    L.a.o_head = q_heads > 1 ? out->head_stride : 0;
-    L.a.signs = cfg->signs;
-    L.a.rows = (int)rows;
-    L.a.Hq = q_heads;
-    L.a.G = q_heads / pages->kv_heads;
-    L.a.causal = causal != 0;
-    L.a.window = window;
-    L.a.scale = scale > 0.0f ? scale : rsqd_of(d);
-    L.a.rsqd = rsqd_of(d);
-    L.st = static_cast<cudaStream_t>(stream);
-    return dispatch(d, q->dtype, cfg->flags == KVQ_HADAMARD, L);
+    const int sms = sm_count();
+    const AttnWorkspace w = attn_workspace(sms, d);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    StepArgs g;
+    AttnArgs& a = g.a;
+    a.b = batch_of(batch);
+    a.p = pool_of(pages);
+    a.q = q->data;
+    a.out = out->data;
+    a.lse = lse;
+    a.q_row = rows > 1 ? q->row_stride : 0;
+    a.q_head = q_heads > 1 ? q->head_stride : 0;
+    a.o_row = rows > 1 ? out->row_stride : 0;
+    a.o_head = q_heads > 1 ? out->head_stride : 0;
+    a.signs = cfg->signs;
+    a.rows = (int)rows;
+    a.Hq = q_heads;
+    a.G = q_heads / pages->kv_heads;
+    a.bf16 = q->dtype == KVQ_BF16;
+    a.causal = causal != 0;
+    a.window = window;
+    a.scale2 = (scale > 0.0f ? scale : rsqd_of(d)) * 1.4426950408889634f;
+    a.rsqd = rsqd_of(d);
+    a.meta = reinterpret_cast<int4*>(base + w.meta);
+    a.ml = reinterpret_cast<float*>(base + w.ml);
+    a.part = reinterpret_cast<float*>(base + w.part);
+    g.many = 0;
+    g.min_units = 0;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const long long queries = (long long)a.G * (batch->max_rows > 0 ? batch->max_rows : 1);
+    const bool had = cfg->flags == KVQ_HADAMARD;
+    if (d == 64) return had ? launch_attn<64, true>(g, queries, sms, st) : launch_attn<64, false>(g, queries, sms, st);
+    return had ? launch_attn<128, true>(g, queries, sms, st) : launch_attn<128, false>(g, queries, sms, st);
 }
 
 kvq_status kvq_pages_read_errors(uint32_t* host_out, int32_t clear) {

@@ -1,9 +1,25 @@
-// kvq_pages_attn.cuh -- attention over the paged 4-bit cache.
+// kvq_pages_attn.cuh -- attention over the paged 4-bit cache: what the kernels
+// share (arguments, ranges of rows, the softmax's scaling, the last steps of a
+// row), and the merge of partial states.
+//
+// The softmax with the value scale inside.  With x_t the score of token t in
+// the log2 domain and sigma_t its value scale, the kernels form
+//   y_t = x_t + log2 sigma_t,   w_t = 2^(y_t - M + kBias),   M >= max y_t
+//   o = sum_t w_t q^V_t,        l = sum_t w_t / sigma_t
+// so that o / l is the softmax average and M + log2 l - kBias its logarithm
+// (base 2).  w is the only value that is rounded to fp16, at most 2^kBias and
+// normal down to 2^-29 of the largest, whatever the scales are; one addition
+// replaces the product with sigma.  A scale of 0 (a zero vector) counts as
+// 2^-24 in y and 1 / sigma: its codes are all 0.
 #pragma once
 
 #include "kvq_pages.cuh"
 
 namespace kvq {
+
+constexpr float kBias = 15.0f;
+constexpr float kLowest = -3.0e38f;  // M before any token: finite, so that M - M is 0
+constexpr float kLn2 = 0.693147180559945f;
 
 struct AttnArgs {
     Batch b;
@@ -13,89 +29,136 @@ struct AttnArgs {
     float* lse;
     long long q_row, q_head, o_row, o_head;  // strides, elements
     const int8_t* signs;
-    int rows, Hq, G;
+    int rows, Hq, G, bf16;
     int causal, window;
-    float scale, rsqd;
+    float scale2, rsqd;  // scale * log2 e; 1 / sqrt(d)
+    float* ml;           // partial states: M, l [slot][query][2]
+    float* part;         // and o [slot][query][D]
+    int4* meta;          // [CTA]: sequence, head, first query, merged slots (0: nothing to merge)
 };
 
-// The plainest form: one CTA per (row, query head), one token a thread for
-// the scores, one channel a thread for the values, online softmax.
-template <int D, typename T, bool HAD>
-__global__ void __launch_bounds__(128) pages_attn_simple_kernel(AttnArgs a) {
-    __shared__ float sq[D], sp[128], red[4];
-    __shared__ long long sslot[128];
-    const int row = blockIdx.x, j = blockIdx.y, g = j / a.G, tid = threadIdx.x;
-    const int s = owner_of(a.b.start, a.b.n_seqs, row);
-    if (s < 0) return;
-    const int len = max(a.b.len[s], 0), pos = a.b.len[s] - a.b.start[s + 1] + row;
-    int t1 = a.causal ? min(pos + 1, len) : len;
-    const int t0 = a.causal && a.window > 0 ? max(pos - a.window + 1, 0) : 0;
-    if (tid < D) {
-        const T x = static_cast<const T*>(a.q)[row * a.q_row + j * a.q_head + tid];
-        sq[tid] = (float)x * (HAD && a.signs ? (float)a.signs[tid] : 1.0f);
+// Tokens [t0, t1) that rows lo .. hi - 1 of sequence s see between them.
+struct Range {
+    int t0, t1;
+};
+__device__ __forceinline__ Range range_of(const AttnArgs& a, int len, int end, int lo, int hi) {
+    const long long n = max(len, 0), first = (long long)len - end + lo, last = (long long)len - end + hi;
+    long long t1 = a.causal ? min(last, n) : n;
+    const long long t0 = a.causal && a.window > 0 ? max(first - a.window + 1, 0ll) : 0;
+    const long long cap = (long long)a.b.max_pages << a.p.page_log2;
+    if (t1 > cap) {
+        if (t0 < t1) report_error(kErrRange);
+        t1 = cap;
     }
-    __syncthreads();
-    auto turn = [&]() {
-        for (int h = 1; h < D; h <<= 1) {
-            float v = 0;
-            if (tid < D) v = (tid & h) ? sq[tid ^ h] - sq[tid] : sq[tid] + sq[tid ^ h];
-            __syncthreads();
-            if (tid < D) sq[tid] = v;
-            __syncthreads();
+    if (t1 <= t0) return Range{0, 0};
+    return Range{(int)t0, (int)t1};
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float r;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float load16(const void* p, long long at, int bf16) {
+    const uint16_t u = static_cast<const uint16_t*>(p)[at];
+    return bf16 ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
+}
+
+// 2^k with k such that m 2^k is in [2^14, 2^15); for infinite or NaN m, NaN
+// (the row's result is then NaN whatever its codes are).
+__device__ __forceinline__ float query_scale(float m) {
+    if (!(m < INFINITY)) return NAN;
+    const int e = (int)(__float_as_uint(m) >> 23) - 127;
+    return __uint_as_float((uint32_t)(min(max(14 - e, -126), 127) + 127) << 23);
+}
+
+// Channel of place `pos` in the order in which the generation-step kernel keeps o:
+// pos = (nibble, word of a pair, row of the tensor core's tile).
+template <int D>
+__device__ __forceinline__ int channel_of(int pos) {
+    const int g = pos & 7, w = (pos >> 3) & 1, j = pos >> 4;
+    return D == 128 ? 16 * g + 8 * w + j : 8 * g + 4 * w + j;
+}
+
+// A warp's last steps for one row: o / l, the rotation back, out and lse.
+// v[i] is o at place lane + 32 i.
+template <int D, bool HAD>
+__device__ __forceinline__ void finish_row(const AttnArgs& a, int row, int head, float (&v)[D / 32], float M, float l) {
+    const int lane = threadIdx.x & 31;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) v[i] *= inv;
+    if constexpr (HAD) {
+        lane_stages<1, D / 32>(v);
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const float sg = (lane & x) ? -1.0f : 1.0f;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) v[i] = __fmaf_rn(v[i], sg, __shfl_xor_sync(~0u, v[i], x));
         }
-        if (tid < D) sq[tid] *= a.rsqd;
-        __syncthreads();
-    };
-    if (HAD) turn();
-    float m = -INFINITY, l = 0, acc = 0;
-    for (int base = t0; base < t1; base += 128) {
-        const int tok = base + tid;
-        long long slot = -1;
-        float x = -INFINITY;
-        if (tok < t1) slot = slot_of(a.b, a.p, s, tok);
-        if (slot >= 0) {
-            slot += (long long)g << a.p.page_log2;
-            const uint8_t* c = a.p.codes[0] + slot * (D / 2);
-            float d = 0;
-            for (int k = 0; k < D / 2; ++k)
-                d += sq[2 * k] * (float)((c[k] & 15) - 8) + sq[2 * k + 1] * (float)((c[k] >> 4) - 8);
-            x = d * __half2float(a.p.tok[0][slot]) * a.scale;
-        }
-        sslot[tid] = slot;
-        float mm = x;
-        for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
-        if ((tid & 31) == 0) red[tid >> 5] = mm;
-        __syncthreads();
-        mm = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-        const float m2 = fmaxf(m, mm);
-        const float keep = m2 == -INFINITY ? 1.0f : expf(m - m2);
-        const float p = slot < 0 ? 0.0f : expf(x - m2);
-        sp[tid] = slot < 0 ? 0.0f : p * __half2float(a.p.tok[1][slot]);
-        float ps = p;
-        for (int o = 16; o; o >>= 1) ps += __shfl_xor_sync(~0u, ps, o);
-        __syncthreads();
-        if ((tid & 31) == 0) red[tid >> 5] = ps;
-        __syncthreads();
-        l = l * keep + red[0] + red[1] + red[2] + red[3];
-        m = m2;
-        acc *= keep;
-        if (tid < D)
-            for (int k = 0; k < min(128, t1 - base); ++k)
-                if (sslot[k] >= 0) {
-                    const int b = a.p.codes[1][sslot[k] * (D / 2) + (tid >> 1)];
-                    acc += sp[k] * (float)(((tid & 1 ? b >> 4 : b) & 15) - 8);
-                }
-        __syncthreads();
     }
-    if (tid < D) sq[tid] = l == 0.0f ? 0.0f : acc / l;
+    uint16_t* dst = static_cast<uint16_t*>(a.out) + row * a.o_row + head * a.o_head;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        const int c = channel_of<D>(lane + 32 * i);
+        float x = v[i];
+        if constexpr (HAD) x *= a.signs ? (float)a.signs[c] * a.rsqd : a.rsqd;
+        dst[c] = (uint16_t)(a.bf16 ? Elem<__nv_bfloat16>::pack(x, x) : Elem<__half>::pack(x, x));
+    }
+    if (lane == 0 && a.lse) a.lse[(long long)row * a.Hq + head] = (M - kBias + lg2(l)) * kLn2;
+}
+
+// Merges the partial states of an item that several CTAs worked on.  One CTA a
+// (main-kernel CTA, query): those of main-kernel CTAs that no split item
+// starts in return at once.  Slot 2b + 1 is the state of an item that CTA b
+// began and did not end, slot 2b of one that it did not begin.  The order of
+// the sums is fixed.
+template <int D, int NQ, bool HAD>
+__global__ void __launch_bounds__(128) pages_merge_kernel(AttnArgs a) {
+    __shared__ float s_o[4][D], s_l[4];
+    const int b = blockIdx.x, qi = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int4 meta = a.meta[b];
+    const int n = meta.w;
+    if (n == 0) return;
+    const int s = meta.x, h = meta.y, i = meta.z + qi;
+    const int end = a.b.start[s + 1], lo = max(a.b.start[s], 0);
+    const int row = lo + i / a.G, head = h * a.G + i % a.G;
+    if (row >= min(end, a.rows)) return;
+    const auto slot = [&](int k) { return ((long long)(k == 0 ? 2 * b + 1 : 2 * (b + k)) * NQ + qi); };
+    float M = kLowest;
+    for (int k = lane; k < n; k += 32) M = fmaxf(M, a.ml[2 * slot(k)]);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, x));
+    float v[D / 32] = {}, l = 0.0f;
+#pragma unroll 4
+    for (int k = warp; k < n; k += 4) {
+        const long long at = slot(k);
+        const float2 ml = reinterpret_cast<const float2*>(a.ml)[at];
+        const float f = ex2(ml.x - M);
+        l = __fmaf_rn(ml.y, f, l);
+#pragma unroll
+        for (int i2 = 0; i2 < D / 32; ++i2) v[i2] = __fmaf_rn(a.part[at * D + lane + 32 * i2], f, v[i2]);
+    }
+#pragma unroll
+    for (int i2 = 0; i2 < D / 32; ++i2) s_o[warp][lane + 32 * i2] = v[i2];
+    if (lane == 0) s_l[warp] = l;
     __syncthreads();
-    if (HAD) turn();
-    if (tid < D) {
-        float o = sq[tid] * (HAD && a.signs ? (float)a.signs[tid] : 1.0f);
-        const uint32_t u = Elem<T>::pack(o, o);
-        static_cast<T*>(a.out)[row * a.o_row + j * a.o_head + tid] = *reinterpret_cast<const T*>(&u);
+    if (warp != 0) return;
+#pragma unroll
+    for (int i2 = 0; i2 < D / 32; ++i2) {
+        v[i2] = s_o[0][lane + 32 * i2];
+        for (int w = 1; w < 4; ++w) v[i2] += s_o[w][lane + 32 * i2];
     }
-    if (tid == 0 && a.lse) a.lse[(long long)row * a.Hq + j] = m + logf(l);
+    l = ((s_l[0] + s_l[1]) + s_l[2]) + s_l[3];
+    finish_row<D, HAD>(a, row, head, v, M, l);
 }
 
 }  // namespace kvq

@@ -1,0 +1,631 @@
+// kvq_pages_step.cuh -- attention of few query rows a kv head (generation
+// steps, a few drafted tokens): the paged cache is read once, straight into
+// the registers of mma.m16n8k16.
+//
+// Work: an item is (sequence, kv head, up to NQ of the head's query rows); its
+// cost is the number of 32-token units that the sequence's rows see.  All
+// items laid end to end are cut into equal ranges, one a CTA of a single-wave
+// grid, whatever the lengths are: one long sequence is spread over the whole
+// GPU, many short ones share CTAs.  Warp w of a CTA takes units w, w + NW, ..
+// of a segment (an item's part of the range) through a ring of its own in
+// shared memory, filled by bulk copies that run ahead over segment borders.  The warps'
+// states are added up in shared memory; a segment that is a whole item is
+// finished there, others leave a partial state for pages_merge_kernel.
+//
+// Per 16 tokens, channels and tokens permuted so that unpacking is cheap:
+//   scores  A = K codes, exact in fp16: a nibble pair ORed into the mantissas of
+//           1024 and less 1032 (or, from the upper nibbles, times 1 / 16 less
+//           72).  Taking the bits as subnormals e 2^-24 would save that
+//           addition, but the tensor core aligns products by their exponent
+//           fields and drops what falls below: errors of 7e-4 of the values.
+//           B = the query, times a power of two for its row so that its
+//           largest element is near 2^15.  A rotated query is split into fp16
+//           high and low parts in neighbouring columns (22 bits of it are
+//           kept); an input that is not rotated fits fp16 exactly.
+//   values  A = V codes transposed (byte permutes pair two tokens' words),
+//           B = w from the score fragments by movmatrix.
+// Instructions a 16-token tile (4 rotated queries, D = 128): about 210 against
+// 332 of the block cache's kernel, whose channel scales need arithmetic per
+// code; 88 of them on the ALU pipe (2 cycles each): 44 SM cycles, of about 90
+// that HBM needs for the tile's 2112 bytes.
+#pragma once
+
+#include "kvq_pages_attn.cuh"
+
+namespace kvq {
+
+constexpr int kUnit = 32;  // tokens of a ring slot: one a lane
+constexpr int kRingPages = 2;
+constexpr uint32_t kWaitUnit = 1u << 22;
+
+template <int D>
+constexpr int slot_bytes() { return kUnit * (D + 4); }  // K codes, V codes, K scales, V scales
+
+struct StepArgs {
+    AttnArgs a;
+    int many;       // sequences of more query rows a kv head than this are not this kernel's (0: all are)
+    int min_units;  // least units a CTA is given
+};
+
+// A sequence's share of the work.
+struct Item {
+    int s, lo, nq, chunks, units, u0, t0, t1;
+    long long cost;
+};
+
+template <int NQ>
+__device__ __forceinline__ Item item_of(const StepArgs& g, int s, int H) {
+    Item it;
+    const int end = g.a.b.start[s + 1];
+    const int hi = min(end, g.a.rows);
+    it.s = s;
+    it.lo = max(g.a.b.start[s], 0);
+    const int rows = hi - it.lo;
+    it.cost = 0;
+    it.nq = 0;
+    if (rows <= 0) return it;
+    it.nq = rows * g.a.G;
+    if (g.many > 0 && it.nq > g.many) {
+        it.nq = 0;
+        return it;
+    }
+    const Range r = range_of(g.a, g.a.b.len[s], end, it.lo, hi);
+    it.t0 = r.t0;
+    it.t1 = r.t1;
+    it.u0 = r.t0 / kUnit;
+    it.units = max((r.t1 + kUnit - 1) / kUnit - it.u0, 1);  // rows that see nothing need an owner too
+    it.chunks = (it.nq + NQ - 1) / NQ;
+    it.cost = (long long)H * it.chunks * it.units;
+    return it;
+}
+
+// A walk over the segments of [x, end) of the work.
+template <int NQ>
+struct Walk {
+    long long x, end;  // the current segment begins at x
+    Item it;
+    int h, c, u, n;    // head, chunk, first unit and units of the segment
+    bool whole_begin, whole_end;
+
+    // x, inside sequence it.s at offset `off` from its first unit.
+    __device__ __forceinline__ void place(long long off) {
+        u = (int)(off % it.units);
+        const long long k = off / it.units;
+        c = (int)(k % it.chunks);
+        h = (int)(k / it.chunks);
+        n = (int)min((long long)(it.units - u), end - x);
+    }
+    __device__ __forceinline__ void next(const StepArgs& g, int H) {
+        x += n;
+        if (x >= end) {
+            n = 0;
+            return;
+        }
+        u = 0;
+        if (++c == it.chunks) {
+            c = 0;
+            if (++h == H) {
+                h = 0;
+                do {
+                    if (it.s + 1 >= g.a.b.n_seqs) {
+                        n = 0, end = x;
+                        return;
+                    }
+                    it = item_of<NQ>(g, it.s + 1, H);
+                } while (it.cost == 0);
+            }
+        }
+        n = (int)min((long long)it.units, end - x);
+    }
+};
+
+// NW warps; NQ query rows an item.
+template <int D, int NQ, bool HAD, int NW>
+struct StepSmem {
+    static constexpr int kQT = HAD ? NQ / 4 : NQ / 8;   // score tiles of 8 columns
+    static constexpr int kNV = HAD ? kQT : 2 * kQT;     // query rows a lane holds scores of
+    static constexpr int kNP = (kNV + 1) / 2;           // value tiles of 8 columns
+    static constexpr int kStride = D + 4;               // floats of a query's o: lanes of one store in 32 banks
+    static constexpr int kMQ = NQ < 8 ? NQ : 8;         // query rows merged at a time
+    alignas(128) uint8_t ring[NW][kRingPages][slot_bytes<D>()];
+    alignas(16) float o[NW][kMQ][kStride];
+    alignas(16) uint32_t q[kQT][D / 32][32][4];
+    alignas(16) float4 par[NW][kUnit];  // a token's K scale, log2 and inverse of its V scale
+    float cq[NQ];
+    int t0[NQ], t1[NQ];
+    float m[NW][NQ], l[NW][NQ];
+    uint64_t bar[NW][kRingPages];
+    int mask[NW][kRingPages];  // which 16-token halves of a slot hold tokens
+    Walk<NQ> own[NW], ahead[NW];  // each warp's place in the work: what it computes, what it fetches
+    long long pref[NW * 32 + 1];
+    long long sums[NW];
+};
+
+__device__ __forceinline__ float max_or_nan(float x, float y) { return x != x || y <= x ? x : y; }
+
+__device__ __forceinline__ uint32_t fma2(uint32_t x, uint32_t y, uint32_t z) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
+    return r;
+}
+// Codes q of the nibbles 0 and 4, or 1 and 5, of a word, as two fp16 (exact).
+__device__ __forceinline__ uint32_t codes_low(uint32_t w) {  // (1024 + e) - 1032
+    return fma2((w & 0x000F000Fu) | 0x64006400u, 0x3C003C00u, 0xE408E408u);
+}
+__device__ __forceinline__ uint32_t codes_high(uint32_t w) {  // (1024 + 16 e) / 16 - 72
+    return fma2((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
+}
+
+__device__ __forceinline__ uint32_t perm(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+    return r;
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+// D += A B, m16n8k16
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&x)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(b0), "r"(b1));
+}
+
+// Query qi's index in the lanes' values: lane t of a quad, value v.
+template <bool HAD>
+__device__ __forceinline__ int query_of(int v, int t) {
+    return HAD ? 4 * v + t : 8 * (v >> 1) + 2 * t + (v & 1);
+}
+
+// Loads, rotates, scales and splits the queries of chunk c into the B
+// fragments.  One warp a query; a lane holds D / 32 neighbouring channels.
+template <int D, int NQ, bool HAD, int NW>
+__device__ __forceinline__ void load_queries(const StepArgs& g, StepSmem<D, NQ, HAD, NW>& sm, const Item& it, int h,
+                                             int c) {
+    constexpr int N = D / 32, C = D / 4;  // channels a lane; channels a fragment lane
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const AttnArgs& a = g.a;
+    const int len = a.b.len[it.s], end = a.b.start[it.s + 1];
+    for (int qi = warp; qi < NQ; qi += NW) {
+        const int i = c * NQ + qi;
+        const bool there = i < it.nq;
+        float v[N] = {};
+        if (there) {
+            const int row = it.lo + i / a.G, head = h * a.G + i % a.G;
+            const uint16_t* src = static_cast<const uint16_t*>(a.q) + row * a.q_row + head * a.q_head + lane * N;
+            uint32_t u[N / 2];
+            if constexpr (N == 4) {
+                const uint2 w = *reinterpret_cast<const uint2*>(src);
+                u[0] = w.x, u[1] = w.y;
+            } else {
+                u[0] = *reinterpret_cast<const uint32_t*>(src);
+            }
+#pragma unroll
+            for (int k = 0; k < N / 2; ++k) {
+                const float2 f = a.bf16 ? Elem<__nv_bfloat16>::wide(u[k]) : Elem<__half>::wide(u[k]);
+                v[2 * k] = f.x, v[2 * k + 1] = f.y;
+            }
+        }
+        if constexpr (HAD) {
+            if (a.signs) {
+#pragma unroll
+                for (int k = 0; k < N; ++k) v[k] *= (float)a.signs[lane * N + k];
+            }
+            lane_stages<1, N>(v);
+#pragma unroll
+            for (int x = 1; x < 32; x <<= 1) {
+                const float sg = (lane & x) ? -1.0f : 1.0f;
+#pragma unroll
+                for (int k = 0; k < N; ++k) v[k] = __fmaf_rn(v[k], sg, __shfl_xor_sync(~0u, v[k], x));
+            }
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] *= a.rsqd;
+        }
+        float m = 0.0f;
+#pragma unroll
+        for (int k = 0; k < N; ++k) m = max_or_nan(m, fabsf(v[k]));
+#pragma unroll
+        for (int x = 16; x; x >>= 1) m = max_or_nan(m, __shfl_xor_sync(~0u, m, x));
+        const float f = m > 0.0f || m != m ? query_scale(m) : 1.0f;
+        const int tile = HAD ? qi >> 2 : qi >> 3, col = HAD ? 2 * (qi & 3) : qi & 7;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int ch = lane * N + k, t = ch / C, i8 = (ch % C) >> 3, cc = ch & 7;
+            const float x = v[k] * f;
+            const int word = (cc & 1) * 2 + ((cc >> 1) & 1);
+            const __half hi = __float2half_rn(x);
+            reinterpret_cast<__half*>(&sm.q[tile][i8][col * 4 + t][word])[cc >> 2] = hi;
+            if constexpr (HAD)
+                reinterpret_cast<__half*>(&sm.q[tile][i8][(col + 1) * 4 + t][word])[cc >> 2] =
+                    __float2half_rn(x - __half2float(hi));
+        }
+        if (lane == 0) {
+            sm.cq[qi] = a.scale2 / f;
+            Range r{0, 0};
+            if (there) {
+                const int row = it.lo + i / a.G;
+                // (the error word was set for the sequence's whole range)
+                const long long n = max(len, 0), pos = (long long)len - end + row;
+                const long long hi = min(a.causal ? min(pos + 1, n) : n, (long long)it.t1);
+                const long long lo = a.causal && a.window > 0 ? max(pos - a.window + 1, 0ll) : 0;
+                if (lo < hi) r = Range{(int)lo, (int)hi};
+            }
+            sm.t0[qi] = r.t0;
+            sm.t1[qi] = r.t1;
+        }
+    }
+}
+
+template <int D, int NQ, bool HAD, int NW, int PER_SM>
+__global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g) {
+    using S = StepSmem<D, NQ, HAD, NW>;
+    constexpr int QT = S::kQT, NV = S::kNV, NP = S::kNP, NJ = D / 16;
+    extern __shared__ __align__(128) uint8_t raw[];
+    S& sm = *reinterpret_cast<S*>(raw);
+    const AttnArgs& a = g.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3, r8 = lane >> 2;
+    const int H = a.p.H;
+
+    if (lane == 0) {
+        for (int i = 0; i < kRingPages; ++i) mbar_init(&sm.bar[warp][i], 1);
+        fence_mbar_init();
+    }
+    grid_dep_wait();
+    grid_dep_launch();
+
+    // ---- this CTA's range: prefix sums of the sequences' costs
+    const int per = (a.b.n_seqs + NW * 32 - 1) / (NW * 32);
+    long long mine = 0;
+    for (int s = threadIdx.x * per; s < min((int)(threadIdx.x + 1) * per, a.b.n_seqs); ++s)
+        mine += item_of<NQ>(g, s, H).cost;
+    long long acc_sum = mine;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const long long o = __shfl_up_sync(~0u, acc_sum, x);
+        if (lane >= x) acc_sum += o;
+    }
+    if (lane == 31) sm.sums[warp] = acc_sum;
+    __syncthreads();
+    long long before = 0;
+    for (int w = 0; w < warp; ++w) before += sm.sums[w];
+    sm.pref[threadIdx.x + 1] = before + acc_sum;
+    if (threadIdx.x == 0) sm.pref[0] = 0;
+    __syncthreads();
+    const long long total = sm.pref[NW * 32];
+    const long long ctas = min((long long)gridDim.x, (total + g.min_units - 1) / g.min_units);
+    if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (blockIdx.x >= ctas) return;
+
+    Walk<NQ>& wk = sm.own[warp];
+    Walk<NQ>& pw = sm.ahead[warp];
+    if (lane == 0) {
+        Walk<NQ> w;
+        w.x = total / ctas * blockIdx.x + min((long long)blockIdx.x, total % ctas);
+        w.end = w.x + total / ctas + (blockIdx.x < total % ctas ? 1 : 0);
+        int lo = 0, hi = NW * 32;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (sm.pref[mid] <= w.x) lo = mid;
+            else hi = mid;
+        }
+        long long off = w.x - sm.pref[lo];
+        int s = lo * per;
+        w.it = item_of<NQ>(g, s, H);
+        while (off >= w.it.cost && s + 1 < a.b.n_seqs) {
+            off -= w.it.cost;
+            w.it = item_of<NQ>(g, ++s, H);
+        }
+        w.place(off);
+        wk = w;
+        pw = w;
+    }
+    __syncwarp();
+
+    // ---- the copies' side of the ring
+    int ahead = 0;  // slots filled or being filled
+    int pk = 0, pg0 = -1, pg1 = -1;  // the warp's next unit of the segment; pages of 32 of them, one a lane
+    const int plog = a.p.page_log2;
+    const bool halves = plog == 4;
+    const auto page_of = [&](int tok) {
+        if (tok >= pw.it.t1 || tok + (halves ? 16 : kUnit) <= pw.it.t0) return -1;
+        const int col = tok >> plog;  // below max_pages, as t1 is
+        const int page = a.b.table[(long long)pw.it.s * a.b.table_stride + col];
+        if (page >= 0 && page < a.p.n_pages) return page;
+        report_error(kErrRange);
+        return -1;
+    };
+    const auto produce = [&](int slot) {
+        int off = warp + NW * pk;
+        while (pw.n > 0 && off >= pw.n) {
+            __syncwarp();
+            if (lane == 0) pw.next(g, H);
+            __syncwarp();
+            pk = 0;
+            off = warp;
+        }
+        if (pw.n == 0) return;
+        if ((pk & 31) == 0) {
+            const int o = warp + NW * (pk + lane);
+            const int tok = (pw.it.u0 + pw.u + o) * kUnit;
+            pg0 = o < pw.n ? page_of(tok) : -1;
+            pg1 = halves && o < pw.n ? page_of(tok + 16) : -1;
+        }
+        const int tok = (pw.it.u0 + pw.u + off) * kUnit;
+        const int p0 = __shfl_sync(~0u, pg0, pk & 31), p1 = __shfl_sync(~0u, pg1, pk & 31);
+        ++pk;
+        ++ahead;
+        const int part = halves ? 16 : kUnit;
+        const int half = lane >> 2, kind = lane & 3;
+        const int page = half ? p1 : p0;
+        if (lane == 0) {
+            sm.mask[warp][slot] = halves ? (p0 >= 0 ? 1 : 0) | (p1 >= 0 ? 2 : 0) : (p0 >= 0 ? 3 : 0);
+            mbar_expect_tx(&sm.bar[warp][slot], ((p0 >= 0) + (p1 >= 0)) * part * (D + 4));
+        }
+        __syncwarp();
+        if (half < (halves ? 2 : 1) && page >= 0) {
+            const long long at = (((long long)page * H + pw.h) << plog) + (tok & ((1 << plog) - 1));
+            uint8_t* dst = sm.ring[warp][slot];
+            const int i = kind & 1;
+            if (kind < 2)
+                bulk_load(dst + i * kUnit * (D / 2) + half * 16 * (D / 2), a.p.codes[i] + at * (D / 2), part * (D / 2),
+                          &sm.bar[warp][slot]);
+            else
+                bulk_load(dst + kUnit * D + i * kUnit * 2 + half * 32, a.p.tok[i] + at, part * 2, &sm.bar[warp][slot]);
+        }
+    };
+    for (int i = 0; i < kRingPages; ++i) produce(i);
+
+    int slot = 0;
+    uint32_t phase = 0;
+    bool failed = false;
+
+    // ---- segments
+    while (wk.n > 0) {
+        const bool begins = wk.u == 0, ends = wk.u + wk.n == wk.it.units;
+        const int units = wk.n, unit0 = wk.it.u0 + wk.u, seen0 = wk.it.t0, seen1 = wk.it.t1;
+        load_queries<D, NQ, HAD, NW>(g, sm, wk.it, wk.h, wk.c);
+        __syncthreads();
+        float M[NV], l[NV], cq[NV];
+        float o[NP][NJ][4];
+        int lo_max = 0, hi_min = 0x7FFFFFFF;  // tokens that all of the chunk's rows see
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            M[v] = kLowest;
+            l[v] = 0.0f;
+            cq[v] = sm.cq[query_of<HAD>(v, t)];
+        }
+        for (int i = 0; i < min(NQ, wk.it.nq - wk.c * NQ); ++i) {
+            lo_max = max(lo_max, sm.t0[i]);
+            hi_min = min(hi_min, sm.t1[i]);
+        }
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[n][j][k] = 0.0f;
+        }
+        constexpr bool kHold = QT * (D / 32) <= 4;  // few enough to stay in registers
+        uint4 qf[kHold ? QT : 1][kHold ? D / 32 : 1];
+        if constexpr (kHold) {
+#pragma unroll
+            for (int n = 0; n < QT; ++n)
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) qf[n][i] = *reinterpret_cast<const uint4*>(sm.q[n][i][lane]);
+        }
+
+        for (int off = warp; off < units; off += NW) {
+            const int tok0 = (unit0 + off) * kUnit;
+            if (!failed) {
+                const bool in = mbar_wait(&sm.bar[warp][slot], phase, KVQ_WAIT_LIMIT(kWaitUnit));
+                if (__any_sync(~0u, !in)) {  // results are void from here on; nothing more is fetched
+                    failed = true;
+                    report_error(kErrBarrierTimeout);
+                    // copies in flight end before the CTA's memory is given back
+                    for (int i = 0, at = slot, ph = phase; i < ahead; ++i) {
+                        mbar_wait(&sm.bar[warp][at], ph, kWaitUnit);
+                        if (++at == kRingPages) at = 0, ph ^= 1;
+                    }
+                }
+            }
+            const uint8_t* ring = sm.ring[warp][slot];
+            {   // one token a lane: scales of K, log2 and inverse of V's
+                const __half* sc = reinterpret_cast<const __half*>(ring + kUnit * D);
+                const float sk = __half2float(sc[lane]), sv = fmaxf(__half2float(sc[kUnit + lane]), 0x1p-24f);
+                const bool there = (sm.mask[warp][slot] >> (lane >> 4) & 1) && tok0 + lane < seen1 && tok0 + lane >= seen0;
+                sm.par[warp][lane] = there ? make_float4(sk, lg2(sv), __frcp_rn(sv), 0.0f)
+                                           : make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
+            }
+            __syncwarp();
+            float y[2][NV][2];  // [tile][value][token r8 or r8 + 8]
+            float4 par[2][2];
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+                uint32_t kw[2][D / 32];
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+                    load_words(ring + (mt * 16 + hf * 8 + r8) * (D / 2) + t * (D / 8), kw[hf]);
+                float s[QT][4];
+#pragma unroll
+                for (int n = 0; n < QT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    uint32_t x[2][4];
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const uint32_t w = kw[hf][i], w8 = w >> 8;
+                        x[0][hf] = codes_low(w);
+                        x[1][hf] = codes_high(w);
+                        x[0][2 + hf] = codes_low(w8);
+                        x[1][2 + hf] = codes_high(w8);
+                    }
+#pragma unroll
+                    for (int n = 0; n < QT; ++n) {
+                        const uint4 f = kHold ? qf[n * kHold][i * kHold]
+                                              : *reinterpret_cast<const uint4*>(sm.q[n][i][lane]);
+                        mma(s[n], x[0], f.x, f.y);
+                        mma(s[n], x[1], f.z, f.w);
+                    }
+                }
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    par[mt][hf] = sm.par[warp][mt * 16 + hf * 8 + r8];
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) {
+                        const float score = HAD ? s[v][2 * hf] + s[v][2 * hf + 1] : s[v >> 1][2 * hf + (v & 1)];
+                        y[mt][v][hf] = __fmaf_rn(score, cq[v] * par[mt][hf].x, par[mt][hf].y);
+                    }
+                }
+            }
+            if (tok0 < lo_max || tok0 + kUnit > hi_min) {
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const int q0 = sm.t0[query_of<HAD>(v, t)], q1 = sm.t1[query_of<HAD>(v, t)];
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            const int tok = tok0 + mt * 16 + hf * 8 + r8;
+                            if (tok < q0 || tok >= q1) y[mt][v][hf] = -INFINITY;
+                        }
+                }
+            }
+            float top[NV];
+            bool more = false;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                top[v] = fmaxf(fmaxf(y[0][v][0], y[0][v][1]), fmaxf(y[1][v][0], y[1][v][1]));
+                more |= top[v] > M[v];
+            }
+            if (__any_sync(~0u, more)) {
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) top[v] = fmaxf(top[v], __shfl_xor_sync(~0u, top[v], x));
+                    const float m2 = fmaxf(M[v], top[v]), f = ex2(M[v] - m2);
+                    M[v] = m2;
+                    l[v] *= f;
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) {
+                        o[v >> 1][j][v & 1] *= f;
+                        o[v >> 1][j][2 + (v & 1)] *= f;
+                    }
+                }
+            }
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+                uint32_t bw[NP][2];
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int n = 0; n < NP; ++n) {
+                        float w[2] = {0.0f, 0.0f};
+#pragma unroll
+                        for (int k = 0; k < 2 && 2 * n + k < NV; ++k) {
+                            w[k] = ex2(y[mt][2 * n + k][hf] - M[2 * n + k] + kBias);
+                            l[2 * n + k] = __fmaf_rn(w[k], par[mt][hf].z, l[2 * n + k]);
+                        }
+                        bw[n][hf] = transposed(Elem<__half>::pack(w[0], w[1]));
+                    }
+                // tokens 2t, 2t + 1 and 2t + 8, 2t + 9; words of channels r8 (and, at D = 128, its neighbour's)
+                constexpr int NWD = D / 64;
+                uint32_t vw[2][2][NWD];
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        load_words(ring + kUnit * (D / 2) + (mt * 16 + hf * 8 + 2 * t + k) * (D / 2) + r8 * (D / 16),
+                                   vw[hf][k]);
+#pragma unroll
+                for (int j0 = 0; j0 < NJ; j0 += 4) {  // four tiles: nibbles 0 .. 3 or 4 .. 7 of the words
+                    uint32_t z[4][4];
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {  // row r8, or r8 + 8: the other word, or half of the word
+                            const int wd = D == 128 ? k : 0;
+                            const bool up = D == 128 ? j0 != 0 : k != 0;
+                            const uint32_t p = perm(vw[hf][0][wd], vw[hf][1][wd], up ? 0x7632u : 0x5410u), p8 = p >> 8;
+                            z[0][2 * hf + k] = codes_low(p);
+                            z[1][2 * hf + k] = codes_high(p);
+                            z[2][2 * hf + k] = codes_low(p8);
+                            z[3][2 * hf + k] = codes_high(p8);
+                        }
+#pragma unroll
+                    for (int n = 0; n < NP; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) mma(o[n][j0 + j], z[j], bw[n][0], bw[n][1]);
+                }
+            }
+            __syncwarp();  // the slot has been read
+            --ahead;
+            if (!failed) produce(slot);
+            if (++slot == kRingPages) slot = 0, phase ^= 1;
+        }
+
+        // ---- the warps' states into one
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) l[v] += __shfl_xor_sync(~0u, l[v], x);
+            if (r8 == 0) {
+                sm.m[warp][query_of<HAD>(v, t)] = M[v];
+                sm.l[warp][query_of<HAD>(v, t)] = l[v];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+#pragma unroll
+            for (int k = 0; k < 2 && 2 * n + k < NV; ++k) {
+                const int v = 2 * n + k, q = query_of<HAD>(v, t);
+                float top = sm.m[0][q];
+#pragma unroll
+                for (int w = 1; w < NW; ++w) top = fmaxf(top, sm.m[w][q]);
+                const float f = ex2(M[v] - top);
+                float* dst = sm.o[warp][q - 8 * n];
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf)
+                        dst[(2 * j + hf) * 8 + r8] = f * o[n][j][2 * hf + k];
+            }
+            __syncthreads();
+            for (int q = 8 * n + warp; q < min(8 * n + S::kMQ, NQ); q += NW) {
+                const int i = wk.c * NQ + q;
+                if (i >= wk.it.nq) break;
+                float top = kLowest, sum = 0.0f, v[D / 32] = {};
+#pragma unroll
+                for (int w = 0; w < NW; ++w) top = fmaxf(top, sm.m[w][q]);
+#pragma unroll
+                for (int w = 0; w < NW; ++w) {
+                    sum = __fmaf_rn(sm.l[w][q], ex2(sm.m[w][q] - top), sum);
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k) v[k] += sm.o[w][q - 8 * n][lane + 32 * k];
+                }
+                if (begins && ends) {
+                    finish_row<D, HAD>(a, wk.it.lo + i / a.G, wk.h * a.G + i % a.G, v, top, sum);
+                } else {
+                    const long long at = (2ll * blockIdx.x + (begins ? 1 : 0)) * NQ + q;
+                    if (lane == 0) reinterpret_cast<float2*>(a.ml)[at] = make_float2(top, sum);
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k) a.part[at * D + lane + 32 * k] = v[k];
+                }
+            }
+            __syncthreads();
+        }
+        if (begins && !ends && threadIdx.x == 0) {
+            // CTAs from this one to that of the item's last unit
+            const long long last = wk.x + wk.it.units - 1, big = total / ctas + 1, nbig = total % ctas;
+            const long long cta = last < big * nbig ? last / big : nbig + (last - big * nbig) / (big - 1);
+            a.meta[blockIdx.x] = make_int4(wk.it.s, wk.h, wk.c * NQ, (int)(cta - blockIdx.x) + 1);
+        }
+        __syncwarp();
+        if (lane == 0) wk.next(g, H);
+        __syncwarp();
+    }
+}
+
+}  // namespace kvq
