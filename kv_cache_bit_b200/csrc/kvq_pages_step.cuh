@@ -8,7 +8,7 @@
 // grid, whatever the lengths are: one long sequence is spread over the whole
 // GPU, many short ones share CTAs.  Warp w of a CTA takes units w, w + NW, ..
 // of a segment (an item's part of the range) through a ring of its own in
-// shared memory, filled by bulk copies that run ahead over segment borders.  The warps'
+// shared memory, filled by cp.async that runs ahead over segment borders.  The warps'
 // states are added up in shared memory; a segment that is a whole item is
 // finished there, others leave a partial state for pages_merge_kernel.
 //
@@ -36,7 +36,6 @@ namespace kvq {
 
 constexpr int kUnit = 32;  // tokens of a ring slot: one a lane
 constexpr int kRingPages = 2;
-constexpr uint32_t kWaitUnit = 1u << 22;
 
 template <int D>
 constexpr int slot_bytes() { return kUnit * (D + 4); }  // K codes, V codes, K scales, V scales
@@ -79,6 +78,11 @@ __device__ __forceinline__ Item item_of(const StepArgs& g, int s, int H) {
     return it;
 }
 
+// x / y of non-negative numbers; 64-bit division only where 32 do not hold x.
+__device__ __forceinline__ long long quotient(long long x, int y) {
+    return x >> 32 ? x / y : (long long)((uint32_t)x / (uint32_t)y);
+}
+
 // A walk over the segments of [x, end) of the work.
 template <int NQ>
 struct Walk {
@@ -89,10 +93,10 @@ struct Walk {
 
     // x, inside sequence it.s at offset `off` from its first unit.
     __device__ __forceinline__ void place(long long off) {
-        u = (int)(off % it.units);
-        const long long k = off / it.units;
-        c = (int)(k % it.chunks);
-        h = (int)(k / it.chunks);
+        const long long k = quotient(off, it.units), kh = quotient(k, it.chunks);
+        u = (int)(off - k * it.units);
+        c = (int)(k - kh * it.chunks);
+        h = (int)kh;
         n = (int)min((long long)(it.units - u), end - x);
     }
     __device__ __forceinline__ void next(const StepArgs& g, int H) {
@@ -134,8 +138,6 @@ struct StepSmem {
     float cq[NQ];
     int t0[NQ], t1[NQ];
     float m[NW][NQ], l[NW][NQ];
-    uint64_t bar[NW][kRingPages];
-    int mask[NW][kRingPages];  // which 16-token halves of a slot hold tokens
     Walk<NQ> own[NW], ahead[NW];  // each warp's place in the work: what it computes, what it fetches
     long long pref[NW * 32 + 1];
     long long sums[NW];
@@ -148,12 +150,27 @@ __device__ __forceinline__ uint32_t fma2(uint32_t x, uint32_t y, uint32_t z) {
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
     return r;
 }
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t in_1024(uint32_t w) {  // (w & MASK) | 1024, 1024: one lop3
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "r"(0x64006400u));
+    return r;
+}
 // Codes q of the nibbles 0 and 4, or 1 and 5, of a word, as two fp16 (exact).
 __device__ __forceinline__ uint32_t codes_low(uint32_t w) {  // (1024 + e) - 1032
-    return fma2((w & 0x000F000Fu) | 0x64006400u, 0x3C003C00u, 0xE408E408u);
+    return fma2(in_1024<0x000F000Fu>(w), 0x3C003C00u, 0xE408E408u);
 }
 __device__ __forceinline__ uint32_t codes_high(uint32_t w) {  // (1024 + 16 e) / 16 - 72
-    return fma2((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
+    return fma2(in_1024<0x00F000F0u>(w), 0x2C002C00u, 0xD480D480u);
+}
+
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ uint32_t perm(uint32_t a, uint32_t b, uint32_t sel) {
@@ -268,10 +285,6 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3, r8 = lane >> 2;
     const int H = a.p.H;
 
-    if (lane == 0) {
-        for (int i = 0; i < kRingPages; ++i) mbar_init(&sm.bar[warp][i], 1);
-        fence_mbar_init();
-    }
     grid_dep_wait();
     grid_dep_launch();
 
@@ -294,16 +307,18 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
     if (threadIdx.x == 0) sm.pref[0] = 0;
     __syncthreads();
     const long long total = sm.pref[NW * 32];
-    const long long ctas = min((long long)gridDim.x, (total + g.min_units - 1) / g.min_units);
+    const int ctas = (int)min((long long)gridDim.x, quotient(total + g.min_units - 1, g.min_units));
     if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
-    if (blockIdx.x >= ctas) return;
+    if ((int)blockIdx.x >= ctas) return;
+    const long long share = quotient(total, ctas);  // the first `extra` CTAs have one unit more
+    const int extra = (int)(total - share * ctas);
 
     Walk<NQ>& wk = sm.own[warp];
     Walk<NQ>& pw = sm.ahead[warp];
     if (lane == 0) {
         Walk<NQ> w;
-        w.x = total / ctas * blockIdx.x + min((long long)blockIdx.x, total % ctas);
-        w.end = w.x + total / ctas + (blockIdx.x < total % ctas ? 1 : 0);
+        w.x = share * blockIdx.x + min((int)blockIdx.x, extra);
+        w.end = w.x + share + ((int)blockIdx.x < extra ? 1 : 0);
         int lo = 0, hi = NW * 32;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -324,12 +339,11 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
     __syncwarp();
 
     // ---- the copies' side of the ring
-    int ahead = 0;  // slots filled or being filled
     int pk = 0, pg0 = -1, pg1 = -1;  // the warp's next unit of the segment; pages of 32 of them, one a lane
+    uint32_t held = 0;               // two bits a ring slot: which 16-token halves hold tokens
     const int plog = a.p.page_log2;
-    const bool halves = plog == 4;
     const auto page_of = [&](int tok) {
-        if (tok >= pw.it.t1 || tok + (halves ? 16 : kUnit) <= pw.it.t0) return -1;
+        if (tok >= pw.it.t1 || tok + 16 <= pw.it.t0) return -1;
         const int col = tok >> plog;  // below max_pages, as t1 is
         const int page = a.b.table[(long long)pw.it.s * a.b.table_stride + col];
         if (page >= 0 && page < a.p.n_pages) return page;
@@ -345,41 +359,44 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
             pk = 0;
             off = warp;
         }
-        if (pw.n == 0) return;
-        if ((pk & 31) == 0) {
-            const int o = warp + NW * (pk + lane);
-            const int tok = (pw.it.u0 + pw.u + o) * kUnit;
-            pg0 = o < pw.n ? page_of(tok) : -1;
-            pg1 = halves && o < pw.n ? page_of(tok + 16) : -1;
-        }
-        const int tok = (pw.it.u0 + pw.u + off) * kUnit;
-        const int p0 = __shfl_sync(~0u, pg0, pk & 31), p1 = __shfl_sync(~0u, pg1, pk & 31);
-        ++pk;
-        ++ahead;
-        const int part = halves ? 16 : kUnit;
-        const int half = lane >> 2, kind = lane & 3;
-        const int page = half ? p1 : p0;
-        if (lane == 0) {
-            sm.mask[warp][slot] = halves ? (p0 >= 0 ? 1 : 0) | (p1 >= 0 ? 2 : 0) : (p0 >= 0 ? 3 : 0);
-            mbar_expect_tx(&sm.bar[warp][slot], ((p0 >= 0) + (p1 >= 0)) * part * (D + 4));
-        }
-        __syncwarp();
-        if (half < (halves ? 2 : 1) && page >= 0) {
-            const long long at = (((long long)page * H + pw.h) << plog) + (tok & ((1 << plog) - 1));
+        if (pw.n > 0) {
+            const int tok = (pw.it.u0 + pw.u + off) * kUnit;
+            if ((pk & 31) == 0) {
+                const int o = off + NW * lane, at = tok + NW * kUnit * lane;
+                pg0 = o < pw.n ? page_of(at) : -1;
+                pg1 = o < pw.n ? page_of(at + 16) : -1;
+            }
+            const int p0 = __shfl_sync(~0u, pg0, pk & 31), p1 = __shfl_sync(~0u, pg1, pk & 31);
+            ++pk;
+            held = (held & ~(3u << (2 * slot))) | ((p0 >= 0 ? 1u : 0u) | (p1 >= 0 ? 2u : 0u)) << (2 * slot);
             uint8_t* dst = sm.ring[warp][slot];
-            const int i = kind & 1;
-            if (kind < 2)
-                bulk_load(dst + i * kUnit * (D / 2) + half * 16 * (D / 2), a.p.codes[i] + at * (D / 2), part * (D / 2),
-                          &sm.bar[warp][slot]);
-            else
-                bulk_load(dst + kUnit * D + i * kUnit * 2 + half * 32, a.p.tok[i] + at, part * 2, &sm.bar[warp][slot]);
+            constexpr int RB = D / 2, PER = 16 * RB / 512;  // bytes of a token's codes; copies a lane makes of a half
+            const int in_page = tok & ((1 << plog) - 1) & ~31;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int page = hf ? p1 : p0;
+                if (page >= 0) {
+                    const long long at =
+                        (((long long)page * H + pw.h) << plog) + in_page + (plog > 4 ? 16 * hf : 0);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int k = 0; k < PER; ++k) {
+                            const int byte = lane * 16 + k * 512;
+                            copy16(dst + i * kUnit * RB + hf * 16 * RB + byte, a.p.codes[i] + at * RB + byte);
+                        }
+                    // 32 bytes of scales a tensor: lanes 0, 1 (K) and 2, 3 (V)
+                    if (lane < 4)
+                        copy16(dst + kUnit * D + (lane >> 1) * kUnit * 2 + hf * 32 + (lane & 1) * 16,
+                               a.p.tok[lane >> 1] + at + (lane & 1) * 8);
+                }
+            }
         }
+        copies_commit();
     };
     for (int i = 0; i < kRingPages; ++i) produce(i);
 
     int slot = 0;
-    uint32_t phase = 0;
-    bool failed = false;
 
     // ---- segments
     while (wk.n > 0) {
@@ -418,23 +435,13 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
 
         for (int off = warp; off < units; off += NW) {
             const int tok0 = (unit0 + off) * kUnit;
-            if (!failed) {
-                const bool in = mbar_wait(&sm.bar[warp][slot], phase, KVQ_WAIT_LIMIT(kWaitUnit));
-                if (__any_sync(~0u, !in)) {  // results are void from here on; nothing more is fetched
-                    failed = true;
-                    report_error(kErrBarrierTimeout);
-                    // copies in flight end before the CTA's memory is given back
-                    for (int i = 0, at = slot, ph = phase; i < ahead; ++i) {
-                        mbar_wait(&sm.bar[warp][at], ph, kWaitUnit);
-                        if (++at == kRingPages) at = 0, ph ^= 1;
-                    }
-                }
-            }
+            copies_wait<kRingPages - 1>();
+            __syncwarp();
             const uint8_t* ring = sm.ring[warp][slot];
             {   // one token a lane: scales of K, log2 and inverse of V's
                 const __half* sc = reinterpret_cast<const __half*>(ring + kUnit * D);
                 const float sk = __half2float(sc[lane]), sv = fmaxf(__half2float(sc[kUnit + lane]), 0x1p-24f);
-                const bool there = (sm.mask[warp][slot] >> (lane >> 4) & 1) && tok0 + lane < seen1 && tok0 + lane >= seen0;
+                const bool there = (held >> (2 * slot + (lane >> 4)) & 1) && tok0 + lane < seen1 && tok0 + lane >= seen0;
                 sm.par[warp][lane] = there ? make_float4(sk, lg2(sv), __frcp_rn(sv), 0.0f)
                                            : make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
             }
@@ -560,9 +567,8 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
                 }
             }
             __syncwarp();  // the slot has been read
-            --ahead;
-            if (!failed) produce(slot);
-            if (++slot == kRingPages) slot = 0, phase ^= 1;
+            produce(slot);
+            if (++slot == kRingPages) slot = 0;
         }
 
         // ---- the warps' states into one
@@ -618,8 +624,8 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
         }
         if (begins && !ends && threadIdx.x == 0) {
             // CTAs from this one to that of the item's last unit
-            const long long last = wk.x + wk.it.units - 1, big = total / ctas + 1, nbig = total % ctas;
-            const long long cta = last < big * nbig ? last / big : nbig + (last - big * nbig) / (big - 1);
+            const long long last = wk.x + wk.it.units - 1, bigs = (share + 1) * extra;
+            const long long cta = last < bigs ? last / (share + 1) : extra + (last - bigs) / share;
             a.meta[blockIdx.x] = make_int4(wk.it.s, wk.h, wk.c * NQ, (int)(cta - blockIdx.x) + 1);
         }
         __syncwarp();
