@@ -4,6 +4,7 @@
 // kvq_pages_read_errors reads.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -152,22 +153,39 @@ kvq_status launch(void (*kernel)(A), const A& args, dim3 grid, int threads, int 
     return launch_status();
 }
 
-// Once per process and kernel would do; the attribute is per device, and the
-// call costs well under a microsecond.
-bool allow_smem(const void* kernel, int bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess &&
-           cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                cudaSharedmemCarveoutMaxShared) == cudaSuccess;
+// Dynamic shared memory and the largest carveout, once per kernel and device
+// (racing callers set the same attributes, which is harmless).
+template <auto Kernel>
+bool allow_smem(int bytes) {
+    static std::atomic<uint64_t> done{0};  // one bit a device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    const uint64_t bit = uint64_t(1) << dev;
+    if (done.load(std::memory_order_acquire) & bit) return true;
+    if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess ||
+        cudaFuncSetAttribute(Kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+            cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    done.fetch_or(bit, std::memory_order_release);
+    return true;
 }
 
 // SMs of the current device.
 int sm_count() {
+    static std::atomic<int> known[64];
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
         cudaGetLastError();
         return 148;
     }
+    if ((n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        return 148;
+    }
+    known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 
@@ -197,13 +215,13 @@ kvq_status launch_step(StepArgs g, int sms, cudaStream_t st) {
     using Sh = StepShape<NQ>;
     constexpr int smem = (int)sizeof(StepSmem<D, NQ, HAD, Sh::kWarps>);
     static_assert(smem * Sh::kPerSm + Sh::kPerSm * 1024 <= 228 * 1024, "shared memory of the CTAs on one SM");
-    const auto kernel = pages_step_kernel<D, NQ, HAD, Sh::kWarps, Sh::kPerSm>;
-    if (!allow_smem(reinterpret_cast<const void*>(kernel), smem)) return KVQ_ERR_CUDA;
+    constexpr auto kernel = pages_step_kernel<D, NQ, HAD, Sh::kWarps, Sh::kPerSm>;
+    if (!allow_smem<kernel>(smem)) return KVQ_ERR_CUDA;
     g.min_units = Sh::kWarps;
     const int grid = sms * Sh::kPerSm;
     kvq_status s = launch<StepArgs>(kernel, g, dim3(grid), Sh::kWarps * 32, smem, st);
     if (s != KVQ_OK) return s;
-    return launch<AttnArgs>(pages_merge_kernel<D, NQ, HAD>, g.a, dim3(grid, NQ), 128, 0, st);
+    return launch<AttnArgs>(pages_merge_kernel<D, NQ, HAD>, g.a, dim3(grid), kMergeWarps * 32, 0, st);
 }
 
 template <int D, bool HAD>

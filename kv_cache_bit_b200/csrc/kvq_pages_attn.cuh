@@ -115,14 +115,17 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, int row, int head,
 }
 
 // Merges the partial states of an item that several CTAs worked on.  One CTA a
-// (main-kernel CTA, query): those of main-kernel CTAs that no split item
-// starts in return at once.  Slot 2b + 1 is the state of an item that CTA b
-// began and did not end, slot 2b of one that it did not begin.  The order of
-// the sums is fixed.
+// main-kernel CTA: those of CTAs that no split item starts in return at once.
+// Slot 2b + 1 is the state of an item that CTA b began and did not end, slot
+// 2b of one that it did not begin.  kMergeWarps / NQ warps share a query's
+// states; the order of the sums is fixed.
+constexpr int kMergeWarps = 16;
+
 template <int D, int NQ, bool HAD>
-__global__ void __launch_bounds__(128) pages_merge_kernel(AttnArgs a) {
-    __shared__ float s_o[4][D], s_l[4];
-    const int b = blockIdx.x, qi = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kMergeWarps * 32) pages_merge_kernel(AttnArgs a) {
+    constexpr int W = kMergeWarps / NQ;
+    __shared__ float s_o[NQ][W][D], s_l[NQ][W];
+    const int b = blockIdx.x, qi = (threadIdx.x >> 5) / W, part = (threadIdx.x >> 5) % W, lane = threadIdx.x & 31;
     grid_dep_wait();
     grid_dep_launch();
     const int4 meta = a.meta[b];
@@ -131,7 +134,6 @@ __global__ void __launch_bounds__(128) pages_merge_kernel(AttnArgs a) {
     const int s = meta.x, h = meta.y, i = meta.z + qi;
     const int end = a.b.start[s + 1], lo = max(a.b.start[s], 0);
     const int row = lo + i / a.G, head = h * a.G + i % a.G;
-    if (row >= min(end, a.rows)) return;
     const auto slot = [&](int k) { return ((long long)(k == 0 ? 2 * b + 1 : 2 * (b + k)) * NQ + qi); };
     float M = kLowest;
     for (int k = lane; k < n; k += 32) M = fmaxf(M, a.ml[2 * slot(k)]);
@@ -139,25 +141,25 @@ __global__ void __launch_bounds__(128) pages_merge_kernel(AttnArgs a) {
     for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, x));
     float v[D / 32] = {}, l = 0.0f;
 #pragma unroll 4
-    for (int k = warp; k < n; k += 4) {
+    for (int k = part; k < n; k += W) {
         const long long at = slot(k);
         const float2 ml = reinterpret_cast<const float2*>(a.ml)[at];
         const float f = ex2(ml.x - M);
         l = __fmaf_rn(ml.y, f, l);
 #pragma unroll
-        for (int i2 = 0; i2 < D / 32; ++i2) v[i2] = __fmaf_rn(a.part[at * D + lane + 32 * i2], f, v[i2]);
+        for (int c = 0; c < D / 32; ++c) v[c] = __fmaf_rn(a.part[at * D + lane + 32 * c], f, v[c]);
     }
 #pragma unroll
-    for (int i2 = 0; i2 < D / 32; ++i2) s_o[warp][lane + 32 * i2] = v[i2];
-    if (lane == 0) s_l[warp] = l;
+    for (int c = 0; c < D / 32; ++c) s_o[qi][part][lane + 32 * c] = v[c];
+    if (lane == 0) s_l[qi][part] = l;
     __syncthreads();
-    if (warp != 0) return;
+    if (part != 0 || row >= min(end, a.rows)) return;
 #pragma unroll
-    for (int i2 = 0; i2 < D / 32; ++i2) {
-        v[i2] = s_o[0][lane + 32 * i2];
-        for (int w = 1; w < 4; ++w) v[i2] += s_o[w][lane + 32 * i2];
+    for (int w = 1; w < W; ++w) {
+        l += s_l[qi][w];
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) v[c] += s_o[qi][w][lane + 32 * c];
     }
-    l = ((s_l[0] + s_l[1]) + s_l[2]) + s_l[3];
     finish_row<D, HAD>(a, row, head, v, M, l);
 }
 

@@ -49,6 +49,7 @@ struct StepArgs {
 // A sequence's share of the work.
 struct Item {
     int s, lo, nq, chunks, units, u0, t0, t1;
+    int len, base;  // tokens of the sequence; token of row r: base + r
     long long cost;
 };
 
@@ -68,7 +69,10 @@ __device__ __forceinline__ Item item_of(const StepArgs& g, int s, int H) {
         it.nq = 0;
         return it;
     }
-    const Range r = range_of(g.a, g.a.b.len[s], end, it.lo, hi);
+    const int len = g.a.b.len[s];
+    it.len = max(len, 0);
+    it.base = len - end;
+    const Range r = range_of(g.a, len, end, it.lo, hi);
     it.t0 = r.t0;
     it.t1 = r.t1;
     it.u0 = r.t0 / kUnit;
@@ -139,7 +143,6 @@ struct StepSmem {
     int t0[NQ], t1[NQ];
     float m[NW][NQ], l[NW][NQ];
     Walk<NQ> own[NW], ahead[NW];  // each warp's place in the work: what it computes, what it fetches
-    long long pref[NW * 32 + 1];
     long long sums[NW];
 };
 
@@ -164,8 +167,9 @@ __device__ __forceinline__ uint32_t codes_high(uint32_t w) {  // (1024 + 16 e) /
     return fma2(in_1024<0x00F000F0u>(w), 0x2C002C00u, 0xD480D480u);
 }
 
-__device__ __forceinline__ void copy16(void* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+// 16 bytes to shared memory: `n` (16 or 0) of them from src, zeros for the rest.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -204,7 +208,6 @@ __device__ __forceinline__ void load_queries(const StepArgs& g, StepSmem<D, NQ, 
     constexpr int N = D / 32, C = D / 4;  // channels a lane; channels a fragment lane
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const AttnArgs& a = g.a;
-    const int len = a.b.len[it.s], end = a.b.start[it.s + 1];
     for (int qi = warp; qi < NQ; qi += NW) {
         const int i = c * NQ + qi;
         const bool there = i < it.nq;
@@ -227,8 +230,11 @@ __device__ __forceinline__ void load_queries(const StepArgs& g, StepSmem<D, NQ, 
         }
         if constexpr (HAD) {
             if (a.signs) {
+                int8_t sg[N];
+                if constexpr (N == 4) *reinterpret_cast<char4*>(sg) = reinterpret_cast<const char4*>(a.signs)[lane];
+                else *reinterpret_cast<char2*>(sg) = reinterpret_cast<const char2*>(a.signs)[lane];
 #pragma unroll
-                for (int k = 0; k < N; ++k) v[k] *= (float)a.signs[lane * N + k];
+                for (int k = 0; k < N; ++k) v[k] *= (float)sg[k];
             }
             lane_stages<1, N>(v);
 #pragma unroll
@@ -262,10 +268,8 @@ __device__ __forceinline__ void load_queries(const StepArgs& g, StepSmem<D, NQ, 
             sm.cq[qi] = a.scale2 / f;
             Range r{0, 0};
             if (there) {
-                const int row = it.lo + i / a.G;
-                // (the error word was set for the sequence's whole range)
-                const long long n = max(len, 0), pos = (long long)len - end + row;
-                const long long hi = min(a.causal ? min(pos + 1, n) : n, (long long)it.t1);
+                const long long pos = (long long)it.base + it.lo + i / a.G;
+                const long long hi = min(a.causal ? pos + 1 : (long long)it.len, (long long)it.t1);
                 const long long lo = a.causal && a.window > 0 ? max(pos - a.window + 1, 0ll) : 0;
                 if (lo < hi) r = Range{(int)lo, (int)hi};
             }
@@ -288,53 +292,59 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
     grid_dep_wait();
     grid_dep_launch();
 
-    // ---- this CTA's range: prefix sums of the sequences' costs
-    const int per = (a.b.n_seqs + NW * 32 - 1) / (NW * 32);
+    // ---- this CTA's range: prefix sums of the sequences' costs, a run of `per` sequences a thread
+    const int per = (a.b.n_seqs + NW * 32 - 1) / (NW * 32), s0 = threadIdx.x * per;
+    Item first;
     long long mine = 0;
-    for (int s = threadIdx.x * per; s < min((int)(threadIdx.x + 1) * per, a.b.n_seqs); ++s)
-        mine += item_of<NQ>(g, s, H).cost;
-    long long acc_sum = mine;
+    for (int s = min(s0 + per, a.b.n_seqs) - 1; s >= s0; --s) {  // the last one read is the run's first
+        first = item_of<NQ>(g, s, H);
+        mine += first.cost;
+    }
+    long long sum = mine;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
-        const long long o = __shfl_up_sync(~0u, acc_sum, x);
-        if (lane >= x) acc_sum += o;
+        const long long o = __shfl_up_sync(~0u, sum, x);
+        if (lane >= x) sum += o;
     }
-    if (lane == 31) sm.sums[warp] = acc_sum;
+    if (lane == 31) sm.sums[warp] = sum;
     __syncthreads();
-    long long before = 0;
-    for (int w = 0; w < warp; ++w) before += sm.sums[w];
-    sm.pref[threadIdx.x + 1] = before + acc_sum;
-    if (threadIdx.x == 0) sm.pref[0] = 0;
-    __syncthreads();
-    const long long total = sm.pref[NW * 32];
+    long long before = sum - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        if (w < warp) before += sm.sums[w];
+        total += sm.sums[w];
+    }
     const int ctas = (int)min((long long)gridDim.x, quotient(total + g.min_units - 1, g.min_units));
     if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
     if ((int)blockIdx.x >= ctas) return;
     const long long share = quotient(total, ctas);  // the first `extra` CTAs have one unit more
     const int extra = (int)(total - share * ctas);
-
-    Walk<NQ>& wk = sm.own[warp];
-    Walk<NQ>& pw = sm.ahead[warp];
-    if (lane == 0) {
+    const long long begin = share * blockIdx.x + min((int)blockIdx.x, extra);
+    if (before <= begin && begin < before + mine) {  // this thread's run holds the first unit
         Walk<NQ> w;
-        w.x = share * blockIdx.x + min((int)blockIdx.x, extra);
-        w.end = w.x + share + ((int)blockIdx.x < extra ? 1 : 0);
-        int lo = 0, hi = NW * 32;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (sm.pref[mid] <= w.x) lo = mid;
-            else hi = mid;
-        }
-        long long off = w.x - sm.pref[lo];
-        int s = lo * per;
-        w.it = item_of<NQ>(g, s, H);
-        while (off >= w.it.cost && s + 1 < a.b.n_seqs) {
+        w.x = begin;
+        w.end = begin + share + ((int)blockIdx.x < extra ? 1 : 0);
+        w.it = first;
+        long long off = begin - before;
+        for (int s = s0; off >= w.it.cost && s + 1 < a.b.n_seqs;) {
             off -= w.it.cost;
             w.it = item_of<NQ>(g, ++s, H);
         }
         w.place(off);
-        wk = w;
-        pw = w;
+        sm.own[0] = w;
+    }
+    __syncthreads();
+    Walk<NQ>& wk = sm.own[warp];
+    Walk<NQ>& pw = sm.ahead[warp];
+    {
+        constexpr int kWords = sizeof(Walk<NQ>) / 4;
+        static_assert(sizeof(Walk<NQ>) % 4 == 0 && kWords <= 32);
+        int word = 0;
+        if (lane < kWords) word = reinterpret_cast<const int*>(&sm.own[0])[lane];
+        if (lane < kWords) {
+            if (warp) reinterpret_cast<int*>(&wk)[lane] = word;
+            reinterpret_cast<int*>(&pw)[lane] = word;
+        }
     }
     __syncwarp();
 
@@ -369,27 +379,24 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
             const int p0 = __shfl_sync(~0u, pg0, pk & 31), p1 = __shfl_sync(~0u, pg1, pk & 31);
             ++pk;
             held = (held & ~(3u << (2 * slot))) | ((p0 >= 0 ? 1u : 0u) | (p1 >= 0 ? 2u : 0u)) << (2 * slot);
-            uint8_t* dst = sm.ring[warp][slot];
             constexpr int RB = D / 2, PER = 16 * RB / 512;  // bytes of a token's codes; copies a lane makes of a half
+            const uint32_t dst = smem_u32(sm.ring[warp][slot]);
             const int in_page = tok & ((1 << plog) - 1) & ~31;
+            // first token of the halves; a half that is not there is filled with zeros
+            const long long at0 = (((long long)max(p0, 0) * H + pw.h) << plog) + in_page;
+            const long long at1 = (((long long)max(p1, 0) * H + pw.h) << plog) + in_page + (plog > 4 ? 16 : 0);
+            const int n0 = p0 >= 0 ? 16 : 0, n1 = p1 >= 0 ? 16 : 0;
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int page = hf ? p1 : p0;
-                if (page >= 0) {
-                    const long long at =
-                        (((long long)page * H + pw.h) << plog) + in_page + (plog > 4 ? 16 * hf : 0);
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int k = 0; k < PER; ++k) {
-                            const int byte = lane * 16 + k * 512;
-                            copy16(dst + i * kUnit * RB + hf * 16 * RB + byte, a.p.codes[i] + at * RB + byte);
-                        }
-                    // 32 bytes of scales a tensor: lanes 0, 1 (K) and 2, 3 (V)
-                    if (lane < 4)
-                        copy16(dst + kUnit * D + (lane >> 1) * kUnit * 2 + hf * 32 + (lane & 1) * 16,
-                               a.p.tok[lane >> 1] + at + (lane & 1) * 8);
+                for (int k = 0; k < PER; ++k) {
+                    const int byte = lane * 16 + k * 512;
+                    copy16(dst + i * kUnit * RB + byte, a.p.codes[i] + at0 * RB + byte, n0);
+                    copy16(dst + i * kUnit * RB + 16 * RB + byte, a.p.codes[i] + at1 * RB + byte, n1);
                 }
+            if (lane < 8) {  // 64 bytes of scales a tensor: lanes 0 .. 3 (K) and 4 .. 7 (V)
+                const __half* src = (lane & 4 ? a.p.tok[1] : a.p.tok[0]) + (lane & 2 ? at1 : at0) + (lane & 1) * 8;
+                copy16(dst + kUnit * D + lane * 16, src, lane & 2 ? n1 : n0);
             }
         }
         copies_commit();
@@ -531,7 +538,7 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
                         float w[2] = {0.0f, 0.0f};
 #pragma unroll
                         for (int k = 0; k < 2 && 2 * n + k < NV; ++k) {
-                            w[k] = ex2(y[mt][2 * n + k][hf] - M[2 * n + k] + kBias);
+                            w[k] = ex2(y[mt][2 * n + k][hf] - (M[2 * n + k] - kBias));
                             l[2 * n + k] = __fmaf_rn(w[k], par[mt][hf].z, l[2 * n + k]);
                         }
                         bw[n][hf] = transposed(Elem<__half>::pack(w[0], w[1]));
@@ -625,7 +632,8 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
         if (begins && !ends && threadIdx.x == 0) {
             // CTAs from this one to that of the item's last unit
             const long long last = wk.x + wk.it.units - 1, bigs = (share + 1) * extra;
-            const long long cta = last < bigs ? last / (share + 1) : extra + (last - bigs) / share;
+            const long long cta = last < bigs ? quotient(last, (int)min(share + 1, 0x7FFFFFFFll))
+                                              : extra + quotient(last - bigs, (int)min(share, 0x7FFFFFFFll));
             a.meta[blockIdx.x] = make_int4(wk.it.s, wk.h, wk.c * NQ, (int)(cta - blockIdx.x) + 1);
         }
         __syncwarp();

@@ -235,11 +235,12 @@ def _paged(call: str, cfg: "Config", pages: "PagedCache", batch: "Batch", *tenso
     for x, heads in tensors:
         if x is None:
             continue
-        if x.device != device or x.dim() != 3 or x.shape[2] != cfg.head_dim or x.stride(2) != 1:
+        shape = x.shape
+        if len(shape) != 3 or shape[2] != cfg.head_dim or x.stride(2) != 1 or x.device != device:
             raise KvqError(KVQ_ERR_INVALID_ARG, call + ": tensors are [rows, heads, head_dim] on the cache's device")
-        if (heads and x.shape[1] != heads) or rows not in (None, x.shape[0]):
+        if (heads and shape[1] != heads) or (rows is not None and rows != shape[0]):
             raise KvqError(KVQ_ERR_INVALID_ARG, call + ": heads or rows of the tensors differ")
-        rows = x.shape[0]
+        rows = shape[0]
     return rows
 
 
@@ -247,14 +248,16 @@ def _rows(x, call: str):
     """kvq_rows of a [rows, heads, head_dim] tensor (None: a null pointer)."""
     if x is None:
         return None
-    if not _DTYPES:
-        import torch
-        _DTYPES.update({torch.float16: KVQ_F16, torch.bfloat16: KVQ_BF16, torch.float32: KVQ_F32})
     kind = _DTYPES.get(x.dtype)
     if kind is None:
-        raise KvqError(KVQ_ERR_UNSUPPORTED, call)
+        import torch
+        _DTYPES.update({torch.float16: KVQ_F16, torch.bfloat16: KVQ_BF16, torch.float32: KVQ_F32})
+        kind = _DTYPES.get(x.dtype)
+        if kind is None:
+            raise KvqError(KVQ_ERR_UNSUPPORTED, call)
+    stride = x.stride()
     # (a tensor without rows has no address; nothing is read through this one)
-    return kvq_rows(x.data_ptr() or 16, x.stride(0), x.stride(1), kind, 0)
+    return kvq_rows(x.data_ptr() or 16, stride[0], stride[1], kind, 0)
 
 
 def _on(pages: "PagedCache", stream, call: str, fn, *args):
@@ -267,9 +270,12 @@ def _on(pages: "PagedCache", stream, call: str, fn, *args):
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
     if torch.cuda.current_device() == index:
-        return _check(fn(*args, stream), call)
-    with torch.cuda.device(index):
-        return _check(fn(*args, stream), call)
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status != KVQ_OK:
+        raise KvqError(status, call)
 
 
 def kvq_pages_write(cfg: "Config", pages: "PagedCache", batch: "Batch", k, v, stream=None):
@@ -307,7 +313,7 @@ def kvq_pages_attention(cfg: "Config", pages: "PagedCache", batch: "Batch", q, o
     if out.shape[1] != heads or ws is None or ws.device != pages.device or not ws.is_contiguous():
         raise KvqError(KVQ_ERR_INVALID_ARG, name + ": out of q's shape, a contiguous workspace on the cache's device")
     if lse is not None and (lse.device != pages.device or tuple(lse.shape) != (rows, heads) or
-                            str(lse.dtype) != "torch.float32" or not lse.is_contiguous()):
+                            lse.element_size() != 4 or not lse.is_floating_point() or not lse.is_contiguous()):
         raise KvqError(KVQ_ERR_INVALID_ARG, name + ": lse is a contiguous float32 [rows, q_heads]")
     _on(pages, stream, name, lib.kvq_pages_attention, cfg.c, pages.c, batch.c, _rows(q, name), heads, rows, scale,
         1 if causal else 0, window, _rows(out, name), _ptr(lse) or None, _ptr(ws), ws.numel() * ws.element_size())
@@ -418,6 +424,10 @@ class PagedCache:
     c: kvq_pages
     codes: list
     tok: list
+    device: object = None
+
+    def __post_init__(self):
+        self.device = self.codes[0].device
 
     @classmethod
     def allocate(cls, cfg: Config, n_pages: int, kv_heads: int, page_tokens: int, device="cuda") -> "PagedCache":
@@ -442,10 +452,6 @@ class PagedCache:
         c = kvq_pages(n, h, cfg.head_dim, t, (ctypes.c_void_p * 2)(*[_ptr(x) for x in codes]),
                       (ctypes.c_void_p * 2)(*[_ptr(x) for x in tok]))
         return cls(c, list(codes), list(tok))
-
-    @property
-    def device(self):
-        return self.codes[0].device
 
     def snapshot(self) -> dict:
         """A host copy of the pool (checkpoint); the batch's tables and
@@ -481,9 +487,6 @@ class Batch:
                 (table.shape[1] > 1 and table.stride(1) != 1):
             raise KvqError(KVQ_ERR_INVALID_ARG, "Batch")
         self.start, self.length, self.table = start, length, table
+        self.device = table.device
         stride = table.stride(0) if n > 1 else table.shape[1]
         self.c = kvq_batch(n, table.shape[1], stride, max_rows, _ptr(start), _ptr(length), _ptr(table))
-
-    @property
-    def device(self):
-        return self.table.device
