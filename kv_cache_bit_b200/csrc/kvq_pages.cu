@@ -196,17 +196,24 @@ struct StepShape {
 };
 
 struct AttnWorkspace {
-    size_t meta, ml, part, bytes;
+    size_t meta, ml, part, left, bytes;
 };
 AttnWorkspace attn_workspace(int sms, int d) {
-    const size_t small = size_t(sms) * StepShape<8>::kPerSm, large = size_t(sms) * StepShape<16>::kPerSm;
-    const size_t ctas = large > small ? large : small;
-    const size_t queries = small * 8 > large * 16 ? small * 8 : large * 16;
+    size_t ctas = 0, queries = 0, warps = 0;  // the most of any shape: CTAs, and query rows over all CTAs and warps
+    const auto take = [&](int per_sm, int nw, int nq) {
+        const size_t n = size_t(sms) * per_sm;
+        if (n > ctas) ctas = n;
+        if (n * nq > queries) queries = n * nq;
+        if (n * nq * nw > warps) warps = n * nq * nw;
+    };
+    take(StepShape<8>::kPerSm, StepShape<8>::kWarps, 8);
+    take(StepShape<16>::kPerSm, StepShape<16>::kWarps, 16);
     AttnWorkspace w;
     w.meta = 0;
     w.ml = ctas * 16;
     w.part = w.ml + 2 * queries * 8;
-    w.bytes = w.part + 2 * queries * d * 4;
+    w.left = w.part + 2 * queries * d * 4;
+    w.bytes = w.left + warps * d * 4;
     return w;
 }
 
@@ -217,7 +224,6 @@ kvq_status launch_step(StepArgs g, int sms, cudaStream_t st) {
     static_assert(smem * Sh::kPerSm + Sh::kPerSm * 1024 <= 228 * 1024, "shared memory of the CTAs on one SM");
     constexpr auto kernel = pages_step_kernel<D, NQ, HAD, Sh::kWarps, Sh::kPerSm>;
     if (!allow_smem<kernel>(smem)) return KVQ_ERR_CUDA;
-    g.min_units = Sh::kWarps;
     const int grid = sms * Sh::kPerSm;
     kvq_status s = launch<StepArgs>(kernel, g, dim3(grid), Sh::kWarps * 32, smem, st);
     if (s != KVQ_OK) return s;
@@ -363,8 +369,8 @@ kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, co
     a.meta = reinterpret_cast<int4*>(base + w.meta);
     a.ml = reinterpret_cast<float*>(base + w.ml);
     a.part = reinterpret_cast<float*>(base + w.part);
+    a.left = reinterpret_cast<float*>(base + w.left);
     g.many = 0;
-    g.min_units = 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const long long queries = (long long)a.G * (batch->max_rows > 0 ? batch->max_rows : 1);
     const bool had = cfg->flags == KVQ_HADAMARD;

@@ -34,6 +34,7 @@ struct AttnArgs {
     float scale2, rsqd;  // scale * log2 e; 1 / sqrt(d)
     float* ml;           // partial states: M, l [slot][query][2]
     float* part;         // and o [slot][query][D]
+    float* left;         // o of warps' first items [warp][query][D]
     int4* meta;          // [CTA]: sequence, head, first query, merged slots (0: nothing to merge)
 };
 

@@ -4,26 +4,32 @@
 //
 // Work: an item is (sequence, kv head, up to NQ of the head's query rows); its
 // cost is the number of 32-token units that the sequence's rows see.  All
-// items laid end to end are cut into equal ranges, one a CTA of a single-wave
+// items laid end to end are cut into equal ranges, one a warp of a single-wave
 // grid, whatever the lengths are: one long sequence is spread over the whole
-// GPU, many short ones share CTAs.  Warp w of a CTA takes units w, w + NW, ..
-// of a segment (an item's part of the range) through a ring of its own in
-// shared memory, filled by cp.async that runs ahead over segment borders.  The warps'
-// states are added up in shared memory; a segment that is a whole item is
-// finished there, others leave a partial state for pages_merge_kernel.
+// GPU, many short ones share warps.  A warp works alone -- its own queries,
+// its own ring in shared memory, filled by cp.async that runs ahead over item
+// borders -- and finishes the items that lie whole in its range.  What is left
+// of items at the ends of the ranges is merged per CTA once all its warps are
+// done, and what goes past a CTA by pages_merge_kernel.  (With ranges a CTA
+// and its warps taking units in turn, each item's end stopped all warps:
+// 11% of the warps' time at 64 ragged sequences, and 24 us instead of 13 at 8
+// sequences, where a warp has one or two units.)
 //
 // Per 16 tokens, channels and tokens permuted so that unpacking is cheap:
-//   scores  A = K codes, exact in fp16: a nibble pair ORed into the mantissas of
-//           1024 and less 1032 (or, from the upper nibbles, times 1 / 16 less
-//           72).  Taking the bits as subnormals e 2^-24 would save that
-//           addition, but the tensor core aligns products by their exponent
-//           fields and drops what falls below: errors of 7e-4 of the values.
+//   scores  A = K codes.  A nibble pair is ORed into fp16 mantissas: the lower
+//           nibble of a byte into 1024's, less 1032 (exact); the upper one into
+//           64's, which gives q + 72 without arithmetic, and the accumulator
+//           starts at -72 times the sum of those channels' queries.  (The bits
+//           taken as subnormals e 2^-24 would save the additions too, but the
+//           tensor core aligns products by their exponent fields and drops what
+//           falls below: errors of 7e-4 of the values.)
 //           B = the query, times a power of two for its row so that its
 //           largest element is near 2^15.  A rotated query is split into fp16
 //           high and low parts in neighbouring columns (22 bits of it are
 //           kept); an input that is not rotated fits fp16 exactly.
 //   values  A = V codes transposed (byte permutes pair two tokens' words),
-//           B = w from the score fragments by movmatrix.
+//           B = w from the score fragments by movmatrix.  One more product,
+//           with ones, gives the sum of w that takes the 72 out.
 // Instructions a 16-token tile (4 rotated queries, D = 128): about 210 against
 // 332 of the block cache's kernel, whose channel scales need arithmetic per
 // code; 88 of them on the ALU pipe (2 cycles each): 44 SM cycles, of about 90
@@ -43,7 +49,6 @@ constexpr int slot_bytes() { return kUnit * (D + 4); }  // K codes, V codes, K s
 struct StepArgs {
     AttnArgs a;
     int many;       // sequences of more query rows a kv head than this are not this kernel's (0: all are)
-    int min_units;  // least units a CTA is given
 };
 
 // A sequence's share of the work.
@@ -82,9 +87,9 @@ __device__ __forceinline__ Item item_of(const StepArgs& g, int s, int H) {
     return it;
 }
 
-// x / y of non-negative numbers; 64-bit division only where 32 do not hold x.
-__device__ __forceinline__ long long quotient(long long x, int y) {
-    return x >> 32 ? x / y : (long long)((uint32_t)x / (uint32_t)y);
+// x / y of non-negative numbers; 64-bit division only where 32 do not hold them.
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+    return (x | y) >> 32 ? x / y : (long long)((uint32_t)x / (uint32_t)y);
 }
 
 // A walk over the segments of [x, end) of the work.
@@ -93,7 +98,6 @@ struct Walk {
     long long x, end;  // the current segment begins at x
     Item it;
     int h, c, u, n;    // head, chunk, first unit and units of the segment
-    bool whole_begin, whole_end;
 
     // x, inside sequence it.s at offset `off` from its first unit.
     __device__ __forceinline__ void place(long long off) {
@@ -127,6 +131,13 @@ struct Walk {
     }
 };
 
+// What a warp leaves of an item whose other parts are elsewhere.
+struct Part {
+    int lo, nq, h, c, s;  // the item
+    int there, begins, ends;
+    int ctas;  // where it begins: how many CTAs the item goes over
+};
+
 // NW warps; NQ query rows an item.
 template <int D, int NQ, bool HAD, int NW>
 struct StepSmem {
@@ -134,38 +145,54 @@ struct StepSmem {
     static constexpr int kNV = HAD ? kQT : 2 * kQT;     // query rows a lane holds scores of
     static constexpr int kNP = (kNV + 1) / 2;           // value tiles of 8 columns
     static constexpr int kStride = D + 4;               // floats of a query's o: lanes of one store in 32 banks
-    static constexpr int kMQ = NQ < 8 ? NQ : 8;         // query rows merged at a time
-    alignas(128) uint8_t ring[NW][kRingPages][slot_bytes<D>()];
-    alignas(16) float o[NW][kMQ][kStride];
-    alignas(16) uint32_t q[kQT][D / 32][32][4];
-    alignas(16) float4 par[NW][kUnit];  // a token's K scale, log2 and inverse of its V scale
-    float cq[NQ];
-    int t0[NQ], t1[NQ];
-    float m[NW][NQ], l[NW][NQ];
-    Walk<NQ> own[NW], ahead[NW];  // each warp's place in the work: what it computes, what it fetches
+    static constexpr int kMQ = NQ < 8 ? NQ : 8;         // query rows staged at a time
+    struct Warp {
+        union {
+            alignas(128) uint8_t ring[kRingPages][slot_bytes<D>()];
+            float last[NQ][kStride];  // o of the range's end, once the ring is done with
+        };
+        union {
+            alignas(16) uint32_t q[kQT][D / 32][32][4];
+            float o[kMQ][kStride];
+        };
+        alignas(16) float4 par[kUnit];  // a token's K scale, log2 and inverse of its V scale
+        float init[kQT][8];  // what the score accumulators start from: -kHigh times the sum of those channels
+        float cq[NQ];
+        int t0[NQ], t1[NQ];
+        float m[2][NQ], l[2][NQ];
+        Walk<NQ> own, ahead;  // the place in the work: what is computed, what is fetched
+        Part part[2];         // of the range's first item and of its last
+    };
+    Warp warp[NW];
     long long sums[NW];
+    int chain[NW + 2], n_chains;  // first part (2 warp + which) of each item that has parts; the end
 };
 
 __device__ __forceinline__ float max_or_nan(float x, float y) { return x != x || y <= x ? x : y; }
 
-__device__ __forceinline__ uint32_t fma2(uint32_t x, uint32_t y, uint32_t z) {
-    uint32_t r;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-template <uint32_t MASK>
-__device__ __forceinline__ uint32_t in_1024(uint32_t w) {  // (w & MASK) | 1024, 1024: one lop3
+__device__ __forceinline__ uint32_t add2(uint32_t x, uint32_t y) {
     uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "r"(0x64006400u));
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
     return r;
 }
-// Codes q of the nibbles 0 and 4, or 1 and 5, of a word, as two fp16 (exact).
+template <uint32_t MASK, uint32_t BASE>
+__device__ __forceinline__ uint32_t in_mantissa(uint32_t w) {  // (w & MASK) | BASE: one lop3
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "r"(BASE));
+    return r;
+}
+// The codes of nibbles 0 and 4 of a word as two fp16: q, exactly.
 __device__ __forceinline__ uint32_t codes_low(uint32_t w) {  // (1024 + e) - 1032
-    return fma2(in_1024<0x000F000Fu>(w), 0x3C003C00u, 0xE408E408u);
+    return add2(in_mantissa<0x000F000Fu, 0x64006400u>(w), 0xE408E408u);
 }
-__device__ __forceinline__ uint32_t codes_high(uint32_t w) {  // (1024 + 16 e) / 16 - 72
-    return fma2(in_1024<0x00F000F0u>(w), 0x2C002C00u, 0xD480D480u);
-}
+// Those of nibbles 1 and 5: 64 + e = q + kHigh, without arithmetic.
+constexpr float kHigh = 72.0f;
+__device__ __forceinline__ uint32_t codes_high(uint32_t w) { return in_mantissa<0x00F000F0u, 0x54005400u>(w); }
 
 // 16 bytes to shared memory: `n` (16 or 0) of them from src, zeros for the rest.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n) {
@@ -200,83 +227,113 @@ __device__ __forceinline__ int query_of(int v, int t) {
     return HAD ? 4 * v + t : 8 * (v >> 1) + 2 * t + (v & 1);
 }
 
-// Loads, rotates, scales and splits the queries of chunk c into the B
-// fragments.  One warp a query; a lane holds D / 32 neighbouring channels.
-template <int D, int NQ, bool HAD, int NW>
-__device__ __forceinline__ void load_queries(const StepArgs& g, StepSmem<D, NQ, HAD, NW>& sm, const Item& it, int h,
-                                             int c) {
+// Loads, rotates, scales and splits the queries of chunk c into the warp's B
+// fragments.  A lane holds D / 32 neighbouring channels of a query.
+template <int D, int NQ, bool HAD, typename W>
+__device__ __forceinline__ void load_queries(const AttnArgs& a, W& sm, const Item& it, int h, int c) {
     constexpr int N = D / 32, C = D / 4;  // channels a lane; channels a fragment lane
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const AttnArgs& a = g.a;
-    for (int qi = warp; qi < NQ; qi += NW) {
-        const int i = c * NQ + qi;
-        const bool there = i < it.nq;
-        float v[N] = {};
-        if (there) {
-            const int row = it.lo + i / a.G, head = h * a.G + i % a.G;
-            const uint16_t* src = static_cast<const uint16_t*>(a.q) + row * a.q_row + head * a.q_head + lane * N;
-            uint32_t u[N / 2];
-            if constexpr (N == 4) {
-                const uint2 w = *reinterpret_cast<const uint2*>(src);
-                u[0] = w.x, u[1] = w.y;
-            } else {
-                u[0] = *reinterpret_cast<const uint32_t*>(src);
-            }
+    const int lane = threadIdx.x & 31;
+    float sg[N];
 #pragma unroll
-            for (int k = 0; k < N / 2; ++k) {
-                const float2 f = a.bf16 ? Elem<__nv_bfloat16>::wide(u[k]) : Elem<__half>::wide(u[k]);
-                v[2 * k] = f.x, v[2 * k + 1] = f.y;
+    for (int k = 0; k < N; ++k) sg[k] = 1.0f;
+    if (HAD && a.signs) {
+        if constexpr (N == 4) {
+            const char4 x = reinterpret_cast<const char4*>(a.signs)[lane];
+            sg[0] = x.x, sg[1] = x.y, sg[2] = x.z, sg[3] = x.w;
+        } else {
+            const char2 x = reinterpret_cast<const char2*>(a.signs)[lane];
+            sg[0] = x.x, sg[1] = x.y;
+        }
+    }
+#pragma unroll 1
+    for (int q4 = 0; q4 < NQ; q4 += 4) {
+        uint32_t u[4][N / 2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = c * NQ + q4 + j;
+#pragma unroll
+            for (int k = 0; k < N / 2; ++k) u[j][k] = 0;
+            if (i < it.nq) {
+                const int r = i / a.G;
+                const uint16_t* src = static_cast<const uint16_t*>(a.q) + (it.lo + r) * a.q_row +
+                                      (h * a.G + i - r * a.G) * a.q_head + lane * N;
+                if constexpr (N == 4) {
+                    const uint2 w = *reinterpret_cast<const uint2*>(src);
+                    u[j][0] = w.x, u[j][1] = w.y;
+                } else {
+                    u[j][0] = *reinterpret_cast<const uint32_t*>(src);
+                }
             }
         }
-        if constexpr (HAD) {
-            if (a.signs) {
-                int8_t sg[N];
-                if constexpr (N == 4) *reinterpret_cast<char4*>(sg) = reinterpret_cast<const char4*>(a.signs)[lane];
-                else *reinterpret_cast<char2*>(sg) = reinterpret_cast<const char2*>(a.signs)[lane];
-#pragma unroll
-                for (int k = 0; k < N; ++k) v[k] *= (float)sg[k];
-            }
-            lane_stages<1, N>(v);
-#pragma unroll
-            for (int x = 1; x < 32; x <<= 1) {
-                const float sg = (lane & x) ? -1.0f : 1.0f;
-#pragma unroll
-                for (int k = 0; k < N; ++k) v[k] = __fmaf_rn(v[k], sg, __shfl_xor_sync(~0u, v[k], x));
-            }
-#pragma unroll
-            for (int k = 0; k < N; ++k) v[k] *= a.rsqd;
-        }
-        float m = 0.0f;
-#pragma unroll
-        for (int k = 0; k < N; ++k) m = max_or_nan(m, fabsf(v[k]));
-#pragma unroll
-        for (int x = 16; x; x >>= 1) m = max_or_nan(m, __shfl_xor_sync(~0u, m, x));
-        const float f = m > 0.0f || m != m ? query_scale(m) : 1.0f;
-        const int tile = HAD ? qi >> 2 : qi >> 3, col = HAD ? 2 * (qi & 3) : qi & 7;
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int ch = lane * N + k, t = ch / C, i8 = (ch % C) >> 3, cc = ch & 7;
-            const float x = v[k] * f;
-            const int word = (cc & 1) * 2 + ((cc >> 1) & 1);
-            const __half hi = __float2half_rn(x);
-            reinterpret_cast<__half*>(&sm.q[tile][i8][col * 4 + t][word])[cc >> 2] = hi;
-            if constexpr (HAD)
-                reinterpret_cast<__half*>(&sm.q[tile][i8][(col + 1) * 4 + t][word])[cc >> 2] =
-                    __float2half_rn(x - __half2float(hi));
-        }
-        if (lane == 0) {
-            sm.cq[qi] = a.scale2 / f;
+        if (lane < 4) {
+            const int i = c * NQ + q4 + lane;
             Range r{0, 0};
-            if (there) {
+            if (i < it.nq) {
                 const long long pos = (long long)it.base + it.lo + i / a.G;
                 const long long hi = min(a.causal ? pos + 1 : (long long)it.len, (long long)it.t1);
                 const long long lo = a.causal && a.window > 0 ? max(pos - a.window + 1, 0ll) : 0;
                 if (lo < hi) r = Range{(int)lo, (int)hi};
             }
-            sm.t0[qi] = r.t0;
-            sm.t1[qi] = r.t1;
+            sm.t0[q4 + lane] = r.t0;
+            sm.t1[q4 + lane] = r.t1;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int qi = q4 + j;
+            float v[N];
+#pragma unroll
+            for (int k = 0; k < N / 2; ++k) {
+                const float2 f = a.bf16 ? Elem<__nv_bfloat16>::wide(u[j][k]) : Elem<__half>::wide(u[j][k]);
+                v[2 * k] = f.x, v[2 * k + 1] = f.y;
+            }
+            if constexpr (HAD) {
+#pragma unroll
+                for (int k = 0; k < N; ++k) v[k] *= sg[k];
+                lane_stages<1, N>(v);
+#pragma unroll
+                for (int x = 1; x < 32; x <<= 1) {
+                    const float flip = (lane & x) ? -1.0f : 1.0f;
+#pragma unroll
+                    for (int k = 0; k < N; ++k) v[k] = __fmaf_rn(v[k], flip, __shfl_xor_sync(~0u, v[k], x));
+                }
+#pragma unroll
+                for (int k = 0; k < N; ++k) v[k] *= a.rsqd;
+            }
+            float m = 0.0f;
+#pragma unroll
+            for (int k = 0; k < N; ++k) m = max_or_nan(m, fabsf(v[k]));
+#pragma unroll
+            for (int x = 16; x; x >>= 1) m = max_or_nan(m, __shfl_xor_sync(~0u, m, x));
+            const float f = m > 0.0f || m != m ? query_scale(m) : 1.0f;
+            const int tile = HAD ? qi >> 2 : qi >> 3, col = HAD ? 2 * (qi & 3) : qi & 7;
+            float sum[2] = {0.0f, 0.0f};  // of the channels whose codes come with kHigh
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const int ch = lane * N + k, t = ch / C, i8 = (ch % C) >> 3, cc = ch & 7;
+                const float x = v[k] * f;
+                const int word = (cc & 1) * 2 + ((cc >> 1) & 1);
+                const __half hi = __float2half_rn(x);
+                reinterpret_cast<__half*>(&sm.q[tile][i8][col * 4 + t][word])[cc >> 2] = hi;
+                if (k & 1) sum[0] += __half2float(hi);
+                if constexpr (HAD) {
+                    const __half lo = __float2half_rn(x - __half2float(hi));
+                    reinterpret_cast<__half*>(&sm.q[tile][i8][(col + 1) * 4 + t][word])[cc >> 2] = lo;
+                    if (k & 1) sum[1] += __half2float(lo);
+                }
+            }
+#pragma unroll
+            for (int x = 16; x; x >>= 1) {
+                sum[0] += __shfl_xor_sync(~0u, sum[0], x);
+                if constexpr (HAD) sum[1] += __shfl_xor_sync(~0u, sum[1], x);
+            }
+            if (lane == 0) {
+                sm.init[tile][col] = -kHigh * sum[0];
+                if constexpr (HAD) sm.init[tile][col + 1] = -kHigh * sum[1];
+                sm.cq[qi] = a.scale2 / f;
+            }
         }
     }
+    __syncwarp();
 }
 
 template <int D, int NQ, bool HAD, int NW, int PER_SM>
@@ -284,15 +341,18 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
     using S = StepSmem<D, NQ, HAD, NW>;
     constexpr int QT = S::kQT, NV = S::kNV, NP = S::kNP, NJ = D / 16;
     extern __shared__ __align__(128) uint8_t raw[];
-    S& sm = *reinterpret_cast<S*>(raw);
+    S& sh = *reinterpret_cast<S*>(raw);
     const AttnArgs& a = g.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3, r8 = lane >> 2;
     const int H = a.p.H;
+    typename S::Warp& sm = sh.warp[warp];
+    Walk<NQ>&wk = sm.own, &pw = sm.ahead;
 
+    if (lane < 2) sm.part[lane].there = 0;
     grid_dep_wait();
     grid_dep_launch();
 
-    // ---- this CTA's range: prefix sums of the sequences' costs, a run of `per` sequences a thread
+    // ---- the warps' ranges: prefix sums of the sequences' costs, a run of `per` sequences a thread
     const int per = (a.b.n_seqs + NW * 32 - 1) / (NW * 32), s0 = threadIdx.x * per;
     Item first;
     long long mine = 0;
@@ -306,45 +366,48 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
         const long long o = __shfl_up_sync(~0u, sum, x);
         if (lane >= x) sum += o;
     }
-    if (lane == 31) sm.sums[warp] = sum;
+    if (lane == 31) sh.sums[warp] = sum;
     __syncthreads();
     long long before = sum - mine, total = 0;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-        if (w < warp) before += sm.sums[w];
-        total += sm.sums[w];
+        if (w < warp) before += sh.sums[w];
+        total += sh.sums[w];
     }
-    const int ctas = (int)min((long long)gridDim.x, quotient(total + g.min_units - 1, g.min_units));
+    const int workers = (int)min((long long)gridDim.x * NW, total);
     if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
-    if ((int)blockIdx.x >= ctas) return;
-    const long long share = quotient(total, ctas);  // the first `extra` CTAs have one unit more
-    const int extra = (int)(total - share * ctas);
-    const long long begin = share * blockIdx.x + min((int)blockIdx.x, extra);
-    if (before <= begin && begin < before + mine) {  // this thread's run holds the first unit
-        Walk<NQ> w;
-        w.x = begin;
-        w.end = begin + share + ((int)blockIdx.x < extra ? 1 : 0);
-        w.it = first;
-        long long off = begin - before;
-        for (int s = s0; off >= w.it.cost && s + 1 < a.b.n_seqs;) {
-            off -= w.it.cost;
-            w.it = item_of<NQ>(g, ++s, H);
+    if ((int)blockIdx.x * NW >= workers) return;
+    const long long share = quotient(total, workers);  // the first `extra` warps have one unit more
+    const int extra = (int)(total - share * workers);
+    const auto begin_of = [&](int worker) { return share * worker + min(worker, extra); };
+    const int me = blockIdx.x * NW + warp;
+    for (int w = 0; w < NW; ++w) {  // the thread whose run holds a range's first unit publishes the run
+        const long long x = begin_of(blockIdx.x * NW + w);
+        if (blockIdx.x * NW + w < workers && before <= x && x < before + mine) {
+            sh.warp[w].own.x = x - before;
+            sh.warp[w].own.it = first;
         }
-        w.place(off);
-        sm.own[0] = w;
     }
     __syncthreads();
-    Walk<NQ>& wk = sm.own[warp];
-    Walk<NQ>& pw = sm.ahead[warp];
+    if (lane == 0) {
+        if (me < workers) {
+            long long off = wk.x;
+            while (off >= wk.it.cost && wk.it.s + 1 < a.b.n_seqs) {
+                off -= wk.it.cost;
+                wk.it = item_of<NQ>(g, wk.it.s + 1, H);
+            }
+            wk.x = begin_of(me);
+            wk.end = begin_of(me + 1);
+            wk.place(off);
+        } else {
+            wk.n = 0;
+        }
+    }
+    __syncwarp();
     {
         constexpr int kWords = sizeof(Walk<NQ>) / 4;
         static_assert(sizeof(Walk<NQ>) % 4 == 0 && kWords <= 32);
-        int word = 0;
-        if (lane < kWords) word = reinterpret_cast<const int*>(&sm.own[0])[lane];
-        if (lane < kWords) {
-            if (warp) reinterpret_cast<int*>(&wk)[lane] = word;
-            reinterpret_cast<int*>(&pw)[lane] = word;
-        }
+        if (lane < kWords) reinterpret_cast<int*>(&pw)[lane] = reinterpret_cast<const int*>(&wk)[lane];
     }
     __syncwarp();
 
@@ -361,26 +424,24 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
         return -1;
     };
     const auto produce = [&](int slot) {
-        int off = warp + NW * pk;
-        while (pw.n > 0 && off >= pw.n) {
+        if (pk == pw.n && pk > 0) {
             __syncwarp();
             if (lane == 0) pw.next(g, H);
             __syncwarp();
             pk = 0;
-            off = warp;
         }
         if (pw.n > 0) {
-            const int tok = (pw.it.u0 + pw.u + off) * kUnit;
+            const int tok = (pw.it.u0 + pw.u + pk) * kUnit;
             if ((pk & 31) == 0) {
-                const int o = off + NW * lane, at = tok + NW * kUnit * lane;
-                pg0 = o < pw.n ? page_of(at) : -1;
-                pg1 = o < pw.n ? page_of(at + 16) : -1;
+                const int at = tok + kUnit * lane;
+                pg0 = pk + lane < pw.n ? page_of(at) : -1;
+                pg1 = pk + lane < pw.n ? page_of(at + 16) : -1;
             }
             const int p0 = __shfl_sync(~0u, pg0, pk & 31), p1 = __shfl_sync(~0u, pg1, pk & 31);
             ++pk;
             held = (held & ~(3u << (2 * slot))) | ((p0 >= 0 ? 1u : 0u) | (p1 >= 0 ? 2u : 0u)) << (2 * slot);
             constexpr int RB = D / 2, PER = 16 * RB / 512;  // bytes of a token's codes; copies a lane makes of a half
-            const uint32_t dst = smem_u32(sm.ring[warp][slot]);
+            const uint32_t dst = smem_u32(sm.ring[slot]);
             const int in_page = tok & ((1 << plog) - 1) & ~31;
             // first token of the halves; a half that is not there is filled with zeros
             const long long at0 = (((long long)max(p0, 0) * H + pw.h) << plog) + in_page;
@@ -409,10 +470,10 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
     while (wk.n > 0) {
         const bool begins = wk.u == 0, ends = wk.u + wk.n == wk.it.units;
         const int units = wk.n, unit0 = wk.it.u0 + wk.u, seen0 = wk.it.t0, seen1 = wk.it.t1;
-        load_queries<D, NQ, HAD, NW>(g, sm, wk.it, wk.h, wk.c);
-        __syncthreads();
-        float M[NV], l[NV], cq[NV];
-        float o[NP][NJ][4];
+        const bool final = wk.x + wk.n >= wk.end;  // the range's last segment
+        load_queries<D, NQ, HAD>(a, sm, wk.it, wk.h, wk.c);
+        float M[NV], l[NV], cq[NV], c_init[QT][2];
+        float o[NP][NJ][4], sums[NP][4];  // sums: of w
         int lo_max = 0, hi_min = 0x7FFFFFFF;  // tokens that all of the chunk's rows see
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -430,6 +491,13 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
             for (int j = 0; j < NJ; ++j)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o[n][j][k] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sums[n][k] = 0.0f;
+        }
+#pragma unroll
+        for (int n = 0; n < QT; ++n) {
+            c_init[n][0] = sm.init[n][2 * t];
+            c_init[n][1] = sm.init[n][2 * t + 1];
         }
         constexpr bool kHold = QT * (D / 32) <= 4;  // few enough to stay in registers
         uint4 qf[kHold ? QT : 1][kHold ? D / 32 : 1];
@@ -440,16 +508,16 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
                 for (int i = 0; i < D / 32; ++i) qf[n][i] = *reinterpret_cast<const uint4*>(sm.q[n][i][lane]);
         }
 
-        for (int off = warp; off < units; off += NW) {
+        for (int off = 0; off < units; ++off) {
             const int tok0 = (unit0 + off) * kUnit;
             copies_wait<kRingPages - 1>();
             __syncwarp();
-            const uint8_t* ring = sm.ring[warp][slot];
+            const uint8_t* ring = sm.ring[slot];
             {   // one token a lane: scales of K, log2 and inverse of V's
                 const __half* sc = reinterpret_cast<const __half*>(ring + kUnit * D);
                 const float sk = __half2float(sc[lane]), sv = fmaxf(__half2float(sc[kUnit + lane]), 0x1p-24f);
                 const bool there = (held >> (2 * slot + (lane >> 4)) & 1) && tok0 + lane < seen1 && tok0 + lane >= seen0;
-                sm.par[warp][lane] = there ? make_float4(sk, lg2(sv), __frcp_rn(sv), 0.0f)
+                sm.par[lane] = there ? make_float4(sk, lg2(sv), rcp(sv), 0.0f)
                                            : make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
             }
             __syncwarp();
@@ -463,7 +531,10 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
                     load_words(ring + (mt * 16 + hf * 8 + r8) * (D / 2) + t * (D / 8), kw[hf]);
                 float s[QT][4];
 #pragma unroll
-                for (int n = 0; n < QT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+                for (int n = 0; n < QT; ++n) {
+                    s[n][0] = s[n][2] = c_init[n][0];
+                    s[n][1] = s[n][3] = c_init[n][1];
+                }
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
                     uint32_t x[2][4];
@@ -485,7 +556,7 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
                 }
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    par[mt][hf] = sm.par[warp][mt * 16 + hf * 8 + r8];
+                    par[mt][hf] = sm.par[mt * 16 + hf * 8 + r8];
 #pragma unroll
                     for (int v = 0; v < NV; ++v) {
                         const float score = HAD ? s[v][2 * hf] + s[v][2 * hf + 1] : s[v >> 1][2 * hf + (v & 1)];
@@ -526,6 +597,7 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
                         o[v >> 1][j][v & 1] *= f;
                         o[v >> 1][j][2 + (v & 1)] *= f;
                     }
+                    sums[v >> 1][v & 1] *= f;
                 }
             }
 #pragma unroll
@@ -572,73 +644,122 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) mma(o[n][j0 + j], z[j], bw[n][0], bw[n][1]);
                 }
+                const uint32_t one[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
+#pragma unroll
+                for (int n = 0; n < NP; ++n) mma(sums[n], one, bw[n][0], bw[n][1]);
             }
             __syncwarp();  // the slot has been read
             produce(slot);
             if (++slot == kRingPages) slot = 0;
         }
 
-        // ---- the warps' states into one
+        // ---- the segment's state: finished, or left for the merge
+        const bool whole = begins && ends;
+        const int which = final || whole ? 1 : 0;  // (0 is kept for the range's first item)
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) l[v] += __shfl_xor_sync(~0u, l[v], x);
             if (r8 == 0) {
-                sm.m[warp][query_of<HAD>(v, t)] = M[v];
-                sm.l[warp][query_of<HAD>(v, t)] = l[v];
+                sm.m[which][query_of<HAD>(v, t)] = M[v];
+                sm.l[which][query_of<HAD>(v, t)] = l[v];
             }
         }
-        __syncthreads();
+        if (!whole && lane == 0) {
+            int ctas = 1;
+            if (begins) {
+                const long long last = wk.x + wk.it.units - 1, longer = (share + 1) * extra;
+                const int worker = (int)(last < longer ? quotient(last, share + 1) : extra + quotient(last - longer, share));
+                ctas = worker / NW - (int)blockIdx.x + 1;
+            }
+            sm.part[which] = Part{wk.it.lo, wk.it.nq, wk.h, wk.c, wk.it.s, 1, begins, ends, ctas};
+        }
+        const int queries = min(NQ, wk.it.nq - wk.c * NQ);
+        float* left = a.left + (long long)me * NQ * D;
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
+            __syncwarp();
 #pragma unroll
             for (int k = 0; k < 2 && 2 * n + k < NV; ++k) {
-                const int v = 2 * n + k, q = query_of<HAD>(v, t);
-                float top = sm.m[0][q];
-#pragma unroll
-                for (int w = 1; w < NW; ++w) top = fmaxf(top, sm.m[w][q]);
-                const float f = ex2(M[v] - top);
-                float* dst = sm.o[warp][q - 8 * n];
+                const int q = query_of<HAD>(2 * n + k, t);
+                float* dst = final && !whole ? sm.last[q] : sm.o[q - 8 * n];
 #pragma unroll
                 for (int j = 0; j < NJ; ++j)
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf)
-                        dst[(2 * j + hf) * 8 + r8] = f * o[n][j][2 * hf + k];
+                        dst[(2 * j + hf) * 8 + r8] = j & 1 ? __fmaf_rn(-kHigh, sums[n][k], o[n][j][2 * hf + k])
+                                                           : o[n][j][2 * hf + k];
             }
-            __syncthreads();
-            for (int q = 8 * n + warp; q < min(8 * n + S::kMQ, NQ); q += NW) {
-                const int i = wk.c * NQ + q;
-                if (i >= wk.it.nq) break;
-                float top = kLowest, sum = 0.0f, v[D / 32] = {};
+            __syncwarp();
+            if (whole || !final) {
+#pragma unroll 1
+                for (int q = 8 * n; q < min(8 * n + S::kMQ, queries); ++q) {
+                    float v[D / 32];
 #pragma unroll
-                for (int w = 0; w < NW; ++w) top = fmaxf(top, sm.m[w][q]);
+                    for (int k = 0; k < D / 32; ++k) v[k] = sm.o[q - 8 * n][lane + 32 * k];
+                    if (whole) {
+                        const int i = wk.c * NQ + q, r = i / a.G;
+                        finish_row<D, HAD>(a, wk.it.lo + r, wk.h * a.G + i - r * a.G, v, sm.m[which][q],
+                                           sm.l[which][q]);
+                    } else {
 #pragma unroll
-                for (int w = 0; w < NW; ++w) {
-                    sum = __fmaf_rn(sm.l[w][q], ex2(sm.m[w][q] - top), sum);
-#pragma unroll
-                    for (int k = 0; k < D / 32; ++k) v[k] += sm.o[w][q - 8 * n][lane + 32 * k];
-                }
-                if (begins && ends) {
-                    finish_row<D, HAD>(a, wk.it.lo + i / a.G, wk.h * a.G + i % a.G, v, top, sum);
-                } else {
-                    const long long at = (2ll * blockIdx.x + (begins ? 1 : 0)) * NQ + q;
-                    if (lane == 0) reinterpret_cast<float2*>(a.ml)[at] = make_float2(top, sum);
-#pragma unroll
-                    for (int k = 0; k < D / 32; ++k) a.part[at * D + lane + 32 * k] = v[k];
+                        for (int k = 0; k < D / 32; ++k) left[q * D + lane + 32 * k] = v[k];
+                    }
                 }
             }
-            __syncthreads();
-        }
-        if (begins && !ends && threadIdx.x == 0) {
-            // CTAs from this one to that of the item's last unit
-            const long long last = wk.x + wk.it.units - 1, bigs = (share + 1) * extra;
-            const long long cta = last < bigs ? quotient(last, (int)min(share + 1, 0x7FFFFFFFll))
-                                              : extra + quotient(last - bigs, (int)min(share, 0x7FFFFFFFll));
-            a.meta[blockIdx.x] = make_int4(wk.it.s, wk.h, wk.c * NQ, (int)(cta - blockIdx.x) + 1);
         }
         __syncwarp();
         if (lane == 0) wk.next(g, H);
         __syncwarp();
+    }
+
+    // ---- items whose parts lie at the ends of the warps' ranges
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int n = 0;
+        bool open = false;  // the last chain's item goes on
+        for (int p = 0; p < 2 * NW; ++p) {
+            const Part& x = sh.warp[p >> 1].part[p & 1];
+            if (!x.there) continue;
+            if (!open) sh.chain[n++] = p;
+            open = !x.ends;
+        }
+        sh.chain[n] = 2 * NW;
+        sh.n_chains = n;
+    }
+    __syncthreads();
+    for (int k = warp; k < sh.n_chains * NQ; k += NW) {
+        const int ch = k / NQ, q = k % NQ, p0 = sh.chain[ch], p1 = sh.chain[ch + 1];
+        const Part& x = sh.warp[p0 >> 1].part[p0 & 1];
+        const int i = x.c * NQ + q;
+        if (i >= x.nq) continue;
+        bool ends = false;
+        float top = kLowest;
+        for (int p = p0; p < p1; ++p)
+            if (sh.warp[p >> 1].part[p & 1].there) {
+                top = fmaxf(top, sh.warp[p >> 1].m[p & 1][q]);
+                ends = sh.warp[p >> 1].part[p & 1].ends;
+            }
+        float v[D / 32] = {}, total_l = 0.0f;
+        for (int p = p0; p < p1; ++p) {
+            const typename S::Warp& w = sh.warp[p >> 1];
+            if (!w.part[p & 1].there) continue;
+            const float f = ex2(w.m[p & 1][q] - top);
+            const float* src = p & 1 ? w.last[q] : a.left + ((long long)(blockIdx.x * NW + (p >> 1)) * NQ + q) * D;
+            total_l = __fmaf_rn(w.l[p & 1][q], f, total_l);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) v[c] = __fmaf_rn(src[lane + 32 * c], f, v[c]);
+        }
+        if (x.begins && ends) {
+            const int r = i / a.G;
+            finish_row<D, HAD>(a, x.lo + r, x.h * a.G + i - r * a.G, v, top, total_l);
+            continue;
+        }
+        const long long at = (2ll * blockIdx.x + (x.begins ? 1 : 0)) * NQ + q;
+        if (lane == 0) reinterpret_cast<float2*>(a.ml)[at] = make_float2(top, total_l);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) a.part[at * D + lane + 32 * c] = v[c];
+        if (x.begins && q == 0 && lane == 0) a.meta[blockIdx.x] = make_int4(x.s, x.h, x.c * NQ, x.ctas);
     }
 }
 
