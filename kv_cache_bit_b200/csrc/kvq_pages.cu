@@ -196,9 +196,10 @@ struct StepShape {
 };
 
 struct AttnWorkspace {
-    size_t meta, ml, part, left, bytes;
+    size_t meta, ml, part, left, frag, scal, bytes;
 };
-AttnWorkspace attn_workspace(int sms, int d) {
+// queries: rows (or places) times query heads
+AttnWorkspace attn_workspace(int sms, int d, bool had, long long prepared) {
     size_t ctas = 0, queries = 0, warps = 0;  // the most of any shape: CTAs, and query rows over all CTAs and warps
     const auto take = [&](int per_sm, int nw, int nq) {
         const size_t n = size_t(sms) * per_sm;
@@ -213,30 +214,35 @@ AttnWorkspace attn_workspace(int sms, int d) {
     w.ml = ctas * 16;
     w.part = w.ml + 2 * queries * 8;
     w.left = w.part + 2 * queries * d * 4;
-    w.bytes = w.left + warps * d * 4;
+    w.frag = w.left + warps * d * 4;
+    w.scal = w.frag + size_t(prepared) * d * (had ? 4 : 2);
+    w.bytes = w.scal + size_t(prepared) * 16;
     return w;
 }
 
 template <int D, int NQ, bool HAD>
-kvq_status launch_step(StepArgs g, int sms, cudaStream_t st) {
+kvq_status launch_step(const StepArgs& g, long long places, int sms, cudaStream_t st) {
     using Sh = StepShape<NQ>;
     constexpr int smem = (int)sizeof(StepSmem<D, NQ, HAD, Sh::kWarps>);
     static_assert(smem * Sh::kPerSm + Sh::kPerSm * 1024 <= 228 * 1024, "shared memory of the CTAs on one SM");
     constexpr auto kernel = pages_step_kernel<D, NQ, HAD, Sh::kWarps, Sh::kPerSm>;
     if (!allow_smem<kernel>(smem)) return KVQ_ERR_CUDA;
     const int grid = sms * Sh::kPerSm;
-    kvq_status s = launch<StepArgs>(kernel, g, dim3(grid), Sh::kWarps * 32, smem, st);
+    const unsigned query_ctas = (unsigned)((places * g.a.Hq + kQueryWarps - 1) / kQueryWarps);
+    kvq_status s = launch<StepArgs>(pages_queries_kernel<D, HAD>, g, dim3(query_ctas), kQueryWarps * 32, 0, st);
+    if (s != KVQ_OK) return s;
+    s = launch<StepArgs>(kernel, g, dim3(grid), Sh::kWarps * 32, smem, st);
     if (s != KVQ_OK) return s;
     return launch<AttnArgs>(pages_merge_kernel<D, NQ, HAD>, g.a, dim3(grid), kMergeWarps * 32, 0, st);
 }
 
 template <int D, bool HAD>
-kvq_status launch_attn(const StepArgs& g, long long queries, int sms, cudaStream_t st) {
+kvq_status launch_attn(const StepArgs& g, long long places, long long queries, int sms, cudaStream_t st) {
     if constexpr (HAD) {
-        if (queries <= 4) return launch_step<D, 4, HAD>(g, sms, st);
+        if (queries <= 4) return launch_step<D, 4, HAD>(g, places, sms, st);
     }
-    if (queries <= 8) return launch_step<D, 8, HAD>(g, sms, st);
-    return launch_step<D, 16, HAD>(g, sms, st);
+    if (queries <= 8) return launch_step<D, 8, HAD>(g, places, sms, st);
+    return launch_step<D, 16, HAD>(g, places, sms, st);
 }
 
 kvq_status check_attention(const kvq_config* cfg, const kvq_pages* p, const kvq_batch* b, int64_t rows, int q_heads) {
@@ -320,7 +326,7 @@ kvq_status kvq_pages_read(const kvq_config* cfg, const kvq_pages* pages, const k
 size_t kvq_pages_attention_workspace_bytes(const kvq_config* cfg, const kvq_pages* pages, const kvq_batch* batch,
                                            int64_t rows, int32_t q_heads) {
     if (check_attention(cfg, pages, batch, rows, q_heads) != KVQ_OK) return 0;
-    return attn_workspace(sm_count(), cfg->head_dim).bytes;
+    return attn_workspace(sm_count(), cfg->head_dim, cfg->flags == KVQ_HADAMARD, rows * q_heads).bytes;
 }
 
 kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, const kvq_batch* batch,
@@ -344,7 +350,9 @@ kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, co
     const size_t need = kvq_pages_attention_workspace_bytes(cfg, pages, batch, rows, q_heads);
     if (!ok_ptr(ws) || ws_bytes < need) return KVQ_ERR_WORKSPACE;
     const int sms = sm_count();
-    const AttnWorkspace w = attn_workspace(sms, d);
+    const bool had = cfg->flags == KVQ_HADAMARD;
+    const long long places = rows;
+    const AttnWorkspace w = attn_workspace(sms, d, had, places * q_heads);
     uint8_t* base = static_cast<uint8_t*>(ws);
     StepArgs g;
     AttnArgs& a = g.a;
@@ -371,11 +379,13 @@ kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, co
     a.part = reinterpret_cast<float*>(base + w.part);
     a.left = reinterpret_cast<float*>(base + w.left);
     g.many = 0;
+    g.stretch = 0;
+    g.frag = reinterpret_cast<__half*>(base + w.frag);
+    g.scal = reinterpret_cast<float4*>(base + w.scal);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const long long queries = (long long)a.G * (batch->max_rows > 0 ? batch->max_rows : 1);
-    const bool had = cfg->flags == KVQ_HADAMARD;
-    if (d == 64) return had ? launch_attn<64, true>(g, queries, sms, st) : launch_attn<64, false>(g, queries, sms, st);
-    return had ? launch_attn<128, true>(g, queries, sms, st) : launch_attn<128, false>(g, queries, sms, st);
+    if (d == 64) return had ? launch_attn<64, true>(g, places, queries, sms, st) : launch_attn<64, false>(g, places, queries, sms, st);
+    return had ? launch_attn<128, true>(g, places, queries, sms, st) : launch_attn<128, false>(g, places, queries, sms, st);
 }
 
 kvq_status kvq_pages_read_errors(uint32_t* host_out, int32_t clear) {

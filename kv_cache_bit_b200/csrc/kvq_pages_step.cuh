@@ -6,8 +6,10 @@
 // cost is the number of 32-token units that the sequence's rows see.  All
 // items laid end to end are cut into equal ranges, one a warp of a single-wave
 // grid, whatever the lengths are: one long sequence is spread over the whole
-// GPU, many short ones share warps.  A warp works alone -- its own queries,
-// its own ring in shared memory, filled by cp.async that runs ahead over item
+// GPU, many short ones share warps.  pages_queries_kernel has rotated, scaled
+// and split the queries once, in the order of the tensor core's fragments; it
+// runs while this kernel looks for its ranges.  A warp works alone -- its own
+// ring in shared memory is filled by cp.async that runs ahead over item
 // borders -- and finishes the items that lie whole in its range.  What is left
 // of items at the ends of the ranges is merged per CTA once all its warps are
 // done, and what goes past a CTA by pages_merge_kernel.  (With ranges a CTA
@@ -48,8 +50,17 @@ constexpr int slot_bytes() { return kUnit * (D + 4); }  // K codes, V codes, K s
 
 struct StepArgs {
     AttnArgs a;
-    int many;       // sequences of more query rows a kv head than this are not this kernel's (0: all are)
+    int many;  // sequences of more query rows a kv head than this are not this kernel's (0: all are)
+    // Prepared queries: fragments [place][head][part][D] and per query the factor of its scores and what
+    // the parts' accumulators start from.  A row's place is its number, or, with `many`, its number in its
+    // sequence behind a stretch of `stretch` places a sequence.
+    __half* frag;
+    float4* scal;
+    int stretch;
 };
+__device__ __forceinline__ long long place_of(const StepArgs& g, int s, int lo, int r) {
+    return g.many > 0 ? (long long)s * g.stretch + r : (long long)lo + r;
+}
 
 // A sequence's share of the work.
 struct Item {
@@ -156,16 +167,12 @@ struct StepSmem {
             float o[kMQ][kStride];
         };
         alignas(16) float4 par[kUnit];  // a token's K scale, log2 and inverse of its V scale
-        float init[kQT][8];  // what the score accumulators start from: -kHigh times the sum of those channels
-        float cq[NQ];
-        int t0[NQ], t1[NQ];
         float m[2][NQ], l[2][NQ];
         Walk<NQ> own, ahead;  // the place in the work: what is computed, what is fetched
         Part part[2];         // of the range's first item and of its last
     };
     Warp warp[NW];
     long long sums[NW];
-    int chain[NW + 2], n_chains;  // first part (2 warp + which) of each item that has parts; the end
 };
 
 __device__ __forceinline__ float max_or_nan(float x, float y) { return x != x || y <= x ? x : y; }
@@ -227,113 +234,97 @@ __device__ __forceinline__ int query_of(int v, int t) {
     return HAD ? 4 * v + t : 8 * (v >> 1) + 2 * t + (v & 1);
 }
 
-// Loads, rotates, scales and splits the queries of chunk c into the warp's B
-// fragments.  A lane holds D / 32 neighbouring channels of a query.
-template <int D, int NQ, bool HAD, typename W>
-__device__ __forceinline__ void load_queries(const AttnArgs& a, W& sm, const Item& it, int h, int c) {
+// Loads, rotates, scales and splits the queries: a warp each, D / 32
+// neighbouring channels a lane.
+constexpr int kQueryWarps = 8;
+
+template <int D, bool HAD>
+__global__ void __launch_bounds__(kQueryWarps * 32) pages_queries_kernel(StepArgs g) {
     constexpr int N = D / 32, C = D / 4;  // channels a lane; channels a fragment lane
+    const AttnArgs& a = g.a;
     const int lane = threadIdx.x & 31;
-    float sg[N];
+    const long long at = (long long)blockIdx.x * kQueryWarps + (threadIdx.x >> 5);
+    const long long place = at / a.Hq;
+    const int head = (int)(at - place * a.Hq);
+    grid_dep_wait();
+    grid_dep_launch();
+    long long row = place;
+    if (g.many > 0) {
+        const int s = (int)(place / g.stretch);
+        if (s >= a.b.n_seqs) return;
+        const int lo = max(a.b.start[s], 0), hi = min(a.b.start[s + 1], a.rows);
+        row = lo + (place - (long long)s * g.stretch);
+        if (row >= hi || (long long)(hi - lo) * a.G > g.many) return;
+    }
+    if (row >= a.rows) return;
+    const uint16_t* src = static_cast<const uint16_t*>(a.q) + row * a.q_row + head * a.q_head + lane * N;
+    uint32_t u[N / 2];
+    load_words(reinterpret_cast<const uint8_t*>(src), u);
+    float v[N];
 #pragma unroll
-    for (int k = 0; k < N; ++k) sg[k] = 1.0f;
-    if (HAD && a.signs) {
-        if constexpr (N == 4) {
-            const char4 x = reinterpret_cast<const char4*>(a.signs)[lane];
-            sg[0] = x.x, sg[1] = x.y, sg[2] = x.z, sg[3] = x.w;
-        } else {
-            const char2 x = reinterpret_cast<const char2*>(a.signs)[lane];
-            sg[0] = x.x, sg[1] = x.y;
+    for (int k = 0; k < N / 2; ++k) {
+        const float2 f = a.bf16 ? Elem<__nv_bfloat16>::wide(u[k]) : Elem<__half>::wide(u[k]);
+        v[2 * k] = f.x, v[2 * k + 1] = f.y;
+    }
+    if constexpr (HAD) {
+        if (a.signs) {
+            if constexpr (N == 4) {
+                const char4 x = reinterpret_cast<const char4*>(a.signs)[lane];
+                v[0] *= x.x, v[1] *= x.y, v[2] *= x.z, v[3] *= x.w;
+            } else {
+                const char2 x = reinterpret_cast<const char2*>(a.signs)[lane];
+                v[0] *= x.x, v[1] *= x.y;
+            }
+        }
+        lane_stages<1, N>(v);
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const float flip = (lane & x) ? -1.0f : 1.0f;
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] = __fmaf_rn(v[k], flip, __shfl_xor_sync(~0u, v[k], x));
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] *= a.rsqd;
+    }
+    float m = 0.0f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) m = max_or_nan(m, fabsf(v[k]));
+#pragma unroll
+    for (int x = 16; x; x >>= 1) m = max_or_nan(m, __shfl_xor_sync(~0u, m, x));
+    const float f = m > 0.0f || m != m ? query_scale(m) : 1.0f;
+    float sum[2] = {0.0f, 0.0f};  // of the channels whose codes come with kHigh
+    __half* dst = g.frag + at * (HAD ? 2 : 1) * D;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        // fragment lane t holds channels C t .. ; of eight of them, channel c8 is half c8 / 4 of word
+        // (tile's nibble parity, register)
+        const int ch = lane * N + k, t = ch / C, i8 = (ch % C) >> 3, c8 = ch & 7;
+        const int place8 = (i8 * 4 + t) * 8 + ((c8 & 1) * 2 + ((c8 >> 1) & 1)) * 2 + (c8 >> 2);
+        const float x = v[k] * f;
+        const __half hi = __float2half_rn(x);
+        dst[place8] = hi;
+        if (k & 1) sum[0] += __half2float(hi);
+        if constexpr (HAD) {
+            const __half lo = __float2half_rn(x - __half2float(hi));
+            dst[D + place8] = lo;
+            if (k & 1) sum[1] += __half2float(lo);
         }
     }
-#pragma unroll 1
-    for (int q4 = 0; q4 < NQ; q4 += 4) {
-        uint32_t u[4][N / 2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int i = c * NQ + q4 + j;
-#pragma unroll
-            for (int k = 0; k < N / 2; ++k) u[j][k] = 0;
-            if (i < it.nq) {
-                const int r = i / a.G;
-                const uint16_t* src = static_cast<const uint16_t*>(a.q) + (it.lo + r) * a.q_row +
-                                      (h * a.G + i - r * a.G) * a.q_head + lane * N;
-                if constexpr (N == 4) {
-                    const uint2 w = *reinterpret_cast<const uint2*>(src);
-                    u[j][0] = w.x, u[j][1] = w.y;
-                } else {
-                    u[j][0] = *reinterpret_cast<const uint32_t*>(src);
-                }
-            }
-        }
-        if (lane < 4) {
-            const int i = c * NQ + q4 + lane;
-            Range r{0, 0};
-            if (i < it.nq) {
-                const long long pos = (long long)it.base + it.lo + i / a.G;
-                const long long hi = min(a.causal ? pos + 1 : (long long)it.len, (long long)it.t1);
-                const long long lo = a.causal && a.window > 0 ? max(pos - a.window + 1, 0ll) : 0;
-                if (lo < hi) r = Range{(int)lo, (int)hi};
-            }
-            sm.t0[q4 + lane] = r.t0;
-            sm.t1[q4 + lane] = r.t1;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int qi = q4 + j;
-            float v[N];
-#pragma unroll
-            for (int k = 0; k < N / 2; ++k) {
-                const float2 f = a.bf16 ? Elem<__nv_bfloat16>::wide(u[j][k]) : Elem<__half>::wide(u[j][k]);
-                v[2 * k] = f.x, v[2 * k + 1] = f.y;
-            }
-            if constexpr (HAD) {
-#pragma unroll
-                for (int k = 0; k < N; ++k) v[k] *= sg[k];
-                lane_stages<1, N>(v);
-#pragma unroll
-                for (int x = 1; x < 32; x <<= 1) {
-                    const float flip = (lane & x) ? -1.0f : 1.0f;
-#pragma unroll
-                    for (int k = 0; k < N; ++k) v[k] = __fmaf_rn(v[k], flip, __shfl_xor_sync(~0u, v[k], x));
-                }
-#pragma unroll
-                for (int k = 0; k < N; ++k) v[k] *= a.rsqd;
-            }
-            float m = 0.0f;
-#pragma unroll
-            for (int k = 0; k < N; ++k) m = max_or_nan(m, fabsf(v[k]));
-#pragma unroll
-            for (int x = 16; x; x >>= 1) m = max_or_nan(m, __shfl_xor_sync(~0u, m, x));
-            const float f = m > 0.0f || m != m ? query_scale(m) : 1.0f;
-            const int tile = HAD ? qi >> 2 : qi >> 3, col = HAD ? 2 * (qi & 3) : qi & 7;
-            float sum[2] = {0.0f, 0.0f};  // of the channels whose codes come with kHigh
-#pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const int ch = lane * N + k, t = ch / C, i8 = (ch % C) >> 3, cc = ch & 7;
-                const float x = v[k] * f;
-                const int word = (cc & 1) * 2 + ((cc >> 1) & 1);
-                const __half hi = __float2half_rn(x);
-                reinterpret_cast<__half*>(&sm.q[tile][i8][col * 4 + t][word])[cc >> 2] = hi;
-                if (k & 1) sum[0] += __half2float(hi);
-                if constexpr (HAD) {
-                    const __half lo = __float2half_rn(x - __half2float(hi));
-                    reinterpret_cast<__half*>(&sm.q[tile][i8][(col + 1) * 4 + t][word])[cc >> 2] = lo;
-                    if (k & 1) sum[1] += __half2float(lo);
-                }
-            }
-#pragma unroll
-            for (int x = 16; x; x >>= 1) {
-                sum[0] += __shfl_xor_sync(~0u, sum[0], x);
-                if constexpr (HAD) sum[1] += __shfl_xor_sync(~0u, sum[1], x);
-            }
-            if (lane == 0) {
-                sm.init[tile][col] = -kHigh * sum[0];
-                if constexpr (HAD) sm.init[tile][col + 1] = -kHigh * sum[1];
-                sm.cq[qi] = a.scale2 / f;
-            }
-        }
+    for (int x = 16; x; x >>= 1) {
+        sum[0] += __shfl_xor_sync(~0u, sum[0], x);
+        if constexpr (HAD) sum[1] += __shfl_xor_sync(~0u, sum[1], x);
     }
-    __syncwarp();
+    if (lane == 0) g.scal[at] = make_float4(a.scale2 / f, -kHigh * sum[0], -kHigh * sum[1], 0.0f);
+}
+
+// Tokens that query i of an item sees.
+__device__ __forceinline__ Range query_range(const AttnArgs& a, const Item& it, int i) {
+    if (i >= it.nq) return Range{0, 0};
+    const long long pos = (long long)it.base + it.lo + i / a.G;
+    const long long hi = min(a.causal ? pos + 1 : (long long)it.len, (long long)it.t1);
+    const long long lo = a.causal && a.window > 0 ? max(pos - a.window + 1, 0ll) : 0;
+    return lo < hi ? Range{(int)lo, (int)hi} : Range{0, 0};
 }
 
 template <int D, int NQ, bool HAD, int NW, int PER_SM>
@@ -349,8 +340,9 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
     Walk<NQ>&wk = sm.own, &pw = sm.ahead;
 
     if (lane < 2) sm.part[lane].there = 0;
-    grid_dep_wait();
     grid_dep_launch();
+    // pages_queries_kernel let this kernel start once all before it was done; what it writes itself is
+    // waited for below
 
     // ---- the warps' ranges: prefix sums of the sequences' costs, a run of `per` sequences a thread
     const int per = (a.b.n_seqs + NW * 32 - 1) / (NW * 32), s0 = threadIdx.x * per;
@@ -376,7 +368,10 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
     }
     const int workers = (int)min((long long)gridDim.x * NW, total);
     if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
-    if ((int)blockIdx.x * NW >= workers) return;
+    if ((int)blockIdx.x * NW >= workers) {
+        grid_dep_wait();  // this grid's end stands for that of the kernels before it
+        return;
+    }
     const long long share = quotient(total, workers);  // the first `extra` warps have one unit more
     const int extra = (int)(total - share * workers);
     const auto begin_of = [&](int worker) { return share * worker + min(worker, extra); };
@@ -463,6 +458,7 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
         copies_commit();
     };
     for (int i = 0; i < kRingPages; ++i) produce(i);
+    grid_dep_wait();
 
     int slot = 0;
 
@@ -471,7 +467,6 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
         const bool begins = wk.u == 0, ends = wk.u + wk.n == wk.it.units;
         const int units = wk.n, unit0 = wk.it.u0 + wk.u, seen0 = wk.it.t0, seen1 = wk.it.t1;
         const bool final = wk.x + wk.n >= wk.end;  // the range's last segment
-        load_queries<D, NQ, HAD>(a, sm, wk.it, wk.h, wk.c);
         float M[NV], l[NV], cq[NV], c_init[QT][2];
         float o[NP][NJ][4], sums[NP][4];  // sums: of w
         int lo_max = 0, hi_min = 0x7FFFFFFF;  // tokens that all of the chunk's rows see
@@ -479,12 +474,20 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
         for (int v = 0; v < NV; ++v) {
             M[v] = kLowest;
             l[v] = 0.0f;
-            cq[v] = sm.cq[query_of<HAD>(v, t)];
+            const int i = wk.c * NQ + query_of<HAD>(v, t), r = i / a.G;
+            float4 sc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (i < wk.it.nq) {
+                sc = g.scal[place_of(g, wk.it.s, wk.it.lo, r) * a.Hq + wk.h * a.G + i - r * a.G];
+                const Range see = query_range(a, wk.it, i);
+                lo_max = max(lo_max, see.t0);
+                hi_min = min(hi_min, see.t1);
+            }
+            cq[v] = sc.x;
+            if constexpr (HAD) c_init[v][0] = sc.y, c_init[v][1] = sc.z;
+            else c_init[v >> 1][v & 1] = sc.y;
         }
-        for (int i = 0; i < min(NQ, wk.it.nq - wk.c * NQ); ++i) {
-            lo_max = max(lo_max, sm.t0[i]);
-            hi_min = min(hi_min, sm.t1[i]);
-        }
+        lo_max = __reduce_max_sync(~0u, lo_max);
+        hi_min = __reduce_min_sync(~0u, hi_min);
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
 #pragma unroll
@@ -494,19 +497,25 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
 #pragma unroll
             for (int k = 0; k < 4; ++k) sums[n][k] = 0.0f;
         }
-#pragma unroll
-        for (int n = 0; n < QT; ++n) {
-            c_init[n][0] = sm.init[n][2 * t];
-            c_init[n][1] = sm.init[n][2 * t + 1];
-        }
-        constexpr bool kHold = QT * (D / 32) <= 4;  // few enough to stay in registers
+        constexpr bool kHold = QT * (D / 32) <= 4;  // few enough fragments to stay in registers
         uint4 qf[kHold ? QT : 1][kHold ? D / 32 : 1];
-        if constexpr (kHold) {
 #pragma unroll
-            for (int n = 0; n < QT; ++n)
+        for (int n = 0; n < QT; ++n) {  // column r8 of tile n
+            const int i = wk.c * NQ + (HAD ? 4 * n + (r8 >> 1) : 8 * n + r8), r = i / a.G;
+            uint4 w[D / 32] = {};
+            if (i < wk.it.nq) {
+                const long long at = place_of(g, wk.it.s, wk.it.lo, r) * a.Hq + wk.h * a.G + i - r * a.G;
+                const uint4* src = reinterpret_cast<const uint4*>(g.frag + (HAD ? 2 * at + (r8 & 1) : at) * D) + t;
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) qf[n][i] = *reinterpret_cast<const uint4*>(sm.q[n][i][lane]);
+                for (int k = 0; k < D / 32; ++k) w[k] = src[4 * k];
+            }
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                if constexpr (kHold) qf[n][k] = w[k];
+                else *reinterpret_cast<uint4*>(sm.q[n][k][lane]) = w[k];
+            }
         }
+        __syncwarp();
 
         for (int off = 0; off < units; ++off) {
             const int tok0 = (unit0 + off) * kUnit;
@@ -567,13 +576,13 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
             if (tok0 < lo_max || tok0 + kUnit > hi_min) {
 #pragma unroll
                 for (int v = 0; v < NV; ++v) {
-                    const int q0 = sm.t0[query_of<HAD>(v, t)], q1 = sm.t1[query_of<HAD>(v, t)];
+                    const Range see = query_range(a, wk.it, wk.c * NQ + query_of<HAD>(v, t));
 #pragma unroll
                     for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {
                             const int tok = tok0 + mt * 16 + hf * 8 + r8;
-                            if (tok < q0 || tok >= q1) y[mt][v][hf] = -INFINITY;
+                            if (tok < see.t0 || tok >= see.t1) y[mt][v][hf] = -INFINITY;
                         }
                 }
             }
@@ -713,53 +722,51 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
         __syncwarp();
     }
 
-    // ---- items whose parts lie at the ends of the warps' ranges
+    // ---- items whose parts lie at the ends of the warps' ranges: part 2 warp + which, in order
     __syncthreads();
-    if (threadIdx.x == 0) {
-        int n = 0;
-        bool open = false;  // the last chain's item goes on
-        for (int p = 0; p < 2 * NW; ++p) {
-            const Part& x = sh.warp[p >> 1].part[p & 1];
-            if (!x.there) continue;
-            if (!open) sh.chain[n++] = p;
-            open = !x.ends;
-        }
-        sh.chain[n] = 2 * NW;
-        sh.n_chains = n;
-    }
-    __syncthreads();
-    for (int k = warp; k < sh.n_chains * NQ; k += NW) {
-        const int ch = k / NQ, q = k % NQ, p0 = sh.chain[ch], p1 = sh.chain[ch + 1];
+    const Part& mine_p = sh.warp[min(lane >> 1, NW - 1)].part[lane & 1];
+    const bool there = lane < 2 * NW && mine_p.there;
+    const uint32_t all = __ballot_sync(~0u, there), closed = __ballot_sync(~0u, there && mine_p.ends);
+    int ch = 0;
+    for (uint32_t rest = all; rest;) {
+        // the first part's item goes on to the first part that ends it
+        const uint32_t close = closed & rest;
+        const uint32_t set = close ? rest & ((close & (0u - close)) * 2 - 1) : rest;
+        const int p0 = __ffs(set) - 1;
+        const bool ends = close != 0;
+        rest &= ~set;
         const Part& x = sh.warp[p0 >> 1].part[p0 & 1];
-        const int i = x.c * NQ + q;
-        if (i >= x.nq) continue;
-        bool ends = false;
-        float top = kLowest;
-        for (int p = p0; p < p1; ++p)
-            if (sh.warp[p >> 1].part[p & 1].there) {
-                top = fmaxf(top, sh.warp[p >> 1].m[p & 1][q]);
-                ends = sh.warp[p >> 1].part[p & 1].ends;
+        const int queries = min(NQ, x.nq - x.c * NQ);
+        for (int q = (warp + NW - ch++ % NW) % NW; q < queries; q += NW) {  // (items begin with different warps)
+            const bool in = set >> lane & 1;
+            const float m = in ? sh.warp[lane >> 1].m[lane & 1][q] : kLowest;
+            float top = m;
+#pragma unroll
+            for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, k));
+            const float f = ex2(m - top);
+            float sum_l = in ? sh.warp[lane >> 1].l[lane & 1][q] * f : 0.0f;
+#pragma unroll
+            for (int k = 16; k; k >>= 1) sum_l += __shfl_xor_sync(~0u, sum_l, k);
+            float v[D / 32] = {};
+            for (uint32_t parts = set; parts; parts &= parts - 1) {
+                const int p = __ffs(parts) - 1;
+                const float fp = __shfl_sync(~0u, f, p);
+                const float* src = p & 1 ? sh.warp[p >> 1].last[q]
+                                         : a.left + ((long long)(blockIdx.x * NW + (p >> 1)) * NQ + q) * D;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) v[c] = __fmaf_rn(src[lane + 32 * c], fp, v[c]);
             }
-        float v[D / 32] = {}, total_l = 0.0f;
-        for (int p = p0; p < p1; ++p) {
-            const typename S::Warp& w = sh.warp[p >> 1];
-            if (!w.part[p & 1].there) continue;
-            const float f = ex2(w.m[p & 1][q] - top);
-            const float* src = p & 1 ? w.last[q] : a.left + ((long long)(blockIdx.x * NW + (p >> 1)) * NQ + q) * D;
-            total_l = __fmaf_rn(w.l[p & 1][q], f, total_l);
+            if (x.begins && ends) {
+                const int i = x.c * NQ + q, r = i / a.G;
+                finish_row<D, HAD>(a, x.lo + r, x.h * a.G + i - r * a.G, v, top, sum_l);
+                continue;
+            }
+            const long long at = (2ll * blockIdx.x + (x.begins ? 1 : 0)) * NQ + q;
+            if (lane == 0) reinterpret_cast<float2*>(a.ml)[at] = make_float2(top, sum_l);
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) v[c] = __fmaf_rn(src[lane + 32 * c], f, v[c]);
+            for (int c = 0; c < D / 32; ++c) a.part[at * D + lane + 32 * c] = v[c];
+            if (x.begins && q == 0 && lane == 0) a.meta[blockIdx.x] = make_int4(x.s, x.h, x.c * NQ, x.ctas);
         }
-        if (x.begins && ends) {
-            const int r = i / a.G;
-            finish_row<D, HAD>(a, x.lo + r, x.h * a.G + i - r * a.G, v, top, total_l);
-            continue;
-        }
-        const long long at = (2ll * blockIdx.x + (x.begins ? 1 : 0)) * NQ + q;
-        if (lane == 0) reinterpret_cast<float2*>(a.ml)[at] = make_float2(top, total_l);
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) a.part[at * D + lane + 32 * c] = v[c];
-        if (x.begins && q == 0 && lane == 0) a.meta[blockIdx.x] = make_int4(x.s, x.h, x.c * NQ, x.ctas);
     }
 }
 
