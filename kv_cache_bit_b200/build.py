@@ -17,7 +17,7 @@ NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 # translation unit -> the headers of csrc/ that only it includes
 UNITS = {"kvq_api.cu": ("kvq_decode_mma.cuh", "kvq_decode_simple.cuh", "kvq_quant.cuh", "kvq_quant_rows.cuh"),
-         "kvq_pages.cu": ("kvq_pages.cuh", "kvq_pages_attn.cuh", "kvq_pages_step.cuh")}
+         "kvq_pages.cu": ("kvq_pages.cuh", "kvq_pages_attn.cuh", "kvq_pages_step.cuh", "kvq_pages_tile.cuh")}
 
 
 def sources():

@@ -14,6 +14,7 @@
 #include "kvq_pages.cuh"
 #include "kvq_pages_attn.cuh"
 #include "kvq_pages_step.cuh"
+#include "kvq_pages_tile.cuh"
 
 namespace kvq {
 namespace {
@@ -134,8 +135,8 @@ struct ReadLaunch {
 
 // Launch as a programmatic dependent of the kernel ahead of it in the stream:
 // the kernels wait for that one (grid_dep_wait) before they read anything.
-template <typename A>
-kvq_status launch(void (*kernel)(A), const A& args, dim3 grid, int threads, int smem, cudaStream_t st) {
+template <typename... A>
+kvq_status launch(void (*kernel)(A...), dim3 grid, int threads, int smem, cudaStream_t st, const A&... args) {
     cudaLaunchConfig_t c = {};
     c.gridDim = grid;
     c.blockDim = dim3(threads);
@@ -146,7 +147,7 @@ kvq_status launch(void (*kernel)(A), const A& args, dim3 grid, int threads, int 
     at[0].val.programmaticStreamSerializationAllowed = 1;
     c.attrs = at;
     c.numAttrs = 1;
-    if (cudaLaunchKernelEx(&c, kernel, args) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&c, kernel, args...) != cudaSuccess) {
         cudaGetLastError();
         return KVQ_ERR_CUDA;
     }
@@ -195,54 +196,108 @@ struct StepShape {
     static constexpr int kWarps = NQ == 16 ? 4 : 8, kPerSm = NQ == 16 ? 3 : 2;
 };
 
-struct AttnWorkspace {
-    size_t meta, ml, part, left, frag, scal, bytes;
+// Sequences of more query rows a kv head than this go to the tile kernel.
+constexpr int kMany = 32;
+
+// Which kernels a call needs, from what the host knows of it.
+struct AttnPlan {
+    bool tiles;        // some sequence may have more than kMany query rows a kv head
+    int stretch;       // with tiles: rows of a sequence that has not
+    long long places;  // rows that the step kernel's queries are prepared for
+    long long queries; // query rows a kv head of the sequences that are the step kernel's
 };
-// queries: rows (or places) times query heads
-AttnWorkspace attn_workspace(int sms, int d, bool had, long long prepared) {
+AttnPlan attn_plan(const kvq_batch* b, long long rows, int G) {
+    AttnPlan p;
+    const long long most = (long long)G * b->max_rows;
+    p.tiles = b->max_rows == 0 || most > kMany;
+    p.stretch = p.tiles ? kMany / G : 0;
+    p.places = p.tiles ? (long long)b->n_seqs * p.stretch : rows;
+    p.queries = p.tiles ? G : most;
+    return p;
+}
+
+struct AttnWorkspace {
+    size_t meta, ml, part, left, frag, scal;                 // step kernel
+    size_t tile_meta, tile_ml, tile_part, plan, seq_cost;    // tile kernel
+    size_t bytes;
+};
+AttnWorkspace attn_workspace(const AttnPlan& p, int sms, int d, bool had, int q_heads, int n_seqs) {
     size_t ctas = 0, queries = 0, warps = 0;  // the most of any shape: CTAs, and query rows over all CTAs and warps
-    const auto take = [&](int per_sm, int nw, int nq) {
+    const auto shape = [&](int per_sm, int nw, int nq) {
         const size_t n = size_t(sms) * per_sm;
         if (n > ctas) ctas = n;
         if (n * nq > queries) queries = n * nq;
         if (n * nq * nw > warps) warps = n * nq * nw;
     };
-    take(StepShape<8>::kPerSm, StepShape<8>::kWarps, 8);
-    take(StepShape<16>::kPerSm, StepShape<16>::kWarps, 16);
+    shape(StepShape<8>::kPerSm, StepShape<8>::kWarps, 8);
+    shape(StepShape<16>::kPerSm, StepShape<16>::kWarps, 16);
     AttnWorkspace w;
-    w.meta = 0;
-    w.ml = ctas * 16;
-    w.part = w.ml + 2 * queries * 8;
-    w.left = w.part + 2 * queries * d * 4;
-    w.frag = w.left + warps * d * 4;
-    w.scal = w.frag + size_t(prepared) * d * (had ? 4 : 2);
-    w.bytes = w.scal + size_t(prepared) * 16;
+    size_t at = 0;
+    const auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    w.meta = take(ctas * 16);
+    w.ml = take(2 * queries * 8);
+    w.part = take(2 * queries * d * 4);
+    w.left = take(warps * d * 4);
+    w.frag = take(size_t(p.places) * q_heads * d * (had ? 4 : 2));
+    w.scal = take(size_t(p.places) * q_heads * 16);
+    const size_t tiles = p.tiles ? size_t(sms) : 0;
+    w.tile_meta = take(tiles * 16);
+    w.tile_ml = take(2 * tiles * kMaxItemRows * 8);
+    w.tile_part = take(2 * tiles * kMaxItemRows * d * 4);
+    w.plan = take(tiles * 16);
+    w.seq_cost = take(p.tiles ? (size_t(n_seqs) + 1) * 8 : 0);
+    w.bytes = at;
     return w;
 }
 
 template <int D, int NQ, bool HAD>
-kvq_status launch_step(const StepArgs& g, long long places, int sms, cudaStream_t st) {
+kvq_status launch_step(StepArgs g, int sms, cudaStream_t st) {
     using Sh = StepShape<NQ>;
     constexpr int smem = (int)sizeof(StepSmem<D, NQ, HAD, Sh::kWarps>);
     static_assert(smem * Sh::kPerSm + Sh::kPerSm * 1024 <= 228 * 1024, "shared memory of the CTAs on one SM");
     constexpr auto kernel = pages_step_kernel<D, NQ, HAD, Sh::kWarps, Sh::kPerSm>;
     if (!allow_smem<kernel>(smem)) return KVQ_ERR_CUDA;
+    g.a.item_rows = NQ;
     const int grid = sms * Sh::kPerSm;
-    const unsigned query_ctas = (unsigned)((places * g.a.Hq + kQueryWarps - 1) / kQueryWarps);
-    kvq_status s = launch<StepArgs>(pages_queries_kernel<D, HAD>, g, dim3(query_ctas), kQueryWarps * 32, 0, st);
+    const kvq_status s = launch(kernel, dim3(grid), Sh::kWarps * 32, smem, st, g);
     if (s != KVQ_OK) return s;
-    s = launch<StepArgs>(kernel, g, dim3(grid), Sh::kWarps * 32, smem, st);
-    if (s != KVQ_OK) return s;
-    return launch<AttnArgs>(pages_merge_kernel<D, NQ, HAD>, g.a, dim3(grid), kMergeWarps * 32, 0, st);
+    return launch(pages_merge_kernel<D, NQ, HAD>, dim3(grid), kMergeWarps * 32, 0, st, g.a);
 }
 
 template <int D, bool HAD>
-kvq_status launch_attn(const StepArgs& g, long long places, long long queries, int sms, cudaStream_t st) {
-    if constexpr (HAD) {
-        if (queries <= 4) return launch_step<D, 4, HAD>(g, places, sms, st);
+kvq_status launch_tiles(const TileArgs& t, int sms, cudaStream_t st) {
+    constexpr auto kernel = pages_tile_kernel<D, HAD>;
+    constexpr int smem = (int)sizeof(TileSmem<D, HAD>);
+    static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+    if (!allow_smem<kernel>(smem)) return KVQ_ERR_CUDA;
+    // the kernel's register split needs all that the launch gives it
+    static const bool fits = [&] {
+        cudaFuncAttributes at;
+        return cudaFuncGetAttributes(&at, kernel) == cudaSuccess &&
+               at.numRegs * kTileThreads >= (kSoftmaxRegs + kOtherRegs) * kTileThreads / 2;
+    }();
+    if (!fits) return KVQ_ERR_CUDA;
+    const kvq_status s = launch(kernel, dim3(sms), kTileThreads, smem, st, t);
+    if (s != KVQ_OK) return s;
+    return launch(pages_merge_kernel<D, kMaxItemRows, HAD>, dim3(sms, kMaxItemRows / kMergeWarps), kMergeWarps * 32, 0,
+                  st, t.a);
+}
+
+template <int D, bool HAD>
+kvq_status launch_attn(const StepArgs& g, const TileArgs& t, const AttnPlan& p, int sms, cudaStream_t st) {
+    const unsigned ctas = (unsigned)((p.places * g.a.Hq + kQueryWarps - 1) / kQueryWarps) + (p.tiles ? 1 : 0);
+    kvq_status s = launch(pages_queries_kernel<D, HAD>, dim3(ctas), kQueryWarps * 32, 0, st, g, t, p.tiles ? sms : 0);
+    if (s == KVQ_OK && p.places > 0) {
+        if (HAD && p.queries <= 4) s = launch_step<D, HAD ? 4 : 8, HAD>(g, sms, st);
+        else if (p.queries <= 8) s = launch_step<D, 8, HAD>(g, sms, st);
+        else s = launch_step<D, 16, HAD>(g, sms, st);
     }
-    if (queries <= 8) return launch_step<D, 8, HAD>(g, places, sms, st);
-    return launch_step<D, 16, HAD>(g, places, sms, st);
+    if (s == KVQ_OK && p.tiles) s = launch_tiles<D, HAD>(t, sms, st);
+    return s;
 }
 
 kvq_status check_attention(const kvq_config* cfg, const kvq_pages* p, const kvq_batch* b, int64_t rows, int q_heads) {
@@ -326,7 +381,8 @@ kvq_status kvq_pages_read(const kvq_config* cfg, const kvq_pages* pages, const k
 size_t kvq_pages_attention_workspace_bytes(const kvq_config* cfg, const kvq_pages* pages, const kvq_batch* batch,
                                            int64_t rows, int32_t q_heads) {
     if (check_attention(cfg, pages, batch, rows, q_heads) != KVQ_OK) return 0;
-    return attn_workspace(sm_count(), cfg->head_dim, cfg->flags == KVQ_HADAMARD, rows * q_heads).bytes;
+    const AttnPlan p = attn_plan(batch, rows, q_heads / pages->kv_heads);
+    return attn_workspace(p, sm_count(), cfg->head_dim, cfg->flags == KVQ_HADAMARD, q_heads, batch->n_seqs).bytes;
 }
 
 kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, const kvq_batch* batch,
@@ -351,8 +407,8 @@ kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, co
     if (!ok_ptr(ws) || ws_bytes < need) return KVQ_ERR_WORKSPACE;
     const int sms = sm_count();
     const bool had = cfg->flags == KVQ_HADAMARD;
-    const long long places = rows;
-    const AttnWorkspace w = attn_workspace(sms, d, had, places * q_heads);
+    const AttnPlan p = attn_plan(batch, rows, q_heads / pages->kv_heads);
+    const AttnWorkspace w = attn_workspace(p, sms, d, had, q_heads, batch->n_seqs);
     uint8_t* base = static_cast<uint8_t*>(ws);
     StepArgs g;
     AttnArgs& a = g.a;
@@ -378,14 +434,23 @@ kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, co
     a.ml = reinterpret_cast<float*>(base + w.ml);
     a.part = reinterpret_cast<float*>(base + w.part);
     a.left = reinterpret_cast<float*>(base + w.left);
-    g.many = 0;
-    g.stretch = 0;
+    a.item_rows = 0;
+    g.many = p.tiles ? kMany : 0;
+    g.stretch = p.stretch;
     g.frag = reinterpret_cast<__half*>(base + w.frag);
     g.scal = reinterpret_cast<float4*>(base + w.scal);
+    TileArgs t;
+    t.a = a;
+    t.a.meta = reinterpret_cast<int4*>(base + w.tile_meta);
+    t.a.ml = reinterpret_cast<float*>(base + w.tile_ml);
+    t.a.part = reinterpret_cast<float*>(base + w.tile_part);
+    t.many = kMany;
+    t.a.item_rows = item_rows(d, had);
+    t.plan = reinterpret_cast<int4*>(base + w.plan);
+    t.seq_cost = reinterpret_cast<long long*>(base + w.seq_cost);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const long long queries = (long long)a.G * (batch->max_rows > 0 ? batch->max_rows : 1);
-    if (d == 64) return had ? launch_attn<64, true>(g, places, queries, sms, st) : launch_attn<64, false>(g, places, queries, sms, st);
-    return had ? launch_attn<128, true>(g, places, queries, sms, st) : launch_attn<128, false>(g, places, queries, sms, st);
+    if (d == 64) return had ? launch_attn<64, true>(g, t, p, sms, st) : launch_attn<64, false>(g, t, p, sms, st);
+    return had ? launch_attn<128, true>(g, t, p, sms, st) : launch_attn<128, false>(g, t, p, sms, st);
 }
 
 kvq_status kvq_pages_read_errors(uint32_t* host_out, int32_t clear) {

@@ -35,6 +35,7 @@ struct AttnArgs {
     float* ml;           // partial states: M, l [slot][query][2]
     float* part;         // and o [slot][query][D]
     float* left;         // o of warps' first items [warp][query][D]
+    int item_rows;       // query rows of an item, at most
     int4* meta;          // [CTA]: sequence, head, first query, merged slots (0: nothing to merge)
 };
 
@@ -118,15 +119,15 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, int row, int head,
 // Merges the partial states of an item that several CTAs worked on.  One CTA a
 // main-kernel CTA: those of CTAs that no split item starts in return at once.
 // Slot 2b + 1 is the state of an item that CTA b began and did not end, slot
-// 2b of one that it did not begin.  kMergeWarps / NQ warps share a query's
-// states; the order of the sums is fixed.
+// 2b of one that it did not begin.  Warps beyond one a query share its states; the order of the sums is fixed.
 constexpr int kMergeWarps = 16;
 
 template <int D, int NQ, bool HAD>
 __global__ void __launch_bounds__(kMergeWarps * 32) pages_merge_kernel(AttnArgs a) {
-    constexpr int W = kMergeWarps / NQ;
-    __shared__ float s_o[NQ][W][D], s_l[NQ][W];
-    const int b = blockIdx.x, qi = (threadIdx.x >> 5) / W, part = (threadIdx.x >> 5) % W, lane = threadIdx.x & 31;
+    constexpr int NB = NQ < kMergeWarps ? NQ : kMergeWarps, W = kMergeWarps / NB;  // queries a block, warps a query
+    __shared__ float s_o[NB][W][D], s_l[NB][W];
+    const int b = blockIdx.x, qb = (threadIdx.x >> 5) / W, part = (threadIdx.x >> 5) % W, lane = threadIdx.x & 31;
+    const int qi = blockIdx.y * NB + qb;
     grid_dep_wait();
     grid_dep_launch();
     const int4 meta = a.meta[b];
@@ -151,15 +152,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32) pages_merge_kernel(AttnArgs 
         for (int c = 0; c < D / 32; ++c) v[c] = __fmaf_rn(a.part[at * D + lane + 32 * c], f, v[c]);
     }
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) s_o[qi][part][lane + 32 * c] = v[c];
-    if (lane == 0) s_l[qi][part] = l;
+    for (int c = 0; c < D / 32; ++c) s_o[qb][part][lane + 32 * c] = v[c];
+    if (lane == 0) s_l[qb][part] = l;
     __syncthreads();
-    if (part != 0 || row >= min(end, a.rows)) return;
+    if (part != 0 || qi >= a.item_rows || row >= min(end, a.rows)) return;
 #pragma unroll
     for (int w = 1; w < W; ++w) {
-        l += s_l[qi][w];
+        l += s_l[qb][w];
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) v[c] += s_o[qi][w][lane + 32 * c];
+        for (int c = 0; c < D / 32; ++c) v[c] += s_o[qb][w][lane + 32 * c];
     }
     finish_row<D, HAD>(a, row, head, v, M, l);
 }

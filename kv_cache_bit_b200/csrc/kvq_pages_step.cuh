@@ -201,6 +201,15 @@ __device__ __forceinline__ uint32_t codes_low(uint32_t w) {  // (1024 + e) - 103
 constexpr float kHigh = 72.0f;
 __device__ __forceinline__ uint32_t codes_high(uint32_t w) { return in_mantissa<0x00F000F0u, 0x54005400u>(w); }
 
+// Those as q, exactly: (1024 + 16 e) / 16 - 72.
+__device__ __forceinline__ uint32_t codes_upper(uint32_t w) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;"
+        : "=r"(r)
+        : "r"(in_mantissa<0x00F000F0u, 0x64006400u>(w)), "r"(0x2C002C00u), "r"(0xD480D480u));
+    return r;
+}
+
 // 16 bytes to shared memory: `n` (16 or 0) of them from src, zeros for the rest.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
@@ -232,90 +241,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&x)[4], uint3
 template <bool HAD>
 __device__ __forceinline__ int query_of(int v, int t) {
     return HAD ? 4 * v + t : 8 * (v >> 1) + 2 * t + (v & 1);
-}
-
-// Loads, rotates, scales and splits the queries: a warp each, D / 32
-// neighbouring channels a lane.
-constexpr int kQueryWarps = 8;
-
-template <int D, bool HAD>
-__global__ void __launch_bounds__(kQueryWarps * 32) pages_queries_kernel(StepArgs g) {
-    constexpr int N = D / 32, C = D / 4;  // channels a lane; channels a fragment lane
-    const AttnArgs& a = g.a;
-    const int lane = threadIdx.x & 31;
-    const long long at = (long long)blockIdx.x * kQueryWarps + (threadIdx.x >> 5);
-    const long long place = at / a.Hq;
-    const int head = (int)(at - place * a.Hq);
-    grid_dep_wait();
-    grid_dep_launch();
-    long long row = place;
-    if (g.many > 0) {
-        const int s = (int)(place / g.stretch);
-        if (s >= a.b.n_seqs) return;
-        const int lo = max(a.b.start[s], 0), hi = min(a.b.start[s + 1], a.rows);
-        row = lo + (place - (long long)s * g.stretch);
-        if (row >= hi || (long long)(hi - lo) * a.G > g.many) return;
-    }
-    if (row >= a.rows) return;
-    const uint16_t* src = static_cast<const uint16_t*>(a.q) + row * a.q_row + head * a.q_head + lane * N;
-    uint32_t u[N / 2];
-    load_words(reinterpret_cast<const uint8_t*>(src), u);
-    float v[N];
-#pragma unroll
-    for (int k = 0; k < N / 2; ++k) {
-        const float2 f = a.bf16 ? Elem<__nv_bfloat16>::wide(u[k]) : Elem<__half>::wide(u[k]);
-        v[2 * k] = f.x, v[2 * k + 1] = f.y;
-    }
-    if constexpr (HAD) {
-        if (a.signs) {
-            if constexpr (N == 4) {
-                const char4 x = reinterpret_cast<const char4*>(a.signs)[lane];
-                v[0] *= x.x, v[1] *= x.y, v[2] *= x.z, v[3] *= x.w;
-            } else {
-                const char2 x = reinterpret_cast<const char2*>(a.signs)[lane];
-                v[0] *= x.x, v[1] *= x.y;
-            }
-        }
-        lane_stages<1, N>(v);
-#pragma unroll
-        for (int x = 1; x < 32; x <<= 1) {
-            const float flip = (lane & x) ? -1.0f : 1.0f;
-#pragma unroll
-            for (int k = 0; k < N; ++k) v[k] = __fmaf_rn(v[k], flip, __shfl_xor_sync(~0u, v[k], x));
-        }
-#pragma unroll
-        for (int k = 0; k < N; ++k) v[k] *= a.rsqd;
-    }
-    float m = 0.0f;
-#pragma unroll
-    for (int k = 0; k < N; ++k) m = max_or_nan(m, fabsf(v[k]));
-#pragma unroll
-    for (int x = 16; x; x >>= 1) m = max_or_nan(m, __shfl_xor_sync(~0u, m, x));
-    const float f = m > 0.0f || m != m ? query_scale(m) : 1.0f;
-    float sum[2] = {0.0f, 0.0f};  // of the channels whose codes come with kHigh
-    __half* dst = g.frag + at * (HAD ? 2 : 1) * D;
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        // fragment lane t holds channels C t .. ; of eight of them, channel c8 is half c8 / 4 of word
-        // (tile's nibble parity, register)
-        const int ch = lane * N + k, t = ch / C, i8 = (ch % C) >> 3, c8 = ch & 7;
-        const int place8 = (i8 * 4 + t) * 8 + ((c8 & 1) * 2 + ((c8 >> 1) & 1)) * 2 + (c8 >> 2);
-        const float x = v[k] * f;
-        const __half hi = __float2half_rn(x);
-        dst[place8] = hi;
-        if (k & 1) sum[0] += __half2float(hi);
-        if constexpr (HAD) {
-            const __half lo = __float2half_rn(x - __half2float(hi));
-            dst[D + place8] = lo;
-            if (k & 1) sum[1] += __half2float(lo);
-        }
-    }
-#pragma unroll
-    for (int x = 16; x; x >>= 1) {
-        sum[0] += __shfl_xor_sync(~0u, sum[0], x);
-        if constexpr (HAD) sum[1] += __shfl_xor_sync(~0u, sum[1], x);
-    }
-    if (lane == 0) g.scal[at] = make_float4(a.scale2 / f, -kHigh * sum[0], -kHigh * sum[1], 0.0f);
 }
 
 // Tokens that query i of an item sees.

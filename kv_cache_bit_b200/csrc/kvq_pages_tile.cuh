@@ -1,0 +1,837 @@
+// kvq_pages_tile.cuh -- attention of many query rows a kv head (prompts, parts
+// of prompts): tcgen05 products on tiles of 256 rows and 128 tokens.
+//
+// Rows: row r and query head j of a kv head's group are tile row r G + j, so
+// that a kv head's codes are unpacked once for all its heads.  An item is
+// (sequence, 256 such rows, kv head); its cost is the number of 128-token
+// tiles that its rows see.  pages_plan lays all items end to end and cuts them
+// into one range a CTA; parts of items at the ends are merged by
+// pages_merge_kernel.
+//
+// A CTA (one an SM):
+//   warps 0 .. 3, 4 .. 7   softmax of the lower and the upper 128 rows, one row a
+//                          thread; they also bring in the queries and finish rows
+//   warps 8 .. 11          K: codes from global memory to fp16 tiles; scales
+//   warp 12                issues the products
+//   warps 13 .. 15         V
+// Products a step, rows X: S_X = Q_X K^T (for rotated queries twice, the high
+// and the low fp16 part: 22 bits of the query are kept), then O_X += W_X V with
+// W_X, fp16, taken from tensor memory, where it lies over S_X.  The order
+// O_A, S_A of the next tile, O_B, S_B lets the softmax of one half run while
+// the tensor core works for the other.  Tiles of K and V go through a ring of
+// three shared-memory buffers.
+// O stays in tensor memory; a row whose maximum rose by more than 2^kSlack
+// scales it there (its O is at rest between its S and its W).
+#pragma once
+
+#include "kvq_pages_attn.cuh"
+#include "kvq_pages_step.cuh"
+
+namespace kvq {
+
+constexpr int kRowsM = 128, kMaxItemRows = 256, kTileTokens = 128;
+constexpr int kTileThreads = 512;
+constexpr int kRingTiles = 3;
+// Rows of an item: 256, but 248 where queries of two parts leave no room in
+// shared memory for the scales (the last eight rows of a product are ignored).
+constexpr int item_rows(int d, bool had) { return d == 128 && had ? 248 : 256; }
+constexpr float kSlack = 8.0f;               // how far a row's maximum may pass its reference
+constexpr float kTileBias = kBias - kSlack;  // w = 2^(y - M + kTileBias) stays in fp16
+constexpr uint32_t kTileWait = 1u << 22;  // polls, of a second at most together
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;  // 256 threads each: the 128 a thread of the launch
+
+struct TileArgs {
+    AttnArgs a;
+    int many;             // sequences of more query rows a kv head than this are this kernel's
+    int4* plan;           // [CTA]: sequence, chunk, head, first tile
+    long long* seq_cost;  // [sequence] tiles, then the total
+};
+
+// One item's place among the tokens and rows.
+struct TileItem {
+    int s, lo, nq, len, base;  // the sequence: first row, query rows a kv head, tokens, token of row 0
+    int chunks, c, h;
+    int u0, units;  // tiles that the item's rows see
+    int t0, t1;
+};
+
+__device__ __forceinline__ bool tile_seq(const TileArgs& g, int s, TileItem& it) {
+    const int end = g.a.b.start[s + 1], lo = max(g.a.b.start[s], 0), hi = min(end, g.a.rows);
+    it.s = s;
+    it.lo = lo;
+    it.nq = max(hi - lo, 0) * g.a.G;
+    it.chunks = 0;
+    if (it.nq <= g.many) return false;
+    const int len = g.a.b.len[s];
+    it.len = len;
+    it.base = len - end;
+    it.chunks = (it.nq + g.a.item_rows - 1) / g.a.item_rows;
+    return true;
+}
+__device__ __forceinline__ void tile_chunk(const TileArgs& g, TileItem& it, int c) {
+    it.c = c;
+    const int r0 = c * g.a.item_rows / g.a.G, r1 = (min((c + 1) * g.a.item_rows, it.nq) - 1) / g.a.G + 1;
+    const Range r = range_of(g.a, it.len, it.len - it.base, it.lo + r0, it.lo + r1);
+    it.t0 = r.t0;
+    it.t1 = r.t1;
+    it.u0 = r.t0 / kTileTokens;
+    it.units = max((r.t1 + kTileTokens - 1) / kTileTokens - it.u0, 1);
+}
+
+// The ranges of the tile kernel's CTAs, by one block of 256 threads.
+__device__ __forceinline__ void pages_plan(const TileArgs& g, int ctas_max) {
+    __shared__ long long sums[8], runs[257];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, H = g.a.p.H, n_seqs = g.a.b.n_seqs;
+    TileItem it;
+    for (int s = warp; s < n_seqs; s += 8) {
+        long long cost = 0;
+        if (tile_seq(g, s, it))
+            for (int c = lane; c < it.chunks; c += 32) {
+                tile_chunk(g, it, c);
+                cost += it.units;
+            }
+#pragma unroll
+        for (int x = 16; x; x >>= 1) cost += __shfl_xor_sync(~0u, cost, x);
+        if (lane == 0) g.seq_cost[s] = cost * H;
+    }
+    __syncthreads();
+    const int per = (n_seqs + 255) / 256, s0 = threadIdx.x * per;
+    long long mine = 0;
+    for (int s = s0; s < min(s0 + per, n_seqs); ++s) mine += g.seq_cost[s];
+    long long sum = mine;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const long long o = __shfl_up_sync(~0u, sum, x);
+        if (lane >= x) sum += o;
+    }
+    if (lane == 31) sums[warp] = sum;
+    __syncthreads();
+    long long before = 0;
+    for (int w = 0; w < warp; ++w) before += sums[w];
+    runs[threadIdx.x + 1] = before + sum;
+    if (threadIdx.x == 0) runs[0] = 0;
+    __syncthreads();
+    const long long total = runs[256];
+    if (threadIdx.x == 0) g.seq_cost[n_seqs] = total;
+    const int ctas = (int)min((long long)ctas_max, total);
+    for (int b = warp; b < ctas; b += 8) {
+        const long long share = total / ctas;
+        long long off = share * b + min((long long)b, total % ctas);
+        int lo = 0, hi = 256;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (runs[mid] <= off) lo = mid;
+            else hi = mid;
+        }
+        off -= runs[lo];
+        int s = lo * per;
+        while (s + 1 < n_seqs && off >= g.seq_cost[s]) off -= g.seq_cost[s++];
+        tile_seq(g, s, it);
+        for (int c0 = 0; c0 < it.chunks; c0 += 32) {
+            long long cost = 0;
+            if (c0 + lane < it.chunks) {
+                tile_chunk(g, it, c0 + lane);
+                cost = (long long)it.units * H;
+            }
+            long long upto = cost;
+#pragma unroll
+            for (int x = 1; x < 32; x <<= 1) {
+                const long long o = __shfl_up_sync(~0u, upto, x);
+                if (lane >= x) upto += o;
+            }
+            const bool here = off >= upto - cost && off < upto;
+            if (here) {
+                const long long in = off - (upto - cost);
+                g.plan[b] = make_int4(s, c0 + lane, (int)(in / it.units), (int)(in % it.units));
+            }
+            if (__any_sync(~0u, here)) break;
+            off -= __shfl_sync(~0u, upto, 31);
+        }
+    }
+}
+
+// Loads, rotates, scales and splits the queries: a warp each, D / 32
+// neighbouring channels a lane.  Where the tile kernel runs too, the last block
+// plans it.
+constexpr int kQueryWarps = 8;
+
+template <int D, bool HAD>
+__global__ void __launch_bounds__(kQueryWarps * 32) pages_queries_kernel(StepArgs g, TileArgs tiles, int plan_ctas) {
+    constexpr int N = D / 32, C = D / 4;  // channels a lane; channels a fragment lane
+    const AttnArgs& a = g.a;
+    const int lane = threadIdx.x & 31;
+    const long long at = (long long)blockIdx.x * kQueryWarps + (threadIdx.x >> 5);
+    const long long place = at / a.Hq;
+    const int head = (int)(at - place * a.Hq);
+    grid_dep_wait();
+    grid_dep_launch();
+    if (plan_ctas > 0 && blockIdx.x == gridDim.x - 1) {  // the last block cuts the tile kernel's work
+        pages_plan(tiles, plan_ctas);
+        return;
+    }
+    long long row = place;
+    if (g.many > 0) {
+        const int s = (int)(place / g.stretch);
+        if (s >= a.b.n_seqs) return;
+        const int lo = max(a.b.start[s], 0), hi = min(a.b.start[s + 1], a.rows);
+        row = lo + (place - (long long)s * g.stretch);
+        if (row >= hi || (long long)(hi - lo) * a.G > g.many) return;
+    }
+    if (row >= a.rows) return;
+    const uint16_t* src = static_cast<const uint16_t*>(a.q) + row * a.q_row + head * a.q_head + lane * N;
+    uint32_t u[N / 2];
+    load_words(reinterpret_cast<const uint8_t*>(src), u);
+    float v[N];
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) {
+        const float2 f = a.bf16 ? Elem<__nv_bfloat16>::wide(u[k]) : Elem<__half>::wide(u[k]);
+        v[2 * k] = f.x, v[2 * k + 1] = f.y;
+    }
+    if constexpr (HAD) {
+        if (a.signs) {
+            if constexpr (N == 4) {
+                const char4 x = reinterpret_cast<const char4*>(a.signs)[lane];
+                v[0] *= x.x, v[1] *= x.y, v[2] *= x.z, v[3] *= x.w;
+            } else {
+                const char2 x = reinterpret_cast<const char2*>(a.signs)[lane];
+                v[0] *= x.x, v[1] *= x.y;
+            }
+        }
+        lane_stages<1, N>(v);
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const float flip = (lane & x) ? -1.0f : 1.0f;
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] = __fmaf_rn(v[k], flip, __shfl_xor_sync(~0u, v[k], x));
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] *= a.rsqd;
+    }
+    float m = 0.0f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) m = max_or_nan(m, fabsf(v[k]));
+#pragma unroll
+    for (int x = 16; x; x >>= 1) m = max_or_nan(m, __shfl_xor_sync(~0u, m, x));
+    const float f = m > 0.0f || m != m ? query_scale(m) : 1.0f;
+    float sum[2] = {0.0f, 0.0f};  // of the channels whose codes come with kHigh
+    __half* dst = g.frag + at * (HAD ? 2 : 1) * D;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        // fragment lane t holds channels C t .. ; of eight of them, channel c8 is half c8 / 4 of word
+        // (tile's nibble parity, register)
+        const int ch = lane * N + k, t = ch / C, i8 = (ch % C) >> 3, c8 = ch & 7;
+        const int place8 = (i8 * 4 + t) * 8 + ((c8 & 1) * 2 + ((c8 >> 1) & 1)) * 2 + (c8 >> 2);
+        const float x = v[k] * f;
+        const __half hi = __float2half_rn(x);
+        dst[place8] = hi;
+        if (k & 1) sum[0] += __half2float(hi);
+        if constexpr (HAD) {
+            const __half lo = __float2half_rn(x - __half2float(hi));
+            dst[D + place8] = lo;
+            if (k & 1) sum[1] += __half2float(lo);
+        }
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1) {
+        sum[0] += __shfl_xor_sync(~0u, sum[0], x);
+        if constexpr (HAD) sum[1] += __shfl_xor_sync(~0u, sum[1], x);
+    }
+    if (lane == 0) g.scal[at] = make_float4(a.scale2 / f, -kHigh * sum[0], -kHigh * sum[1], 0.0f);
+}
+
+// A walk over a CTA's segments; every warp has its own.
+struct TileWalk {
+    TileItem it;
+    int u, n;        // first tile (of the item's) and tiles of the segment
+    long long left;  // tiles of the range from the segment's first on
+
+    __device__ __forceinline__ void begin(const TileArgs& g, int b, int ctas, long long total) {
+        const int4 p = g.plan[b];
+        left = total / ctas + (b < total % ctas ? 1 : 0);
+        tile_seq(g, p.x, it);
+        tile_chunk(g, it, p.y);
+        it.h = p.z;
+        u = p.w;
+        n = (int)min((long long)(it.units - u), left);
+    }
+    __device__ __forceinline__ void next(const TileArgs& g) {
+        left -= n;
+        n = 0;
+        if (left <= 0) return;
+        u = 0;
+        if (++it.h == g.a.p.H) {
+            it.h = 0;
+            if (it.c + 1 < it.chunks) {
+                tile_chunk(g, it, it.c + 1);
+            } else {
+                int s = it.s + 1;
+                while (s < g.a.b.n_seqs && !tile_seq(g, s, it)) ++s;
+                if (s >= g.a.b.n_seqs) {
+                    left = 0;
+                    return;
+                }
+                tile_chunk(g, it, 0);
+            }
+        }
+        n = (int)min((long long)it.units, left);
+    }
+};
+
+template <int D, bool HAD>
+struct TileSmem {
+    static constexpr int kTile = kTileTokens * D * 2;  // bytes of a K or V tile
+    static constexpr int kParts = HAD ? 2 : 1, kRows = item_rows(D, HAD), kUpper = kRows - kRowsM;
+    static constexpr int kQ0 = kRowsM * D * 2, kQ1 = kUpper * D * 2;  // bytes of a part of a half's queries
+    static constexpr int kPieces = D / 32;                            // 16-byte pieces of a token's codes
+    alignas(1024) uint8_t q[kParts * (kQ0 + kQ1)];                    // [half][high, low][64 channels][row]
+    alignas(1024) uint8_t ring[kRingTiles][kTile];
+    alignas(16) float par[2][3][kTileTokens];          // K scale times scale2, log2 and inverse of the V scale
+    uint64_t full[kRingTiles], empty[kRingTiles];
+    uint64_t par_full[2], par_empty[2];
+    uint64_t q_full[2], s_full[2], w_full[2], o_full[2];
+    uint32_t tmem;
+};
+
+// ---------------------------------------------------------------- tcgen05
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar, uint32_t n = 1) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+// mbar_wait that also gives up once a second has passed (a poll's suspension is the hardware's choice).
+__device__ __forceinline__ bool mbar_wait_1s(uint64_t* bar, uint32_t parity, uint32_t max_iter) {
+    uint64_t t0 = 0, t;
+    for (uint32_t left = max_iter; left > 0;) {
+        const uint32_t n = min(left, 64u);
+        if (mbar_wait(bar, parity, n)) return true;
+        left -= n;
+        asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+        if (t0 == 0) t0 = t;
+        else if (t - t0 > 1000000000ull) break;
+    }
+    return false;
+}
+// The tensor core's arrival once all products issued so far are done.
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void tc_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Shared-memory descriptor of a 128-byte-swizzled operand.  K-major (queries,
+// K): 8-row groups 1024 bytes apart (stride offset); the other offset is not
+// used.  MN-major (V, channels contiguous): 8-token groups 1024 bytes apart,
+// the next 64 channels kTile / (D / 64) on (leading offset).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t leading) {
+    return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(leading >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// fp16 operands, fp32 sums, M = 128.
+__host__ __device__ constexpr uint32_t mma_desc(int n, bool b_mn_major) {
+    return 1u << 4 | (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(kRowsM >> 4) << 24;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+        : "memory");
+}
+
+// 32 columns of the thread's row.
+__device__ __forceinline__ void tmem_load32(uint32_t (&r)[32], uint32_t at) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Packed fp32 pairs.
+__device__ __forceinline__ uint64_t pair2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpair2(uint64_t v, float& x, float& y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f2(uint64_t x, uint64_t y, uint64_t z) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+
+// Four 16-byte pieces of a 128-byte-swizzled tile from 32 codes of one token:
+// channels 32 quarter .. + 31 (D = 128) of row `row`.  Of eight channels the
+// halves are in the order 0 4 1 5 2 6 3 7, as the queries' and O's are.
+template <int D>
+__device__ __forceinline__ void store_codes(uint8_t* tile, int row, int quarter, const uint4& w) {
+    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+    uint8_t* base = tile + (quarter >> 1) * (kTileTokens * 128) + row * 128;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t x = words[k], x8 = x >> 8;
+        const int chunk = ((quarter & 1) * 4 + k) ^ (row & 7);
+        *reinterpret_cast<uint4*>(base + chunk * 16) =
+            make_uint4(codes_low(x), codes_upper(x), codes_low(x8), codes_upper(x8));
+    }
+}
+// Order of eight channels in a 16-byte piece: place p holds channel place8(p).
+__host__ __device__ constexpr int place8(int p) { return (p >> 1) + 4 * (p & 1); }
+
+// Pages of the tile's tokens: this thread's token's slot, or -1.
+__device__ __forceinline__ long long tile_slot(const TileArgs& g, const TileItem& it, int tok) {
+    if (tok < it.t0 || tok >= it.t1) return -1;
+    return slot_of(g.a.b, g.a.p, it.s, tok);
+}
+
+template <int D, bool HAD>
+__global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g) {
+    using S = TileSmem<D, HAD>;
+    constexpr int kTile = S::kTile, kSlab = kTileTokens * 128, kPieces = S::kPieces;
+    extern __shared__ __align__(1024) uint8_t tile_raw[];
+    S& sm = *reinterpret_cast<S*>(tile_raw);
+    const AttnArgs& a = g.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kRingTiles; ++i) mbar_init(&sm.full[i], 4), mbar_init(&sm.empty[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.par_full[i], 4), mbar_init(&sm.par_empty[i], 8);
+            mbar_init(&sm.q_full[i], 4), mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.w_full[i], 4), mbar_init(&sm.o_full[i], 1);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    grid_dep_wait();
+    grid_dep_launch();
+    const long long total = g.seq_cost[a.b.n_seqs];
+    const int ctas = (int)min((long long)gridDim.x, total);
+    if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+    tc_before_sync();
+    __syncthreads();
+    tc_after_sync();
+    const uint32_t tmem = sm.tmem;
+    const bool works = (int)blockIdx.x < ctas;
+    // Waits give up after a while: results are void then, and every warp leaves its loop.
+    const auto wait_one = [&](uint64_t* bar, uint32_t parity) {
+        if (mbar_wait_1s(bar, parity, KVQ_WAIT_LIMIT(kTileWait))) return true;
+        report_error(kErrBarrierTimeout);
+        return false;
+    };
+    const auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(~0u, wait_one(bar, parity)) != 0; };
+
+    if (works && warp < 8) {
+        // ------------------------------------------------ softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        const int half = warp >> 2, r = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
+        const uint32_t ts = tmem + lanes + half * 128, to = tmem + lanes + 256 + half * 128;
+        TileWalk wk;
+        wk.begin(g, blockIdx.x, ctas, total);
+        uint32_t tile = 0;
+        bool ok = true;
+        for (uint32_t item = 0; ok && wk.n > 0; wk.next(g), ++item) {
+            const TileItem& it = wk.it;
+            const int i = it.c * S::kRows + half * kRowsM + r;  // row of the kv head's queries
+            const bool stored = half == 0 || r < S::kUpper, there = stored && i < it.nq;
+            const int qr = i / a.G, row = it.lo + qr, head = it.h * a.G + i - qr * a.G;
+            Range see{0, 0};
+            float factor = 1.0f;
+            {   // the query: rotated, split, into the tile
+                uint64_t v[D / 2];
+                uint32_t u[D / 2];
+#pragma unroll
+                for (int k = 0; k < D / 2; ++k) u[k] = 0;
+                if (there) {
+                    const uint8_t* src = reinterpret_cast<const uint8_t*>(static_cast<const uint16_t*>(a.q) +
+                                                                          row * a.q_row + head * a.q_head);
+                    load_words(src, u);
+                    const long long n = max(it.len, 0), pos = (long long)it.base + row;
+                    const long long t1 = min(a.causal ? min(pos + 1, n) : n, (long long)it.t1);
+                    const long long t0 = a.causal && a.window > 0 ? max(pos - a.window + 1, 0ll) : 0;
+                    if (t0 < t1) see = Range{(int)t0, (int)t1};
+                }
+#pragma unroll
+                for (int k = 0; k < D / 2; ++k) {
+                    float2 f = a.bf16 ? Elem<__nv_bfloat16>::wide(u[k]) : Elem<__half>::wide(u[k]);
+                    if (HAD && a.signs) {
+                        const char2 sg = reinterpret_cast<const char2*>(a.signs)[k];
+                        f.x *= sg.x, f.y *= sg.y;
+                    }
+                    v[k] = pair2(f.x, f.y);
+                }
+                if constexpr (HAD) {
+                    const uint64_t minus = pair2(-1.0f, -1.0f);
+#pragma unroll
+                    for (int x = 1; x < D / 2; x <<= 1)
+#pragma unroll
+                        for (int k = 0; k < D / 2; ++k)
+                            if (!(k & x)) {
+                                const uint64_t p = v[k], q = v[k + x];
+                                v[k] = add_f2(p, q);
+                                v[k + x] = fma_f2(q, minus, p);
+                            }
+                }
+                float m = 0.0f;
+#pragma unroll
+                for (int k = 0; k < D / 2; ++k) {
+                    float x, y;
+                    unpair2(v[k], x, y);
+                    if constexpr (HAD) {
+                        const float p = (x + y) * a.rsqd, q = (x - y) * a.rsqd;
+                        x = p, y = q;
+                        v[k] = pair2(x, y);
+                    }
+                    m = max_or_nan(max_or_nan(m, fabsf(x)), fabsf(y));
+                }
+                // Rows in this range keep 22 bits in the two fp16 parts as they are; others are scaled.
+                if (!(m == 0.0f || (m >= 0x1p-4f && m <= 0x1p14f))) factor = query_scale(m);
+                const int slab = (half ? S::kUpper : kRowsM) * 128;
+                uint8_t* hi = sm.q + half * S::kParts * S::kQ0 + r * 128;
+#pragma unroll
+                for (int k8 = 0; k8 < D / 8; ++k8) {
+                    uint32_t wh[4], wl[4];
+                    float x[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) unpair2(v[4 * k8 + k], x[2 * k], x[2 * k + 1]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float p = x[place8(2 * k)] * factor, q = x[place8(2 * k + 1)] * factor;
+                        const __half2 h = __floats2half2_rn(p, q);
+                        wh[k] = *reinterpret_cast<const uint32_t*>(&h);
+                        if constexpr (HAD) {
+                            const float2 b = __half22float2(h);
+                            const __half2 l = __floats2half2_rn(p - b.x, q - b.y);
+                            wl[k] = *reinterpret_cast<const uint32_t*>(&l);
+                        }
+                    }
+                    const int at = (k8 >> 3) * slab + ((k8 & 7) ^ (r & 7)) * 16;
+                    if (stored) {
+                        *reinterpret_cast<uint4*>(hi + at) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+                        if constexpr (HAD)
+                            *reinterpret_cast<uint4*>(hi + (half ? S::kQ1 : S::kQ0) + at) =
+                                make_uint4(wl[0], wl[1], wl[2], wl[3]);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.q_full[half]);
+            const bool scaled = __any_sync(~0u, factor != 1.0f);
+            const float back = 1.0f / factor;
+            // tokens that all rows of the warp see (rows that are not there count as seeing all)
+            const int see_lo = __reduce_max_sync(~0u, there ? see.t0 : 0);
+            const int see_hi = __reduce_min_sync(~0u, there ? see.t1 : 0x7FFFFFFF);
+
+            float M = kLowest;
+            uint64_t l2 = pair2(0.0f, 0.0f);
+            for (int n = 0; n < wk.n; ++n, ++tile) {
+                const int tok0 = (it.u0 + wk.u + n) * kTileTokens;
+                if (!(ok = wait(&sm.par_full[tile & 1], tile >> 1 & 1)) || !(ok = wait(&sm.s_full[half], tile & 1))) break;
+                tc_after_sync();
+                const float(*par)[kTileTokens] = sm.par[tile & 1];
+                uint32_t s[4][32];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tmem_load32(s[k], ts + 32 * k);
+                tmem_wait_load();
+                if (scaled) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) s[k][c] = __float_as_uint(__uint_as_float(s[k][c]) * back);
+                }
+                float top = kLowest;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int c = 0; c < 32; c += 4) {
+                        const float4 sk = *reinterpret_cast<const float4*>(&par[0][32 * k + c]);
+                        const float4 lv = *reinterpret_cast<const float4*>(&par[1][32 * k + c]);
+                        float y[4];
+                        unpair2(fma_f2(pair2(__uint_as_float(s[k][c]), __uint_as_float(s[k][c + 1])), pair2(sk.x, sk.y),
+                                       pair2(lv.x, lv.y)), y[0], y[1]);
+                        unpair2(fma_f2(pair2(__uint_as_float(s[k][c + 2]), __uint_as_float(s[k][c + 3])),
+                                       pair2(sk.z, sk.w), pair2(lv.z, lv.w)), y[2], y[3]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s[k][c + j] = __float_as_uint(y[j]);
+                    }
+                if (tok0 < see_lo || tok0 + kTileTokens > see_hi) {
+                    const int from = see.t0 - tok0, to_ = see.t1 - tok0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (32 * k + c < from || 32 * k + c >= to_) s[k][c] = 0xFF800000u;  // -inf
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2)
+                        top = fmaxf(top, fmaxf(__uint_as_float(s[k][c]), __uint_as_float(s[k][c + 1])));
+                if (__any_sync(~0u, top > M + kSlack)) {
+                    const float m2 = fmaxf(M, top), f = ex2(M - m2);
+                    const uint64_t ff = pair2(f, f);
+                    M = m2;
+                    l2 = fma_f2(l2, ff, pair2(0.0f, 0.0f));
+                    if (n > 0) {
+#pragma unroll 1
+                        for (int k = 0; k < D; k += 32) {
+                            uint32_t o[32];
+                            tmem_load32(o, to + k);
+                            tmem_wait_load();
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+                            tmem_store32(to + k, o);
+                        }
+                    }
+                }
+                const uint64_t ref = pair2(kTileBias - M, kTileBias - M);
+#pragma unroll
+                for (int k = 0; k < 4; k += 2) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4) {
+                            const float4 rv = *reinterpret_cast<const float4*>(&par[2][32 * (k + e) + c]);
+                            float x[4];
+                            const uint32_t* y = &s[k + e][c];
+                            unpair2(add_f2(pair2(__uint_as_float(y[0]), __uint_as_float(y[1])), ref), x[0], x[1]);
+                            unpair2(add_f2(pair2(__uint_as_float(y[2]), __uint_as_float(y[3])), ref), x[2], x[3]);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) x[j] = ex2(x[j]);
+                            l2 = fma_f2(pair2(x[0], x[1]), pair2(rv.x, rv.y), l2);
+                            l2 = fma_f2(pair2(x[2], x[3]), pair2(rv.z, rv.w), l2);
+                            w[16 * e + c / 2] = Elem<__half>::pack(x[0], x[1]);
+                            w[16 * e + c / 2 + 1] = Elem<__half>::pack(x[2], x[3]);
+                        }
+                    tmem_store32(ts + 16 * k, w);
+                }
+                tmem_wait_store();
+                tc_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sm.w_full[half]);
+                    mbar_arrive(&sm.par_empty[tile & 1]);
+                }
+            }
+            if (!ok || !(ok = wait(&sm.o_full[half], item & 1))) break;
+            tc_after_sync();
+            float la, lb;
+            unpair2(l2, la, lb);
+            const float l = la + lb;
+            const bool begins = wk.u == 0, ends = wk.u + wk.n == it.units, whole = begins && ends;
+            float o[D];
+#pragma unroll
+            for (int k = 0; k < D; k += 32) {
+                uint32_t x[32];
+                tmem_load32(x, to + k);
+                tmem_wait_load();
+#pragma unroll
+                for (int c = 0; c < 32; ++c) o[k + (c & ~7) + place8(c & 7)] = __uint_as_float(x[c]);
+            }
+            tc_before_sync();
+            if (whole) {
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                if constexpr (HAD) lane_stages<1, D>(o);
+                const float unit = HAD ? inv * a.rsqd : inv;
+                uint16_t* dst = static_cast<uint16_t*>(a.out) + row * a.o_row + head * a.o_head;
+#pragma unroll
+                for (int k = 0; k < D; k += 8) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float x = o[k + 2 * c] * unit, y = o[k + 2 * c + 1] * unit;
+                        if (HAD && a.signs) {
+                            const char2 sg = reinterpret_cast<const char2*>(a.signs)[k / 2 + c];
+                            x *= sg.x, y *= sg.y;
+                        }
+                        w[c] = a.bf16 ? Elem<__nv_bfloat16>::pack(x, y) : Elem<__half>::pack(x, y);
+                    }
+                    if (there) *reinterpret_cast<uint4*>(dst + k) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                if (there && a.lse) a.lse[(long long)row * a.Hq + head] = (M - kTileBias + lg2(l)) * kLn2;
+            } else if (there) {
+                const long long at = (2ll * blockIdx.x + (begins ? 1 : 0)) * kMaxItemRows + half * kRowsM + r;
+                reinterpret_cast<float2*>(a.ml)[at] = make_float2(M + kSlack, l);
+                float4* dst = reinterpret_cast<float4*>(a.part + at * D);
+#pragma unroll
+                for (int p = 0; p < D; p += 4)
+                    dst[p / 4] = make_float4(o[channel_of<D>(p)], o[channel_of<D>(p + 1)], o[channel_of<D>(p + 2)],
+                                             o[channel_of<D>(p + 3)]);
+            }
+            if (begins && !ends && threadIdx.x == 0) {
+                // CTAs from this one to that of the item's last tile
+                const long long share = total / ctas, extra = total % ctas;
+                const long long x = share * blockIdx.x + min((long long)blockIdx.x, extra) + share +
+                                    (blockIdx.x < extra ? 1 : 0) - wk.left;
+                const long long last = x + it.units - 1, longer = (share + 1) * extra;
+                const long long b = last < longer ? last / (share + 1) : extra + (last - longer) / share;
+                a.meta[blockIdx.x] = make_int4(it.s, it.h, it.c * S::kRows, (int)(b - blockIdx.x) + 1);
+            }
+        }
+    } else if (works) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        TileWalk wk;
+        wk.begin(g, blockIdx.x, ctas, total);
+        if (warp == 12) {
+            // -------------------------------------------- products
+            if (lane == 0) {
+                constexpr uint32_t kS = mma_desc(kTileTokens, false), kO = mma_desc(D, true);
+                uint32_t seq = 0, tile = 0;  // tiles of the ring taken (K, V, K, ..); steps
+                const uint32_t ring = smem_u32(sm.ring[0]), q = smem_u32(sm.q);
+                const auto scores = [&](int half, uint32_t buf) {
+#pragma unroll
+                    for (int part = 0; part < (HAD ? 2 : 1); ++part)
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint32_t from = half ? S::kParts * S::kQ0 + part * S::kQ1 + (k >> 2) * S::kUpper * 128
+                                                       : part * S::kQ0 + (k >> 2) * kRowsM * 128;
+                            mma_ss(tmem + half * 128, smem_desc(q + from + (k & 3) * 32, 16),
+                                   smem_desc(ring + buf * kTile + (k >> 2) * kSlab + (k & 3) * 32, 16), kS, part + k > 0);
+                        }
+                };
+                const auto values = [&](int half, uint32_t buf, bool add) {
+#pragma unroll
+                    for (int k = 0; k < kTileTokens / 16; ++k)
+                        mma_ts(tmem + 256 + half * 128, tmem + half * 128 + 8 * k,
+                               smem_desc(ring + buf * kTile + k * 2048, kSlab), kO, add || k > 0);
+                };
+                bool ok = true;
+                for (uint32_t item = 0; ok && wk.n > 0; wk.next(g), ++item) {
+                    for (int n = 0; n <= wk.n && ok; ++n) {
+                        // O of tile n - 1, S of tile n; tile n's K is `seq`, tile n - 1's V `seq - 1`
+                        const uint32_t kb = seq % kRingTiles, vb = (seq + 2) % kRingTiles;
+                        if (n > 0) ok = wait_one(&sm.full[vb], (seq - 1) / kRingTiles & 1);
+                        for (int half = 0; half < 2 && ok; ++half) {
+                            if (n > 0) {
+                                if (!(ok = wait_one(&sm.w_full[half], (tile - 1) & 1))) break;
+                                tc_after_sync();
+                                values(half, vb, n > 1);
+                                if (half == 1) mma_commit(&sm.empty[vb]);
+                                if (n == wk.n) mma_commit(&sm.o_full[half]);
+                            }
+                            if (n < wk.n) {
+                                if (n == 0 && !(ok = wait_one(&sm.q_full[half], item & 1))) break;
+                                if (half == 0 && !(ok = wait_one(&sm.full[kb], seq / kRingTiles & 1))) break;
+                                tc_after_sync();
+                                scores(half, kb);
+                                mma_commit(&sm.s_full[half]);
+                                if (half == 1) mma_commit(&sm.empty[kb]);
+                            }
+                        }
+                        if (n < wk.n) seq += 2, ++tile;
+                    }
+                }
+                if (!ok) {  // products in flight end before tensor memory is given back
+                    mma_commit(&sm.o_full[0]);
+                    mma_commit(&sm.o_full[1]);
+                    mbar_wait_1s(&sm.o_full[1], 0, kTileWait);
+                    mbar_wait_1s(&sm.o_full[1], 1, kTileWait);
+                }
+            }
+            __syncwarp();
+        } else {
+            // -------------------------------------------- K (warps 8 .. 11) and V (13 .. 15) tiles
+            const bool is_v = warp > 12;
+            const int me = is_v ? threadIdx.x - 13 * 32 : threadIdx.x - 8 * 32, count = is_v ? 96 : 128;
+            constexpr int kMost = (kTileTokens * kPieces + 95) / 96;  // pieces a lane (V's three warps; K's four have less)
+            uint32_t seq = is_v ? 1 : 0, tile = 0;
+            bool ok = true;
+            for (; ok && wk.n > 0; wk.next(g)) {
+                const TileItem& it = wk.it;
+                for (int n = 0; n < wk.n && ok; ++n, ++tile, seq += 2) {
+                    const int tok0 = (it.u0 + wk.u + n) * kTileTokens;
+                    const uint32_t buf = seq % kRingTiles, round = seq / kRingTiles;
+                    uint4 w[kMost];
+                    float p_sk = 0.0f, p_lv = -INFINITY, p_rv = 0.0f;
+                    if (!is_v) {
+                        const long long slot = tile_slot(g, it, tok0 + me);
+                        if (slot >= 0) {
+                            const long long at = slot + ((long long)it.h << a.p.page_log2);
+                            const float sv = fmaxf(__half2float(a.p.tok[1][at]), 0x1p-24f);
+                            p_sk = __half2float(a.p.tok[0][at]) * a.scale2;
+                            p_lv = lg2(sv);
+                            p_rv = rcp(sv);
+                        }
+                    }
+                    int pieces = 0;
+#pragma unroll
+                    for (int k = 0; k < kMost; ++k) {
+                        const int piece = me + k * count;
+                        w[k] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+                        if (piece < kTileTokens * kPieces) {
+                            const int tok = tok0 + piece / kPieces;
+                            const long long slot = tile_slot(g, it, tok);
+                            if (slot >= 0)
+                                w[k] = reinterpret_cast<const uint4*>(
+                                    a.p.codes[is_v] + (slot + ((long long)it.h << a.p.page_log2)) * (D / 2))[piece % kPieces];
+                            pieces = k + 1;
+                        }
+                    }
+                    if (round > 0 && !(ok = wait(&sm.empty[buf], (round - 1) & 1))) break;
+                    if (!is_v) {
+                        if (tile >= 2 && !(ok = wait(&sm.par_empty[tile & 1], ((tile >> 1) - 1) & 1))) break;
+                        sm.par[tile & 1][0][me] = p_sk;
+                        sm.par[tile & 1][1][me] = p_lv;
+                        sm.par[tile & 1][2][me] = p_rv;
+                    }
+#pragma unroll
+                    for (int k = 0; k < kMost; ++k) {
+                        const int piece = me + k * count;
+                        if (k < pieces) store_codes<D>(sm.ring[buf], piece / kPieces, piece % kPieces, w[k]);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&sm.full[buf], warp == 13 ? 2 : 1);
+                        if (!is_v) mbar_arrive(&sm.par_full[tile & 1]);
+                    }
+                }
+            }
+        }
+    }
+    tc_before_sync();
+    __syncthreads();
+    if (warp == 12) {
+        tc_after_sync();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    }
+}
+
+}  // namespace kvq
