@@ -246,8 +246,8 @@ AttnWorkspace attn_workspace(const AttnPlan& p, int sms, int d, bool had, int q_
     w.scal = take(size_t(p.places) * q_heads * 16);
     const size_t tiles = p.tiles ? size_t(sms) : 0;
     w.tile_meta = take(tiles * 16);
-    w.tile_ml = take(2 * tiles * kMaxItemRows * 8);
-    w.tile_part = take(2 * tiles * kMaxItemRows * d * 4);
+    w.tile_ml = take(2 * tiles * kItemRows * 8);
+    w.tile_part = take(2 * tiles * kItemRows * d * 4);
     w.plan = take(tiles * 16);
     w.seq_cost = take(p.tiles ? (size_t(n_seqs) + 1) * 8 : 0);
     w.bytes = at;
@@ -255,13 +255,12 @@ AttnWorkspace attn_workspace(const AttnPlan& p, int sms, int d, bool had, int q_
 }
 
 template <int D, int NQ, bool HAD>
-kvq_status launch_step(StepArgs g, int sms, cudaStream_t st) {
+kvq_status launch_step(const StepArgs& g, int sms, cudaStream_t st) {
     using Sh = StepShape<NQ>;
     constexpr int smem = (int)sizeof(StepSmem<D, NQ, HAD, Sh::kWarps>);
     static_assert(smem * Sh::kPerSm + Sh::kPerSm * 1024 <= 228 * 1024, "shared memory of the CTAs on one SM");
     constexpr auto kernel = pages_step_kernel<D, NQ, HAD, Sh::kWarps, Sh::kPerSm>;
     if (!allow_smem<kernel>(smem)) return KVQ_ERR_CUDA;
-    g.a.item_rows = NQ;
     const int grid = sms * Sh::kPerSm;
     const kvq_status s = launch(kernel, dim3(grid), Sh::kWarps * 32, smem, st, g);
     if (s != KVQ_OK) return s;
@@ -283,7 +282,7 @@ kvq_status launch_tiles(const TileArgs& t, int sms, cudaStream_t st) {
     if (!fits) return KVQ_ERR_CUDA;
     const kvq_status s = launch(kernel, dim3(sms), kTileThreads, smem, st, t);
     if (s != KVQ_OK) return s;
-    return launch(pages_merge_kernel<D, kMaxItemRows, HAD>, dim3(sms, kMaxItemRows / kMergeWarps), kMergeWarps * 32, 0,
+    return launch(pages_merge_kernel<D, kItemRows, HAD>, dim3(sms, kItemRows / kMergeWarps), kMergeWarps * 32, 0,
                   st, t.a);
 }
 
@@ -434,7 +433,6 @@ kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, co
     a.ml = reinterpret_cast<float*>(base + w.ml);
     a.part = reinterpret_cast<float*>(base + w.part);
     a.left = reinterpret_cast<float*>(base + w.left);
-    a.item_rows = 0;
     g.many = p.tiles ? kMany : 0;
     g.stretch = p.stretch;
     g.frag = reinterpret_cast<__half*>(base + w.frag);
@@ -445,7 +443,6 @@ kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, co
     t.a.ml = reinterpret_cast<float*>(base + w.tile_ml);
     t.a.part = reinterpret_cast<float*>(base + w.tile_part);
     t.many = kMany;
-    t.a.item_rows = item_rows(d, had);
     t.plan = reinterpret_cast<int4*>(base + w.plan);
     t.seq_cost = reinterpret_cast<long long*>(base + w.seq_cost);
     cudaStream_t st = static_cast<cudaStream_t>(stream);

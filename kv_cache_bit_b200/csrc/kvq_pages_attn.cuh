@@ -35,7 +35,6 @@ struct AttnArgs {
     float* ml;           // partial states: M, l [slot][query][2]
     float* part;         // and o [slot][query][D]
     float* left;         // o of warps' first items [warp][query][D]
-    int item_rows;       // query rows of an item, at most
     int4* meta;          // [CTA]: sequence, head, first query, merged slots (0: nothing to merge)
 };
 
@@ -155,7 +154,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) pages_merge_kernel(AttnArgs 
     for (int c = 0; c < D / 32; ++c) s_o[qb][part][lane + 32 * c] = v[c];
     if (lane == 0) s_l[qb][part] = l;
     __syncthreads();
-    if (part != 0 || qi >= a.item_rows || row >= min(end, a.rows)) return;
+    if (part != 0 || row >= min(end, a.rows)) return;
 #pragma unroll
     for (int w = 1; w < W; ++w) {
         l += s_l[qb][w];

@@ -20,21 +20,30 @@
 // O_A, S_A of the next tile, O_B, S_B lets the softmax of one half run while
 // the tensor core works for the other.  Tiles of K and V go through a ring of
 // three shared-memory buffers.
+// W is the probability itself here, 2^(x - M), and the V tile holds sigma q
+// rounded to fp16 (2^-12, as W is): the scheme of the step kernel, with the V
+// scale in the exponent, needs two more numbers a token in every softmax
+// thread, and a number that all lanes read from shared memory takes it as long
+// as 32 different ones (3072 cycles a step for three numbers; the products
+// take as long).  Values below fp16's normal range are kept to 2^-25, which is
+// also what their fp16 scale was rounded to.
 // O stays in tensor memory; a row whose maximum rose by more than 2^kSlack
 // scales it there (its O is at rest between its S and its W).
 #pragma once
+
+#include <type_traits>
 
 #include "kvq_pages_attn.cuh"
 #include "kvq_pages_step.cuh"
 
 namespace kvq {
 
-constexpr int kRowsM = 128, kMaxItemRows = 256, kTileTokens = 128;
+constexpr int kRowsM = 128, kItemRows = 256, kTileTokens = 128;
+// What an item costs besides its tiles (queries in, rows out), in tiles: with 0, the CTA of a prompt's first
+// rows, whose items are short, took twice the time of the others.
+constexpr int kItemCost = 4;
 constexpr int kTileThreads = 512;
 constexpr int kRingTiles = 3;
-// Rows of an item: 256, but 248 where queries of two parts leave no room in
-// shared memory for the scales (the last eight rows of a product are ignored).
-constexpr int item_rows(int d, bool had) { return d == 128 && had ? 248 : 256; }
 constexpr float kSlack = 8.0f;               // how far a row's maximum may pass its reference
 constexpr float kTileBias = kBias - kSlack;  // w = 2^(y - M + kTileBias) stays in fp16
 constexpr uint32_t kTileWait = 1u << 22;  // polls, of a second at most together
@@ -65,12 +74,12 @@ __device__ __forceinline__ bool tile_seq(const TileArgs& g, int s, TileItem& it)
     const int len = g.a.b.len[s];
     it.len = len;
     it.base = len - end;
-    it.chunks = (it.nq + g.a.item_rows - 1) / g.a.item_rows;
+    it.chunks = (it.nq + kItemRows - 1) / kItemRows;
     return true;
 }
 __device__ __forceinline__ void tile_chunk(const TileArgs& g, TileItem& it, int c) {
     it.c = c;
-    const int r0 = c * g.a.item_rows / g.a.G, r1 = (min((c + 1) * g.a.item_rows, it.nq) - 1) / g.a.G + 1;
+    const int r0 = c * kItemRows / g.a.G, r1 = (min((c + 1) * kItemRows, it.nq) - 1) / g.a.G + 1;
     const Range r = range_of(g.a, it.len, it.len - it.base, it.lo + r0, it.lo + r1);
     it.t0 = r.t0;
     it.t1 = r.t1;
@@ -78,9 +87,26 @@ __device__ __forceinline__ void tile_chunk(const TileArgs& g, TileItem& it, int 
     it.units = max((r.t1 + kTileTokens - 1) / kTileTokens - it.u0, 1);
 }
 
-// The ranges of the tile kernel's CTAs, by one block of 256 threads.
+// The first position of range b when `total` positions are cut into `ctas` ranges.
+struct Cut {
+    long long share, extra;
+    __device__ __forceinline__ Cut(long long total, int ctas) {
+        share = quotient(total, ctas);
+        extra = total - share * ctas;
+    }
+    __device__ __forceinline__ long long begin(long long b) const { return share * b + min(b, extra); }
+    // the range that position x lies in
+    __device__ __forceinline__ long long of(long long x) const {
+        const long long longer = (share + 1) * extra;
+        return x < longer ? quotient(x, share + 1) : extra + quotient(x - longer, share);
+    }
+};
+
+// The ranges of the tile kernel's CTAs, by one block of 256 threads: a warp
+// a sequence sums its items' costs; then, with the sequences' running sums,
+// every chunk of rows writes the plans of the ranges that begin in its items.
 __device__ __forceinline__ void pages_plan(const TileArgs& g, int ctas_max) {
-    __shared__ long long sums[8], runs[257];
+    __shared__ long long sums[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, H = g.a.p.H, n_seqs = g.a.b.n_seqs;
     TileItem it;
     for (int s = warp; s < n_seqs; s += 8) {
@@ -88,16 +114,16 @@ __device__ __forceinline__ void pages_plan(const TileArgs& g, int ctas_max) {
         if (tile_seq(g, s, it))
             for (int c = lane; c < it.chunks; c += 32) {
                 tile_chunk(g, it, c);
-                cost += it.units;
+                cost += it.units + kItemCost;
             }
 #pragma unroll
         for (int x = 16; x; x >>= 1) cost += __shfl_xor_sync(~0u, cost, x);
         if (lane == 0) g.seq_cost[s] = cost * H;
     }
     __syncthreads();
-    const int per = (n_seqs + 255) / 256, s0 = threadIdx.x * per;
+    const int per = (n_seqs + 255) / 256, s0 = threadIdx.x * per, s1 = min(s0 + per, n_seqs);
     long long mine = 0;
-    for (int s = s0; s < min(s0 + per, n_seqs); ++s) mine += g.seq_cost[s];
+    for (int s = s0; s < s1; ++s) mine += g.seq_cost[s];
     long long sum = mine;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
@@ -106,32 +132,29 @@ __device__ __forceinline__ void pages_plan(const TileArgs& g, int ctas_max) {
     }
     if (lane == 31) sums[warp] = sum;
     __syncthreads();
-    long long before = 0;
-    for (int w = 0; w < warp; ++w) before += sums[w];
-    runs[threadIdx.x + 1] = before + sum;
-    if (threadIdx.x == 0) runs[0] = 0;
-    __syncthreads();
-    const long long total = runs[256];
+    long long before = sum - mine, total = 0;
+    for (int w = 0; w < 8; ++w) {
+        if (w < warp) before += sums[w];
+        total += sums[w];
+    }
+    for (int s = s0; s < s1; ++s) {  // costs to running sums
+        const long long cost = g.seq_cost[s];
+        g.seq_cost[s] = before;
+        before += cost;
+    }
     if (threadIdx.x == 0) g.seq_cost[n_seqs] = total;
+    __syncthreads();
+    if (total == 0) return;
     const int ctas = (int)min((long long)ctas_max, total);
-    for (int b = warp; b < ctas; b += 8) {
-        const long long share = total / ctas;
-        long long off = share * b + min((long long)b, total % ctas);
-        int lo = 0, hi = 256;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (runs[mid] <= off) lo = mid;
-            else hi = mid;
-        }
-        off -= runs[lo];
-        int s = lo * per;
-        while (s + 1 < n_seqs && off >= g.seq_cost[s]) off -= g.seq_cost[s++];
-        tile_seq(g, s, it);
+    const Cut cut(total, ctas);
+    for (int s = warp; s < n_seqs; s += 8) {
+        if (!tile_seq(g, s, it)) continue;
+        long long at = g.seq_cost[s];
         for (int c0 = 0; c0 < it.chunks; c0 += 32) {
             long long cost = 0;
             if (c0 + lane < it.chunks) {
                 tile_chunk(g, it, c0 + lane);
-                cost = (long long)it.units * H;
+                cost = (long long)(it.units + kItemCost) * H;
             }
             long long upto = cost;
 #pragma unroll
@@ -139,13 +162,16 @@ __device__ __forceinline__ void pages_plan(const TileArgs& g, int ctas_max) {
                 const long long o = __shfl_up_sync(~0u, upto, x);
                 if (lane >= x) upto += o;
             }
-            const bool here = off >= upto - cost && off < upto;
-            if (here) {
-                const long long in = off - (upto - cost);
-                g.plan[b] = make_int4(s, c0 + lane, (int)(in / it.units), (int)(in % it.units));
+            const long long lo = at + upto - cost, hi = at + upto;
+            if (cost > 0) {
+                long long b = cut.of(lo);
+                if (cut.begin(b) < lo) ++b;
+                for (; b < ctas && cut.begin(b) < hi; ++b) {
+                    const long long in = cut.begin(b) - lo, h = quotient(in, it.units + kItemCost);
+                    g.plan[b] = make_int4(s, c0 + lane, (int)h, (int)(in - h * (it.units + kItemCost)));
+                }
             }
-            if (__any_sync(~0u, here)) break;
-            off -= __shfl_sync(~0u, upto, 31);
+            at += __shfl_sync(~0u, upto, 31);
         }
     }
 }
@@ -239,53 +265,66 @@ __global__ void __launch_bounds__(kQueryWarps * 32) pages_queries_kernel(StepArg
     if (lane == 0) g.scal[at] = make_float4(a.scale2 / f, -kHigh * sum[0], -kHigh * sum[1], 0.0f);
 }
 
-// A walk over a CTA's segments; every warp has its own.
+// A walk over a CTA's segments; every warp has its own.  An item takes
+// kItemCost + units positions, of which the first kItemCost hold no tile.
 struct TileWalk {
     TileItem it;
-    int u, n;        // first tile (of the item's) and tiles of the segment
-    long long left;  // tiles of the range from the segment's first on
+    int u, n;        // first tile (of the item's) and tiles of the segment; n = 0: the end
+    long long left;  // positions of the range from the segment's first on
+    int from, span;  // where in the item they begin, and how many are the segment's
 
-    __device__ __forceinline__ void begin(const TileArgs& g, int b, int ctas, long long total) {
+    __device__ __forceinline__ void cut_at(const TileArgs& g, int position) {
+        from = position;
+        while (true) {
+            const int all = it.units + kItemCost;
+            span = (int)min((long long)(all - from), left);
+            u = max(from - kItemCost, 0);
+            n = max(from + span - kItemCost, 0) - u;
+            if (n > 0) return;
+            left -= span;
+            if (left <= 0) return;
+            step(g);
+            if (left <= 0) return;
+            from = 0;
+        }
+    }
+    __device__ __forceinline__ void step(const TileArgs& g) {  // to the next item
+        if (++it.h < g.a.p.H) return;
+        it.h = 0;
+        if (it.c + 1 < it.chunks) {
+            tile_chunk(g, it, it.c + 1);
+            return;
+        }
+        int s = it.s + 1;
+        while (s < g.a.b.n_seqs && !tile_seq(g, s, it)) ++s;
+        if (s >= g.a.b.n_seqs) left = 0, n = 0;
+        else tile_chunk(g, it, 0);
+    }
+    __device__ __forceinline__ void begin(const TileArgs& g, int b, const Cut& cut) {
         const int4 p = g.plan[b];
-        left = total / ctas + (b < total % ctas ? 1 : 0);
+        left = cut.begin(b + 1) - cut.begin(b);
         tile_seq(g, p.x, it);
         tile_chunk(g, it, p.y);
         it.h = p.z;
-        u = p.w;
-        n = (int)min((long long)(it.units - u), left);
+        cut_at(g, p.w);
     }
     __device__ __forceinline__ void next(const TileArgs& g) {
-        left -= n;
+        left -= span;
         n = 0;
         if (left <= 0) return;
-        u = 0;
-        if (++it.h == g.a.p.H) {
-            it.h = 0;
-            if (it.c + 1 < it.chunks) {
-                tile_chunk(g, it, it.c + 1);
-            } else {
-                int s = it.s + 1;
-                while (s < g.a.b.n_seqs && !tile_seq(g, s, it)) ++s;
-                if (s >= g.a.b.n_seqs) {
-                    left = 0;
-                    return;
-                }
-                tile_chunk(g, it, 0);
-            }
-        }
-        n = (int)min((long long)it.units, left);
+        step(g);
+        if (left > 0) cut_at(g, 0);
     }
 };
 
 template <int D, bool HAD>
 struct TileSmem {
     static constexpr int kTile = kTileTokens * D * 2;  // bytes of a K or V tile
-    static constexpr int kParts = HAD ? 2 : 1, kRows = item_rows(D, HAD), kUpper = kRows - kRowsM;
-    static constexpr int kQ0 = kRowsM * D * 2, kQ1 = kUpper * D * 2;  // bytes of a part of a half's queries
-    static constexpr int kPieces = D / 32;                            // 16-byte pieces of a token's codes
-    alignas(1024) uint8_t q[kParts * (kQ0 + kQ1)];                    // [half][high, low][64 channels][row]
+    alignas(1024) uint8_t q[2][HAD ? 2 : 1][kTile];    // [half][high, low][64 channels][row]
     alignas(1024) uint8_t ring[kRingTiles][kTile];
-    alignas(16) float par[2][3][kTileTokens];          // K scale times scale2, log2 and inverse of the V scale
+    alignas(16) float par[2][kTileTokens];             // K scale times scale2
+    alignas(16) uint32_t absent[2][4];                 // tokens of the tile that are not there, a bit each
+    alignas(16) uint32_t signs[D / 2];                 // sign bits of two channels' signs
     uint64_t full[kRingTiles], empty[kRingTiles];
     uint64_t par_full[2], par_empty[2];
     uint64_t q_full[2], s_full[2], w_full[2], o_full[2];
@@ -384,6 +423,11 @@ __device__ __forceinline__ uint64_t fma_f2(uint64_t x, uint64_t y, uint64_t z) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
     return r;
 }
+__device__ __forceinline__ uint64_t mul_f2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
 __device__ __forceinline__ uint64_t add_f2(uint64_t x, uint64_t y) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
@@ -393,31 +437,94 @@ __device__ __forceinline__ uint64_t add_f2(uint64_t x, uint64_t y) {
 // Four 16-byte pieces of a 128-byte-swizzled tile from 32 codes of one token:
 // channels 32 quarter .. + 31 (D = 128) of row `row`.  Of eight channels the
 // halves are in the order 0 4 1 5 2 6 3 7, as the queries' and O's are.
-template <int D>
-__device__ __forceinline__ void store_codes(uint8_t* tile, int row, int quarter, const uint4& w) {
+__device__ __forceinline__ uint32_t mul2(uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
+}
+template <int D, bool SCALED>
+__device__ __forceinline__ void store_codes(uint8_t* tile, int row, int quarter, const uint4& w, uint32_t scale) {
     const uint32_t words[4] = {w.x, w.y, w.z, w.w};
     uint8_t* base = tile + (quarter >> 1) * (kTileTokens * 128) + row * 128;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const uint32_t x = words[k], x8 = x >> 8;
         const int chunk = ((quarter & 1) * 4 + k) ^ (row & 7);
-        *reinterpret_cast<uint4*>(base + chunk * 16) =
-            make_uint4(codes_low(x), codes_upper(x), codes_low(x8), codes_upper(x8));
+        uint4 v = make_uint4(codes_low(x), codes_upper(x), codes_low(x8), codes_upper(x8));
+        if constexpr (SCALED) v = make_uint4(mul2(v.x, scale), mul2(v.y, scale), mul2(v.z, scale), mul2(v.w, scale));
+        *reinterpret_cast<uint4*>(base + chunk * 16) = v;
     }
 }
 // Order of eight channels in a 16-byte piece: place p holds channel place8(p).
 __host__ __device__ constexpr int place8(int p) { return (p >> 1) + 4 * (p & 1); }
 
-// Pages of the tile's tokens: this thread's token's slot, or -1.
-__device__ __forceinline__ long long tile_slot(const TileArgs& g, const TileItem& it, int tok) {
-    if (tok < it.t0 || tok >= it.t1) return -1;
-    return slot_of(g.a.b, g.a.p, it.s, tok);
-}
+// One producer group's part of the tiles: T threads, of which this is number
+// `me`.  Pages are looked up a tile ahead of the codes and scales, which are
+// on their way while the thread waits for the buffer.
+template <int D, int T, bool IS_V>
+struct Producer {
+    static constexpr int kPieces = D / 32, kAll = kTileTokens * kPieces, kMost = (kAll + T - 1) / T;
+    int me;
+    int page[kMost], page_s;  // as the table has them, of the pieces' tokens and (K) of the token whose scale this thread brings
+    uint4 w[kMost];
+    __half scale[kMost];
+    float sk;
+    bool absent;
+
+    __device__ __forceinline__ void pages(const TileArgs& g, const TileItem& it, int tok0) {
+        const int* row = g.a.b.table + (long long)it.s * g.a.b.table_stride;
+        const auto look = [&](int tok) { return tok >= it.t0 && tok < it.t1 ? row[tok >> g.a.p.page_log2] : 0; };
+#pragma unroll
+        for (int k = 0; k < kMost; ++k) page[k] = look(tok0 + min(me + k * T, kAll - 1) / kPieces);
+        if (!IS_V) page_s = look(tok0 + me);
+    }
+    // Index of token tok of the pool, or -1 (a refused page sets the error word).
+    __device__ __forceinline__ long long place(const TileArgs& g, int h, int t0, int t1, int tok, int pg) const {
+        const Pool& p = g.a.p;
+        if (tok < t0 || tok >= t1) return -1;
+        if (pg >= 0 && pg < p.n_pages)
+            return (((long long)pg * p.H + h) << p.page_log2) + (tok & ((1 << p.page_log2) - 1));
+        report_error(kErrRange);
+        return -1;
+    }
+    __device__ __forceinline__ void fetch(const TileArgs& g, int h, int t0, int t1, int tok0) {
+        const Pool& p = g.a.p;
+#pragma unroll
+        for (int k = 0; k < kMost; ++k) {
+            const int piece = min(me + k * T, kAll - 1);
+            const long long at = place(g, h, t0, t1, tok0 + piece / kPieces, page[k]);
+            w[k] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // zeros
+            if (IS_V) scale[k] = __float2half_rn(0.0f);
+            if (at >= 0) {
+                w[k] = reinterpret_cast<const uint4*>(p.codes[IS_V] + at * (D / 2))[piece % kPieces];
+                if (IS_V) scale[k] = p.tok[1][at];
+            }
+        }
+        if (!IS_V) {
+            const int tok = tok0 + me;
+            const long long at = place(g, h, t0, t1, tok, page_s);
+            absent = at < 0;
+            sk = absent ? 0.0f : __half2float(p.tok[0][at]) * g.a.scale2;
+        }
+    }
+    __device__ __forceinline__ void store(uint8_t* tile) const {
+#pragma unroll
+        for (int k = 0; k < kMost; ++k) {
+            const int piece = me + k * T;
+            uint32_t two = 0;
+            if constexpr (IS_V) {
+                const __half2 x = __half2half2(scale[k]);
+                two = *reinterpret_cast<const uint32_t*>(&x);
+            }
+            if (piece < kAll) store_codes<D, IS_V>(tile, piece / kPieces, piece % kPieces, w[k], two);
+        }
+    }
+};
 
 template <int D, bool HAD>
 __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g) {
     using S = TileSmem<D, HAD>;
-    constexpr int kTile = S::kTile, kSlab = kTileTokens * 128, kPieces = S::kPieces;
+    constexpr int kTile = S::kTile, kSlab = kTileTokens * 128;
     extern __shared__ __align__(1024) uint8_t tile_raw[];
     S& sm = *reinterpret_cast<S*>(tile_raw);
     const AttnArgs& a = g.a;
@@ -440,13 +547,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
     grid_dep_wait();
     grid_dep_launch();
     const long long total = g.seq_cost[a.b.n_seqs];
-    const int ctas = (int)min((long long)gridDim.x, total);
+    const int ctas = (int)min((long long)gridDim.x, max(total, 1ll));
+    const Cut cut(total, ctas);
+    if (threadIdx.x < D / 2)
+        sm.signs[threadIdx.x] = HAD && a.signs ? (a.signs[2 * threadIdx.x] < 0 ? 0x8000u : 0u) |
+                                                     (a.signs[2 * threadIdx.x + 1] < 0 ? 0x80000000u : 0u)
+                                               : 0u;
     if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
     const uint32_t tmem = sm.tmem;
-    const bool works = (int)blockIdx.x < ctas;
+    const bool works = (int)blockIdx.x < ctas && total > 0;
     // Waits give up after a while: results are void then, and every warp leaves its loop.
     const auto wait_one = [&](uint64_t* bar, uint32_t parity) {
         if (mbar_wait_1s(bar, parity, KVQ_WAIT_LIMIT(kTileWait))) return true;
@@ -462,38 +574,39 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
         const uint32_t ts = tmem + lanes + half * 128, to = tmem + lanes + 256 + half * 128;
         TileWalk wk;
-        wk.begin(g, blockIdx.x, ctas, total);
+        wk.begin(g, blockIdx.x, cut);
         uint32_t tile = 0;
         bool ok = true;
         for (uint32_t item = 0; ok && wk.n > 0; wk.next(g), ++item) {
             const TileItem& it = wk.it;
-            const int i = it.c * S::kRows + half * kRowsM + r;  // row of the kv head's queries
-            const bool stored = half == 0 || r < S::kUpper, there = stored && i < it.nq;
+            const int i = it.c * kItemRows + half * kRowsM + r;  // row of the kv head's queries
+            const bool there = i < it.nq;
             const int qr = i / a.G, row = it.lo + qr, head = it.h * a.G + i - qr * a.G;
             Range see{0, 0};
             float factor = 1.0f;
             {   // the query: rotated, split, into the tile
                 uint64_t v[D / 2];
-                uint32_t u[D / 2];
-#pragma unroll
-                for (int k = 0; k < D / 2; ++k) u[k] = 0;
+                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + row * a.q_row +
+                                                                  head * a.q_head);
                 if (there) {
-                    const uint8_t* src = reinterpret_cast<const uint8_t*>(static_cast<const uint16_t*>(a.q) +
-                                                                          row * a.q_row + head * a.q_head);
-                    load_words(src, u);
                     const long long n = max(it.len, 0), pos = (long long)it.base + row;
                     const long long t1 = min(a.causal ? min(pos + 1, n) : n, (long long)it.t1);
                     const long long t0 = a.causal && a.window > 0 ? max(pos - a.window + 1, 0ll) : 0;
                     if (t0 < t1) see = Range{(int)t0, (int)t1};
                 }
 #pragma unroll
-                for (int k = 0; k < D / 2; ++k) {
-                    float2 f = a.bf16 ? Elem<__nv_bfloat16>::wide(u[k]) : Elem<__half>::wide(u[k]);
-                    if (HAD && a.signs) {
-                        const char2 sg = reinterpret_cast<const char2*>(a.signs)[k];
-                        f.x *= sg.x, f.y *= sg.y;
+                for (int k = 0; k < D / 8; ++k) {
+                    uint4 u = there ? src[k] : make_uint4(0, 0, 0, 0);
+                    if constexpr (HAD) {
+                        const uint4 sg = *reinterpret_cast<const uint4*>(&sm.signs[4 * k]);
+                        u.x ^= sg.x, u.y ^= sg.y, u.z ^= sg.z, u.w ^= sg.w;
                     }
-                    v[k] = pair2(f.x, f.y);
+                    const uint32_t word[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 f = a.bf16 ? Elem<__nv_bfloat16>::wide(word[j]) : Elem<__half>::wide(word[j]);
+                        v[4 * k + j] = pair2(f.x, f.y);
+                    }
                 }
                 if constexpr (HAD) {
                     const uint64_t minus = pair2(-1.0f, -1.0f);
@@ -507,7 +620,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                                 v[k + x] = fma_f2(q, minus, p);
                             }
                 }
-                float m = 0.0f;
+                float m = 0.0f, bad = 0.0f;  // bad: NaN if anything is infinite or NaN
 #pragma unroll
                 for (int k = 0; k < D / 2; ++k) {
                     float x, y;
@@ -517,12 +630,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                         x = p, y = q;
                         v[k] = pair2(x, y);
                     }
-                    m = max_or_nan(max_or_nan(m, fabsf(x)), fabsf(y));
+                    bad = __fmaf_rn(x, 0.0f, __fmaf_rn(y, 0.0f, bad));
+                    m = fmaxf(m, fmaxf(fabsf(x), fabsf(y)));
                 }
+                if (bad != 0.0f) m = NAN;
                 // Rows in this range keep 22 bits in the two fp16 parts as they are; others are scaled.
                 if (!(m == 0.0f || (m >= 0x1p-4f && m <= 0x1p14f))) factor = query_scale(m);
-                const int slab = (half ? S::kUpper : kRowsM) * 128;
-                uint8_t* hi = sm.q + half * S::kParts * S::kQ0 + r * 128;
+                uint8_t* hi = sm.q[half][0] + r * 128;
 #pragma unroll
                 for (int k8 = 0; k8 < D / 8; ++k8) {
                     uint32_t wh[4], wl[4];
@@ -540,13 +654,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                             wl[k] = *reinterpret_cast<const uint32_t*>(&l);
                         }
                     }
-                    const int at = (k8 >> 3) * slab + ((k8 & 7) ^ (r & 7)) * 16;
-                    if (stored) {
-                        *reinterpret_cast<uint4*>(hi + at) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
-                        if constexpr (HAD)
-                            *reinterpret_cast<uint4*>(hi + (half ? S::kQ1 : S::kQ0) + at) =
-                                make_uint4(wl[0], wl[1], wl[2], wl[3]);
-                    }
+                    const int at = (k8 >> 3) * kSlab + ((k8 & 7) ^ (r & 7)) * 16;
+                    *reinterpret_cast<uint4*>(hi + at) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+                    if constexpr (HAD) *reinterpret_cast<uint4*>(hi + kTile + at) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
                 }
             }
             fence_proxy_async_smem();
@@ -559,12 +669,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
             const int see_hi = __reduce_min_sync(~0u, there ? see.t1 : 0x7FFFFFFF);
 
             float M = kLowest;
-            uint64_t l2 = pair2(0.0f, 0.0f);
+            uint64_t l2[2] = {pair2(0.0f, 0.0f), pair2(0.0f, 0.0f)};
             for (int n = 0; n < wk.n; ++n, ++tile) {
                 const int tok0 = (it.u0 + wk.u + n) * kTileTokens;
                 if (!(ok = wait(&sm.par_full[tile & 1], tile >> 1 & 1)) || !(ok = wait(&sm.s_full[half], tile & 1))) break;
                 tc_after_sync();
-                const float(*par)[kTileTokens] = sm.par[tile & 1];
+                const float* par = sm.par[tile & 1];
                 uint32_t s[4][32];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) tmem_load32(s[k], ts + 32 * k);
@@ -575,39 +685,46 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
 #pragma unroll
                         for (int c = 0; c < 32; ++c) s[k][c] = __float_as_uint(__uint_as_float(s[k][c]) * back);
                 }
-                float top = kLowest;
+                float top;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
-                        const float4 sk = *reinterpret_cast<const float4*>(&par[0][32 * k + c]);
-                        const float4 lv = *reinterpret_cast<const float4*>(&par[1][32 * k + c]);
-                        float y[4];
-                        unpair2(fma_f2(pair2(__uint_as_float(s[k][c]), __uint_as_float(s[k][c + 1])), pair2(sk.x, sk.y),
-                                       pair2(lv.x, lv.y)), y[0], y[1]);
-                        unpair2(fma_f2(pair2(__uint_as_float(s[k][c + 2]), __uint_as_float(s[k][c + 3])),
-                                       pair2(sk.z, sk.w), pair2(lv.z, lv.w)), y[2], y[3]);
+                    for (int c = 0; c < 32; c += 4) {  // x = S sigma scale
+                        const float4 sk = *reinterpret_cast<const float4*>(&par[32 * k + c]);
+                        float x[4];
+                        unpair2(mul_f2(pair2(__uint_as_float(s[k][c]), __uint_as_float(s[k][c + 1])), pair2(sk.x, sk.y)),
+                                x[0], x[1]);
+                        unpair2(mul_f2(pair2(__uint_as_float(s[k][c + 2]), __uint_as_float(s[k][c + 3])),
+                                       pair2(sk.z, sk.w)), x[2], x[3]);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) s[k][c + j] = __float_as_uint(y[j]);
+                        for (int j = 0; j < 4; ++j) s[k][c + j] = __float_as_uint(x[j]);
                     }
-                if (tok0 < see_lo || tok0 + kTileTokens > see_hi) {
-                    const int from = see.t0 - tok0, to_ = see.t1 - tok0;
+                const uint4 absent = *reinterpret_cast<const uint4*>(sm.absent[tile & 1]);
+                if (tok0 < see_lo || tok0 + kTileTokens > see_hi || (absent.x | absent.y | absent.z | absent.w)) {
+                    const uint32_t gone[4] = {absent.x, absent.y, absent.z, absent.w};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                    for (int k = 0; k < 4; ++k) {
+                        const int from = see.t0 - tok0 - 32 * k, to_ = see.t1 - tok0 - 32 * k;  // of these 32 tokens
+                        const uint32_t sees = (to_ >= 32 ? ~0u : to_ > 0 ? (1u << to_) - 1 : 0u) &
+                                              (from <= 0 ? ~0u : from < 32 ? ~0u << from : 0u) & ~gone[k];
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
-                            if (32 * k + c < from || 32 * k + c >= to_) s[k][c] = 0xFF800000u;  // -inf
+                            if (!(sees >> c & 1)) s[k][c] = 0xFF800000u;  // -inf
+                    }
                 }
+                float tops[4] = {kLowest, kLowest, kLowest, kLowest};
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
 #pragma unroll
                     for (int c = 0; c < 32; c += 2)
-                        top = fmaxf(top, fmaxf(__uint_as_float(s[k][c]), __uint_as_float(s[k][c + 1])));
+                        tops[k] = fmaxf(tops[k], fmaxf(__uint_as_float(s[k][c]), __uint_as_float(s[k][c + 1])));
+                top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 if (__any_sync(~0u, top > M + kSlack)) {
                     const float m2 = fmaxf(M, top), f = ex2(M - m2);
                     const uint64_t ff = pair2(f, f);
                     M = m2;
-                    l2 = fma_f2(l2, ff, pair2(0.0f, 0.0f));
+                    l2[0] = mul_f2(l2[0], ff);
+                    l2[1] = mul_f2(l2[1], ff);
                     if (n > 0) {
 #pragma unroll 1
                         for (int k = 0; k < D; k += 32) {
@@ -628,15 +745,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                     for (int e = 0; e < 2; ++e)
 #pragma unroll
                         for (int c = 0; c < 32; c += 4) {
-                            const float4 rv = *reinterpret_cast<const float4*>(&par[2][32 * (k + e) + c]);
                             float x[4];
                             const uint32_t* y = &s[k + e][c];
                             unpair2(add_f2(pair2(__uint_as_float(y[0]), __uint_as_float(y[1])), ref), x[0], x[1]);
                             unpair2(add_f2(pair2(__uint_as_float(y[2]), __uint_as_float(y[3])), ref), x[2], x[3]);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) x[j] = ex2(x[j]);
-                            l2 = fma_f2(pair2(x[0], x[1]), pair2(rv.x, rv.y), l2);
-                            l2 = fma_f2(pair2(x[2], x[3]), pair2(rv.z, rv.w), l2);
+                            l2[0] = add_f2(l2[0], pair2(x[0], x[1]));
+                            l2[1] = add_f2(l2[1], pair2(x[2], x[3]));
                             w[16 * e + c / 2] = Elem<__half>::pack(x[0], x[1]);
                             w[16 * e + c / 2 + 1] = Elem<__half>::pack(x[2], x[3]);
                         }
@@ -653,7 +769,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
             if (!ok || !(ok = wait(&sm.o_full[half], item & 1))) break;
             tc_after_sync();
             float la, lb;
-            unpair2(l2, la, lb);
+            unpair2(add_f2(l2[0], l2[1]), la, lb);
             const float l = la + lb;
             const bool begins = wk.u == 0, ends = wk.u + wk.n == it.units, whole = begins && ends;
             float o[D];
@@ -676,18 +792,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                     uint32_t w[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        float x = o[k + 2 * c] * unit, y = o[k + 2 * c + 1] * unit;
-                        if (HAD && a.signs) {
-                            const char2 sg = reinterpret_cast<const char2*>(a.signs)[k / 2 + c];
-                            x *= sg.x, y *= sg.y;
-                        }
+                        const float x = o[k + 2 * c] * unit, y = o[k + 2 * c + 1] * unit;
                         w[c] = a.bf16 ? Elem<__nv_bfloat16>::pack(x, y) : Elem<__half>::pack(x, y);
+                        if constexpr (HAD) w[c] ^= sm.signs[k / 2 + c];
                     }
                     if (there) *reinterpret_cast<uint4*>(dst + k) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
                 if (there && a.lse) a.lse[(long long)row * a.Hq + head] = (M - kTileBias + lg2(l)) * kLn2;
             } else if (there) {
-                const long long at = (2ll * blockIdx.x + (begins ? 1 : 0)) * kMaxItemRows + half * kRowsM + r;
+                const long long at = (2ll * blockIdx.x + (begins ? 1 : 0)) * kItemRows + half * kRowsM + r;
                 reinterpret_cast<float2*>(a.ml)[at] = make_float2(M + kSlack, l);
                 float4* dst = reinterpret_cast<float4*>(a.part + at * D);
 #pragma unroll
@@ -697,33 +810,29 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
             }
             if (begins && !ends && threadIdx.x == 0) {
                 // CTAs from this one to that of the item's last tile
-                const long long share = total / ctas, extra = total % ctas;
-                const long long x = share * blockIdx.x + min((long long)blockIdx.x, extra) + share +
-                                    (blockIdx.x < extra ? 1 : 0) - wk.left;
-                const long long last = x + it.units - 1, longer = (share + 1) * extra;
-                const long long b = last < longer ? last / (share + 1) : extra + (last - longer) / share;
-                a.meta[blockIdx.x] = make_int4(it.s, it.h, it.c * S::kRows, (int)(b - blockIdx.x) + 1);
+                const long long item = cut.begin(blockIdx.x + 1) - wk.left - wk.from;  // its first position
+                a.meta[blockIdx.x] = make_int4(it.s, it.h, it.c * kItemRows,
+                                               (int)(cut.of(item + kItemCost + it.units - 1) - blockIdx.x) + 1);
             }
         }
     } else if (works) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         TileWalk wk;
-        wk.begin(g, blockIdx.x, ctas, total);
+        wk.begin(g, blockIdx.x, cut);
         if (warp == 12) {
             // -------------------------------------------- products
             if (lane == 0) {
                 constexpr uint32_t kS = mma_desc(kTileTokens, false), kO = mma_desc(D, true);
                 uint32_t seq = 0, tile = 0;  // tiles of the ring taken (K, V, K, ..); steps
-                const uint32_t ring = smem_u32(sm.ring[0]), q = smem_u32(sm.q);
+                const uint32_t ring = smem_u32(sm.ring[0]), q = smem_u32(sm.q[0][0]);
                 const auto scores = [&](int half, uint32_t buf) {
 #pragma unroll
                     for (int part = 0; part < (HAD ? 2 : 1); ++part)
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t from = half ? S::kParts * S::kQ0 + part * S::kQ1 + (k >> 2) * S::kUpper * 128
-                                                       : part * S::kQ0 + (k >> 2) * kRowsM * 128;
-                            mma_ss(tmem + half * 128, smem_desc(q + from + (k & 3) * 32, 16),
-                                   smem_desc(ring + buf * kTile + (k >> 2) * kSlab + (k & 3) * 32, 16), kS, part + k > 0);
+                            const uint32_t at = (k >> 2) * kSlab + (k & 3) * 32;
+                            mma_ss(tmem + half * 128, smem_desc(q + (half * (HAD ? 2 : 1) + part) * kTile + at, 16),
+                                   smem_desc(ring + buf * kTile + at, 16), kS, part + k > 0);
                         }
                 };
                 const auto values = [&](int half, uint32_t buf, bool add) {
@@ -768,61 +877,42 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
             __syncwarp();
         } else {
             // -------------------------------------------- K (warps 8 .. 11) and V (13 .. 15) tiles
-            const bool is_v = warp > 12;
-            const int me = is_v ? threadIdx.x - 13 * 32 : threadIdx.x - 8 * 32, count = is_v ? 96 : 128;
-            constexpr int kMost = (kTileTokens * kPieces + 95) / 96;  // pieces a lane (V's three warps; K's four have less)
-            uint32_t seq = is_v ? 1 : 0, tile = 0;
-            bool ok = true;
-            for (; ok && wk.n > 0; wk.next(g)) {
-                const TileItem& it = wk.it;
-                for (int n = 0; n < wk.n && ok; ++n, ++tile, seq += 2) {
-                    const int tok0 = (it.u0 + wk.u + n) * kTileTokens;
+            const auto produce = [&](auto& pr, uint32_t seq, auto is_v) {
+                constexpr bool kV = decltype(is_v)::value;
+                int n = 0;
+                if (wk.n > 0) pr.pages(g, wk.it, (wk.it.u0 + wk.u) * kTileTokens);
+                for (uint32_t tile = 0; wk.n > 0; ++tile, seq += 2) {
                     const uint32_t buf = seq % kRingTiles, round = seq / kRingTiles;
-                    uint4 w[kMost];
-                    float p_sk = 0.0f, p_lv = -INFINITY, p_rv = 0.0f;
-                    if (!is_v) {
-                        const long long slot = tile_slot(g, it, tok0 + me);
-                        if (slot >= 0) {
-                            const long long at = slot + ((long long)it.h << a.p.page_log2);
-                            const float sv = fmaxf(__half2float(a.p.tok[1][at]), 0x1p-24f);
-                            p_sk = __half2float(a.p.tok[0][at]) * a.scale2;
-                            p_lv = lg2(sv);
-                            p_rv = rcp(sv);
-                        }
+                    pr.fetch(g, wk.it.h, wk.it.t0, wk.it.t1, (wk.it.u0 + wk.u + n) * kTileTokens);
+                    if (++n == wk.n) {
+                        wk.next(g);
+                        n = 0;
                     }
-                    int pieces = 0;
-#pragma unroll
-                    for (int k = 0; k < kMost; ++k) {
-                        const int piece = me + k * count;
-                        w[k] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-                        if (piece < kTileTokens * kPieces) {
-                            const int tok = tok0 + piece / kPieces;
-                            const long long slot = tile_slot(g, it, tok);
-                            if (slot >= 0)
-                                w[k] = reinterpret_cast<const uint4*>(
-                                    a.p.codes[is_v] + (slot + ((long long)it.h << a.p.page_log2)) * (D / 2))[piece % kPieces];
-                            pieces = k + 1;
-                        }
+                    if (wk.n > 0) pr.pages(g, wk.it, (wk.it.u0 + wk.u + n) * kTileTokens);
+                    if (round > 0 && !wait(&sm.empty[buf], (round - 1) & 1)) return;
+                    if constexpr (!kV) {
+                        if (tile >= 2 && !wait(&sm.par_empty[tile & 1], ((tile >> 1) - 1) & 1)) return;
+                        sm.par[tile & 1][pr.me] = pr.sk;
+                        const uint32_t absent = __ballot_sync(~0u, pr.absent);
+                        if (lane == 0) sm.absent[tile & 1][warp - 8] = absent;
                     }
-                    if (round > 0 && !(ok = wait(&sm.empty[buf], (round - 1) & 1))) break;
-                    if (!is_v) {
-                        if (tile >= 2 && !(ok = wait(&sm.par_empty[tile & 1], ((tile >> 1) - 1) & 1))) break;
-                        sm.par[tile & 1][0][me] = p_sk;
-                        sm.par[tile & 1][1][me] = p_lv;
-                        sm.par[tile & 1][2][me] = p_rv;
-                    }
-#pragma unroll
-                    for (int k = 0; k < kMost; ++k) {
-                        const int piece = me + k * count;
-                        if (k < pieces) store_codes<D>(sm.ring[buf], piece / kPieces, piece % kPieces, w[k]);
-                    }
+                    pr.store(sm.ring[buf]);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(&sm.full[buf], warp == 13 ? 2 : 1);
-                        if (!is_v) mbar_arrive(&sm.par_full[tile & 1]);
+                        if (!kV) mbar_arrive(&sm.par_full[tile & 1]);
                     }
                 }
+            };
+            if (warp > 12) {
+                Producer<D, 96, true> pr;
+                pr.me = threadIdx.x - 13 * 32;
+                produce(pr, 1, std::true_type{});
+            } else {
+                Producer<D, 128, false> pr;
+                pr.me = threadIdx.x - 8 * 32;
+                produce(pr, 0, std::false_type{});
             }
         }
     }
