@@ -47,7 +47,7 @@ constexpr int kRingTiles = 3;
 constexpr float kSlack = 8.0f;               // how far a row's maximum may pass its reference
 constexpr float kTileBias = kBias - kSlack;  // w = 2^(y - M + kTileBias) stays in fp16
 constexpr uint32_t kTileWait = 1u << 22;  // polls, of a second at most together
-constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;  // 256 threads each: the 128 a thread of the launch
+constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;  // 256 threads each: the 128 a thread of the launch
 
 struct TileArgs {
     AttnArgs a;
@@ -329,6 +329,7 @@ struct TileSmem {
     uint64_t par_full[2], par_empty[2];
     uint64_t q_full[2], s_full[2], w_full[2], o_full[2];
     uint32_t tmem;
+    TileWalk walk[kTileThreads / 32];                  // each warp's place in the work
 };
 
 // ---------------------------------------------------------------- tcgen05
@@ -406,6 +407,13 @@ __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -478,12 +486,12 @@ struct Producer {
         for (int k = 0; k < kMost; ++k) page[k] = look(tok0 + min(me + k * T, kAll - 1) / kPieces);
         if (!IS_V) page_s = look(tok0 + me);
     }
-    // Index of token tok of the pool, or -1 (a refused page sets the error word).
-    __device__ __forceinline__ long long place(const TileArgs& g, int h, int t0, int t1, int tok, int pg) const {
+    // Index of token tok in the pool (below 2^31), or -1 (a refused page sets the error word).
+    __device__ __forceinline__ int place(const TileArgs& g, int h, int t0, int t1, int tok, int pg) const {
         const Pool& p = g.a.p;
         if (tok < t0 || tok >= t1) return -1;
         if (pg >= 0 && pg < p.n_pages)
-            return (((long long)pg * p.H + h) << p.page_log2) + (tok & ((1 << p.page_log2) - 1));
+            return ((pg * p.H + h) << p.page_log2) + (tok & ((1 << p.page_log2) - 1));
         report_error(kErrRange);
         return -1;
     }
@@ -492,17 +500,17 @@ struct Producer {
 #pragma unroll
         for (int k = 0; k < kMost; ++k) {
             const int piece = min(me + k * T, kAll - 1);
-            const long long at = place(g, h, t0, t1, tok0 + piece / kPieces, page[k]);
+            const int at = place(g, h, t0, t1, tok0 + piece / kPieces, page[k]);
             w[k] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // zeros
             if (IS_V) scale[k] = __float2half_rn(0.0f);
             if (at >= 0) {
-                w[k] = reinterpret_cast<const uint4*>(p.codes[IS_V] + at * (D / 2))[piece % kPieces];
+                w[k] = reinterpret_cast<const uint4*>(p.codes[IS_V])[(uint32_t)at * (uint64_t)kPieces + piece % kPieces];
                 if (IS_V) scale[k] = p.tok[1][at];
             }
         }
         if (!IS_V) {
             const int tok = tok0 + me;
-            const long long at = place(g, h, t0, t1, tok, page_s);
+            const int at = place(g, h, t0, t1, tok, page_s);
             absent = at < 0;
             sk = absent ? 0.0f : __half2float(p.tok[0][at]) * g.a.scale2;
         }
@@ -565,6 +573,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
         report_error(kErrBarrierTimeout);
         return false;
     };
+    TileWalk& wk = sm.walk[warp];
+    const auto advance = [&] {
+        __syncwarp();
+        if (lane == 0) wk.next(g);
+        __syncwarp();
+    };
+    if (works && lane == 0) wk.begin(g, blockIdx.x, cut);
+    __syncwarp();
     const auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(~0u, wait_one(bar, parity)) != 0; };
 
     if (works && warp < 8) {
@@ -573,18 +589,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
         const int half = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
         const uint32_t ts = tmem + lanes + half * 128, to = tmem + lanes + 256 + half * 128;
-        TileWalk wk;
-        wk.begin(g, blockIdx.x, cut);
         uint32_t tile = 0;
         bool ok = true;
-        for (uint32_t item = 0; ok && wk.n > 0; wk.next(g), ++item) {
+        for (uint32_t item = 0; ok && wk.n > 0; advance(), ++item) {
             const TileItem& it = wk.it;
-            const int i = it.c * kItemRows + half * kRowsM + r;  // row of the kv head's queries
-            const bool there = i < it.nq;
-            const int qr = i / a.G, row = it.lo + qr, head = it.h * a.G + i - qr * a.G;
-            Range see{0, 0};
+            Range see{0, 0x7FFFFFFF};  // rows that are not there count as seeing all
             float factor = 1.0f;
             {   // the query: rotated, split, into the tile
+                const int i = it.c * kItemRows + half * kRowsM + r;  // row of the kv head's queries
+                const bool there = i < it.nq;
+                const int qr = i / a.G, row = it.lo + qr, head = it.h * a.G + i - qr * a.G;
                 uint64_t v[D / 2];
                 const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + row * a.q_row +
                                                                   head * a.q_head);
@@ -592,7 +606,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                     const long long n = max(it.len, 0), pos = (long long)it.base + row;
                     const long long t1 = min(a.causal ? min(pos + 1, n) : n, (long long)it.t1);
                     const long long t0 = a.causal && a.window > 0 ? max(pos - a.window + 1, 0ll) : 0;
-                    if (t0 < t1) see = Range{(int)t0, (int)t1};
+                    see = t0 < t1 ? Range{(int)t0, (int)t1} : Range{0, 0};
                 }
 #pragma unroll
                 for (int k = 0; k < D / 8; ++k) {
@@ -664,14 +678,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
             if (lane == 0) mbar_arrive(&sm.q_full[half]);
             const bool scaled = __any_sync(~0u, factor != 1.0f);
             const float back = 1.0f / factor;
-            // tokens that all rows of the warp see (rows that are not there count as seeing all)
-            const int see_lo = __reduce_max_sync(~0u, there ? see.t0 : 0);
-            const int see_hi = __reduce_min_sync(~0u, there ? see.t1 : 0x7FFFFFFF);
+            const int see_lo = __reduce_max_sync(~0u, see.t0), see_hi = __reduce_min_sync(~0u, see.t1);  // all rows of the warp
 
+            const int tiles = wk.n, first = (it.u0 + wk.u) * kTileTokens;
             float M = kLowest;
             uint64_t l2[2] = {pair2(0.0f, 0.0f), pair2(0.0f, 0.0f)};
-            for (int n = 0; n < wk.n; ++n, ++tile) {
-                const int tok0 = (it.u0 + wk.u + n) * kTileTokens;
+            for (int n = 0; n < tiles; ++n, ++tile) {
+                const int tok0 = first + n * kTileTokens;
                 if (!(ok = wait(&sm.par_full[tile & 1], tile >> 1 & 1)) || !(ok = wait(&sm.s_full[half], tile & 1))) break;
                 tc_after_sync();
                 const float* par = sm.par[tile & 1];
@@ -739,24 +752,22 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                 }
                 const uint64_t ref = pair2(kTileBias - M, kTileBias - M);
 #pragma unroll
-                for (int k = 0; k < 4; k += 2) {
-                    uint32_t w[32];
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t w[16];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
+                    for (int c = 0; c < 32; c += 4) {
+                        const uint32_t* x = &s[k][c];
+                        float p[4];
+                        unpair2(add_f2(pair2(__uint_as_float(x[0]), __uint_as_float(x[1])), ref), p[0], p[1]);
+                        unpair2(add_f2(pair2(__uint_as_float(x[2]), __uint_as_float(x[3])), ref), p[2], p[3]);
 #pragma unroll
-                        for (int c = 0; c < 32; c += 4) {
-                            float x[4];
-                            const uint32_t* y = &s[k + e][c];
-                            unpair2(add_f2(pair2(__uint_as_float(y[0]), __uint_as_float(y[1])), ref), x[0], x[1]);
-                            unpair2(add_f2(pair2(__uint_as_float(y[2]), __uint_as_float(y[3])), ref), x[2], x[3]);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) x[j] = ex2(x[j]);
-                            l2[0] = add_f2(l2[0], pair2(x[0], x[1]));
-                            l2[1] = add_f2(l2[1], pair2(x[2], x[3]));
-                            w[16 * e + c / 2] = Elem<__half>::pack(x[0], x[1]);
-                            w[16 * e + c / 2 + 1] = Elem<__half>::pack(x[2], x[3]);
-                        }
-                    tmem_store32(ts + 16 * k, w);
+                        for (int j = 0; j < 4; ++j) p[j] = ex2(p[j]);
+                        l2[0] = add_f2(l2[0], pair2(p[0], p[1]));
+                        l2[1] = add_f2(l2[1], pair2(p[2], p[3]));
+                        w[c / 2] = Elem<__half>::pack(p[0], p[1]);
+                        w[c / 2 + 1] = Elem<__half>::pack(p[2], p[3]);
+                    }
+                    tmem_store16(ts + 16 * k, w);
                 }
                 tmem_wait_store();
                 tc_before_sync();
@@ -768,6 +779,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
             }
             if (!ok || !(ok = wait(&sm.o_full[half], item & 1))) break;
             tc_after_sync();
+            const int i = it.c * kItemRows + half * kRowsM + r;
+            const bool there = i < it.nq;
+            const int row = it.lo + i / a.G, head = it.h * a.G + i % a.G;
             float la, lb;
             unpair2(add_f2(l2[0], l2[1]), la, lb);
             const float l = la + lb;
@@ -817,8 +831,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
         }
     } else if (works) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        TileWalk wk;
-        wk.begin(g, blockIdx.x, cut);
         if (warp == 12) {
             // -------------------------------------------- products
             if (lane == 0) {
@@ -885,7 +897,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                     const uint32_t buf = seq % kRingTiles, round = seq / kRingTiles;
                     pr.fetch(g, wk.it.h, wk.it.t0, wk.it.t1, (wk.it.u0 + wk.u + n) * kTileTokens);
                     if (++n == wk.n) {
-                        wk.next(g);
+                        advance();
                         n = 0;
                     }
                     if (wk.n > 0) pr.pages(g, wk.it, (wk.it.u0 + wk.u + n) * kTileTokens);
