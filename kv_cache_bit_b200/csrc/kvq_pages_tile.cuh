@@ -31,8 +31,6 @@
 // scales it there (its O is at rest between its S and its W).
 #pragma once
 
-#include <type_traits>
-
 #include "kvq_pages_attn.cuh"
 #include "kvq_pages_step.cuh"
 
@@ -47,7 +45,7 @@ constexpr int kRingTiles = 3;
 constexpr float kSlack = 8.0f;               // how far a row's maximum may pass its reference
 constexpr float kTileBias = kBias - kSlack;  // w = 2^(y - M + kTileBias) stays in fp16
 constexpr uint32_t kTileWait = 1u << 22;  // polls, of a second at most together
-constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;  // 256 threads each: the 128 a thread of the launch
+constexpr int kSoftmaxRegs = 160, kOtherRegs = 96;  // 256 threads each: the 128 a thread of the launch
 
 struct TileArgs {
     AttnArgs a;
@@ -407,13 +405,6 @@ __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
-__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -450,7 +441,7 @@ __device__ __forceinline__ uint32_t mul2(uint32_t x, uint32_t y) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
     return r;
 }
-template <int D, bool SCALED>
+template <int D>
 __device__ __forceinline__ void store_codes(uint8_t* tile, int row, int quarter, const uint4& w, uint32_t scale) {
     const uint32_t words[4] = {w.x, w.y, w.z, w.w};
     uint8_t* base = tile + (quarter >> 1) * (kTileTokens * 128) + row * 128;
@@ -459,21 +450,24 @@ __device__ __forceinline__ void store_codes(uint8_t* tile, int row, int quarter,
         const uint32_t x = words[k], x8 = x >> 8;
         const int chunk = ((quarter & 1) * 4 + k) ^ (row & 7);
         uint4 v = make_uint4(codes_low(x), codes_upper(x), codes_low(x8), codes_upper(x8));
-        if constexpr (SCALED) v = make_uint4(mul2(v.x, scale), mul2(v.y, scale), mul2(v.z, scale), mul2(v.w, scale));
+        v = make_uint4(mul2(v.x, scale), mul2(v.y, scale), mul2(v.z, scale), mul2(v.w, scale));
         *reinterpret_cast<uint4*>(base + chunk * 16) = v;
     }
 }
 // Order of eight channels in a 16-byte piece: place p holds channel place8(p).
 __host__ __device__ constexpr int place8(int p) { return (p >> 1) + 4 * (p & 1); }
 
-// One producer group's part of the tiles: T threads, of which this is number
-// `me`.  Pages are looked up a tile ahead of the codes and scales, which are
-// on their way while the thread waits for the buffer.
-template <int D, int T, bool IS_V>
+// A producer group's part of the tiles: T threads (K: 128, V: 96), of which
+// this is number `me`.  Pages are looked up a tile ahead of the codes and
+// scales, which are on their way while the thread waits for the buffer.  K and
+// V share the code (K's codes are multiplied by 1): the instruction cache
+// holds the loops of all roles, and hardly more.
+template <int D>
 struct Producer {
-    static constexpr int kPieces = D / 32, kAll = kTileTokens * kPieces, kMost = (kAll + T - 1) / T;
-    int me;
-    int page[kMost], page_s;  // as the table has them, of the pieces' tokens and (K) of the token whose scale this thread brings
+    static constexpr int kPieces = D / 32, kAll = kTileTokens * kPieces, kMost = (kAll + 95) / 96;
+    int me, T, is_v;
+    const uint8_t* codes;
+    int page[kMost], page_s;  // as the table has them: of the pieces' tokens, and of the token whose K scale this thread brings
     uint4 w[kMost];
     __half scale[kMost];
     float sk;
@@ -481,10 +475,11 @@ struct Producer {
 
     __device__ __forceinline__ void pages(const TileArgs& g, const TileItem& it, int tok0) {
         const int* row = g.a.b.table + (long long)it.s * g.a.b.table_stride;
-        const auto look = [&](int tok) { return tok >= it.t0 && tok < it.t1 ? row[tok >> g.a.p.page_log2] : 0; };
+        const int t0 = it.t0, t1 = it.t1;
+        const auto look = [&](int tok) { return tok >= t0 && tok < t1 ? row[tok >> g.a.p.page_log2] : 0; };
 #pragma unroll
         for (int k = 0; k < kMost; ++k) page[k] = look(tok0 + min(me + k * T, kAll - 1) / kPieces);
-        if (!IS_V) page_s = look(tok0 + me);
+        page_s = look(tok0 + me);
     }
     // Index of token tok in the pool (below 2^31), or -1 (a refused page sets the error word).
     __device__ __forceinline__ int place(const TileArgs& g, int h, int t0, int t1, int tok, int pg) const {
@@ -502,29 +497,26 @@ struct Producer {
             const int piece = min(me + k * T, kAll - 1);
             const int at = place(g, h, t0, t1, tok0 + piece / kPieces, page[k]);
             w[k] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // zeros
-            if (IS_V) scale[k] = __float2half_rn(0.0f);
+            scale[k] = __ushort_as_half(0x3C00);
             if (at >= 0) {
-                w[k] = reinterpret_cast<const uint4*>(p.codes[IS_V])[(uint32_t)at * (uint64_t)kPieces + piece % kPieces];
-                if (IS_V) scale[k] = p.tok[1][at];
+                w[k] = reinterpret_cast<const uint4*>(codes)[(uint32_t)at * (uint64_t)kPieces + piece % kPieces];
+                if (is_v) scale[k] = p.tok[1][at];
             }
         }
-        if (!IS_V) {
-            const int tok = tok0 + me;
-            const int at = place(g, h, t0, t1, tok, page_s);
+        if (!is_v) {
+            const int at = place(g, h, t0, t1, tok0 + me, page_s);
             absent = at < 0;
-            sk = absent ? 0.0f : __half2float(p.tok[0][at]) * g.a.scale2;
+            // (never 0: a score of -inf stays -inf; a zero vector's scores are 0 all the same)
+            sk = absent ? 1.0f : fmaxf(__half2float(p.tok[0][at]) * g.a.scale2, 1e-37f);
         }
     }
     __device__ __forceinline__ void store(uint8_t* tile) const {
 #pragma unroll
         for (int k = 0; k < kMost; ++k) {
             const int piece = me + k * T;
-            uint32_t two = 0;
-            if constexpr (IS_V) {
-                const __half2 x = __half2half2(scale[k]);
-                two = *reinterpret_cast<const uint32_t*>(&x);
-            }
-            if (piece < kAll) store_codes<D, IS_V>(tile, piece / kPieces, piece % kPieces, w[k], two);
+            const __half2 two = __half2half2(scale[k]);
+            if (piece < kAll)
+                store_codes<D>(tile, piece / kPieces, piece % kPieces, w[k], *reinterpret_cast<const uint32_t*>(&two));
         }
     }
 };
@@ -688,50 +680,49 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                 if (!(ok = wait(&sm.par_full[tile & 1], tile >> 1 & 1)) || !(ok = wait(&sm.s_full[half], tile & 1))) break;
                 tc_after_sync();
                 const float* par = sm.par[tile & 1];
-                uint32_t s[4][32];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) tmem_load32(s[k], ts + 32 * k);
-                tmem_wait_load();
-                if (scaled) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) s[k][c] = __float_as_uint(__uint_as_float(s[k][c]) * back);
-                }
-                float top;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int c = 0; c < 32; c += 4) {  // x = S sigma scale
-                        const float4 sk = *reinterpret_cast<const float4*>(&par[32 * k + c]);
-                        float x[4];
-                        unpair2(mul_f2(pair2(__uint_as_float(s[k][c]), __uint_as_float(s[k][c + 1])), pair2(sk.x, sk.y)),
-                                x[0], x[1]);
-                        unpair2(mul_f2(pair2(__uint_as_float(s[k][c + 2]), __uint_as_float(s[k][c + 3])),
-                                       pair2(sk.z, sk.w)), x[2], x[3]);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) s[k][c + j] = __float_as_uint(x[j]);
-                    }
                 const uint4 absent = *reinterpret_cast<const uint4*>(sm.absent[tile & 1]);
-                if (tok0 < see_lo || tok0 + kTileTokens > see_hi || (absent.x | absent.y | absent.z | absent.w)) {
-                    const uint32_t gone[4] = {absent.x, absent.y, absent.z, absent.w};
-#pragma unroll
+                if (scaled || tok0 < see_lo || tok0 + kTileTokens > see_hi ||
+                    (absent.x | absent.y | absent.z | absent.w)) {
+                    // scores that are not plain: scaled rows, tokens that a row does not see
+#pragma unroll 1
                     for (int k = 0; k < 4; ++k) {
                         const int from = see.t0 - tok0 - 32 * k, to_ = see.t1 - tok0 - 32 * k;  // of these 32 tokens
                         const uint32_t sees = (to_ >= 32 ? ~0u : to_ > 0 ? (1u << to_) - 1 : 0u) &
-                                              (from <= 0 ? ~0u : from < 32 ? ~0u << from : 0u) & ~gone[k];
+                                              (from <= 0 ? ~0u : from < 32 ? ~0u << from : 0u) &
+                                              ~sm.absent[tile & 1][k];
+                        uint32_t s[32];
+                        tmem_load32(s, ts + 32 * k);
+                        tmem_wait_load();
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
-                            if (!(sees >> c & 1)) s[k][c] = 0xFF800000u;  // -inf
+                            s[c] = sees >> c & 1 ? __float_as_uint(__uint_as_float(s[c]) * back) : 0xFF800000u;  // -inf
+                        tmem_store32(ts + 32 * k, s);
                     }
+                    tmem_wait_store();
                 }
-                float tops[4] = {kLowest, kLowest, kLowest, kLowest};
+                float top = kLowest;
+#pragma unroll 1
+                for (int k = 0; k < kTileTokens; k += 64) {
+                    uint32_t s[2][32];
+                    tmem_load32(s[0], ts + k);
+                    tmem_load32(s[1], ts + k + 32);
+                    tmem_wait_load();
+                    float tops[2] = {kLowest, kLowest};
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                    for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int c = 0; c < 32; c += 2)
-                        tops[k] = fmaxf(tops[k], fmaxf(__uint_as_float(s[k][c]), __uint_as_float(s[k][c + 1])));
-                top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                        for (int c = 0; c < 32; c += 4) {  // x = S sigma scale
+                            const float4 sk = *reinterpret_cast<const float4*>(&par[k + 32 * e + c]);
+                            float x[4];
+                            unpair2(mul_f2(pair2(__uint_as_float(s[e][c]), __uint_as_float(s[e][c + 1])),
+                                           pair2(sk.x, sk.y)), x[0], x[1]);
+                            unpair2(mul_f2(pair2(__uint_as_float(s[e][c + 2]), __uint_as_float(s[e][c + 3])),
+                                           pair2(sk.z, sk.w)), x[2], x[3]);
+                            tops[e] = fmaxf(tops[e], fmaxf(x[0], x[1]));
+                            tops[e] = fmaxf(tops[e], fmaxf(x[2], x[3]));
+                        }
+                    top = fmaxf(top, fmaxf(tops[0], tops[1]));
+                }
                 if (__any_sync(~0u, top > M + kSlack)) {
                     const float m2 = fmaxf(M, top), f = ex2(M - m2);
                     const uint64_t ff = pair2(f, f);
@@ -751,23 +742,31 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                     }
                 }
                 const uint64_t ref = pair2(kTileBias - M, kTileBias - M);
+                // (the probabilities of 64 tokens take the place of the scores of 32 that were read before)
+#pragma unroll 1
+                for (int k = 0; k < kTileTokens; k += 64) {
+                    uint32_t s[2][32], w[32];
+                    tmem_load32(s[0], ts + k);
+                    tmem_load32(s[1], ts + k + 32);
+                    tmem_wait_load();
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t w[16];
+                    for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
-                        const uint32_t* x = &s[k][c];
-                        float p[4];
-                        unpair2(add_f2(pair2(__uint_as_float(x[0]), __uint_as_float(x[1])), ref), p[0], p[1]);
-                        unpair2(add_f2(pair2(__uint_as_float(x[2]), __uint_as_float(x[3])), ref), p[2], p[3]);
+                        for (int c = 0; c < 32; c += 4) {
+                            const float4 sk = *reinterpret_cast<const float4*>(&par[k + 32 * e + c]);
+                            float p[4];
+                            unpair2(fma_f2(pair2(__uint_as_float(s[e][c]), __uint_as_float(s[e][c + 1])),
+                                           pair2(sk.x, sk.y), ref), p[0], p[1]);
+                            unpair2(fma_f2(pair2(__uint_as_float(s[e][c + 2]), __uint_as_float(s[e][c + 3])),
+                                           pair2(sk.z, sk.w), ref), p[2], p[3]);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) p[j] = ex2(p[j]);
-                        l2[0] = add_f2(l2[0], pair2(p[0], p[1]));
-                        l2[1] = add_f2(l2[1], pair2(p[2], p[3]));
-                        w[c / 2] = Elem<__half>::pack(p[0], p[1]);
-                        w[c / 2 + 1] = Elem<__half>::pack(p[2], p[3]);
-                    }
-                    tmem_store16(ts + 16 * k, w);
+                            for (int j = 0; j < 4; ++j) p[j] = ex2(p[j]);
+                            l2[0] = add_f2(l2[0], pair2(p[0], p[1]));
+                            l2[1] = add_f2(l2[1], pair2(p[2], p[3]));
+                            w[16 * e + c / 2] = Elem<__half>::pack(p[0], p[1]);
+                            w[16 * e + c / 2 + 1] = Elem<__half>::pack(p[2], p[3]);
+                        }
+                    tmem_store32(ts + k / 2, w);
                 }
                 tmem_wait_store();
                 tc_before_sync();
@@ -889,42 +888,36 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
             __syncwarp();
         } else {
             // -------------------------------------------- K (warps 8 .. 11) and V (13 .. 15) tiles
-            const auto produce = [&](auto& pr, uint32_t seq, auto is_v) {
-                constexpr bool kV = decltype(is_v)::value;
-                int n = 0;
-                if (wk.n > 0) pr.pages(g, wk.it, (wk.it.u0 + wk.u) * kTileTokens);
-                for (uint32_t tile = 0; wk.n > 0; ++tile, seq += 2) {
-                    const uint32_t buf = seq % kRingTiles, round = seq / kRingTiles;
-                    pr.fetch(g, wk.it.h, wk.it.t0, wk.it.t1, (wk.it.u0 + wk.u + n) * kTileTokens);
-                    if (++n == wk.n) {
-                        advance();
-                        n = 0;
-                    }
-                    if (wk.n > 0) pr.pages(g, wk.it, (wk.it.u0 + wk.u + n) * kTileTokens);
-                    if (round > 0 && !wait(&sm.empty[buf], (round - 1) & 1)) return;
-                    if constexpr (!kV) {
-                        if (tile >= 2 && !wait(&sm.par_empty[tile & 1], ((tile >> 1) - 1) & 1)) return;
-                        sm.par[tile & 1][pr.me] = pr.sk;
-                        const uint32_t absent = __ballot_sync(~0u, pr.absent);
-                        if (lane == 0) sm.absent[tile & 1][warp - 8] = absent;
-                    }
-                    pr.store(sm.ring[buf]);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&sm.full[buf], warp == 13 ? 2 : 1);
-                        if (!kV) mbar_arrive(&sm.par_full[tile & 1]);
-                    }
+            Producer<D> pr;
+            pr.is_v = warp > 12;
+            pr.T = pr.is_v ? 96 : 128;
+            pr.me = threadIdx.x - (pr.is_v ? 13 : 8) * 32;
+            pr.codes = a.p.codes[pr.is_v];
+            int n = 0;
+            if (wk.n > 0) pr.pages(g, wk.it, (wk.it.u0 + wk.u) * kTileTokens);
+            uint32_t seq = pr.is_v;
+            for (uint32_t tile = 0; wk.n > 0; ++tile, seq += 2) {
+                const uint32_t buf = seq % kRingTiles, round = seq / kRingTiles;
+                pr.fetch(g, wk.it.h, wk.it.t0, wk.it.t1, (wk.it.u0 + wk.u + n) * kTileTokens);
+                if (++n == wk.n) {
+                    advance();
+                    n = 0;
                 }
-            };
-            if (warp > 12) {
-                Producer<D, 96, true> pr;
-                pr.me = threadIdx.x - 13 * 32;
-                produce(pr, 1, std::true_type{});
-            } else {
-                Producer<D, 128, false> pr;
-                pr.me = threadIdx.x - 8 * 32;
-                produce(pr, 0, std::false_type{});
+                if (wk.n > 0) pr.pages(g, wk.it, (wk.it.u0 + wk.u + n) * kTileTokens);
+                if (round > 0 && !wait(&sm.empty[buf], (round - 1) & 1)) break;
+                if (!pr.is_v) {
+                    if (tile >= 2 && !wait(&sm.par_empty[tile & 1], ((tile >> 1) - 1) & 1)) break;
+                    sm.par[tile & 1][pr.me] = pr.sk;
+                    const uint32_t absent = __ballot_sync(~0u, pr.absent);
+                    if (lane == 0) sm.absent[tile & 1][warp - 8] = absent;
+                }
+                pr.store(sm.ring[buf]);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sm.full[buf], warp == 13 ? 2 : 1);
+                    if (!pr.is_v) mbar_arrive(&sm.par_full[tile & 1]);
+                }
             }
         }
     }
