@@ -277,7 +277,7 @@ kvq_status launch_tiles(const TileArgs& t, int sms, cudaStream_t st) {
     static const bool fits = [&] {
         cudaFuncAttributes at;
         return cudaFuncGetAttributes(&at, kernel) == cudaSuccess &&
-               at.numRegs * kTileThreads >= (kSoftmaxRegs + kOtherRegs) * kTileThreads / 2;
+               at.numRegs >= kLaunchRegs;
     }();
     if (!fits) return KVQ_ERR_CUDA;
     const kvq_status s = launch(kernel, dim3(sms), kTileThreads, smem, st, t);

@@ -11,9 +11,9 @@
 // A CTA (one an SM):
 //   warps 0 .. 3, 4 .. 7   softmax of the lower and the upper 128 rows, one row a
 //                          thread; they also bring in the queries and finish rows
-//   warps 8 .. 11          K: codes from global memory to fp16 tiles; scales
-//   warp 12                issues the products
-//   warps 13 .. 15         V
+//   warps 8 .. 14          codes from global memory to the fp16 tiles of K and V,
+//                          16 tokens at a time in turn; scales
+//   warp 15                issues the products
 // Products a step, rows X: S_X = Q_X K^T (for rotated queries twice, the high
 // and the low fp16 part: 22 bits of the query are kept), then O_X += W_X V with
 // W_X, fp16, taken from tensor memory, where it lies over S_X.  The order
@@ -45,7 +45,10 @@ constexpr int kRingTiles = 3;
 constexpr float kSlack = 8.0f;               // how far a row's maximum may pass its reference
 constexpr float kTileBias = kBias - kSlack;  // w = 2^(y - M + kTileBias) stays in fp16
 constexpr uint32_t kTileWait = 1u << 22;  // polls, of a second at most together
-constexpr int kSoftmaxRegs = 160, kOtherRegs = 96;  // 256 threads each: the 128 a thread of the launch
+// Registers a thread; the launch gives 128.
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 160, kProducerRegs = 96;
+static_assert(256 * (kSoftmaxRegs + kProducerRegs) <= kTileThreads * kLaunchRegs);
+constexpr int kProducers = 7;
 
 struct TileArgs {
     AttnArgs a;
@@ -321,7 +324,7 @@ struct TileSmem {
     alignas(1024) uint8_t q[2][HAD ? 2 : 1][kTile];    // [half][high, low][64 channels][row]
     alignas(1024) uint8_t ring[kRingTiles][kTile];
     alignas(16) float par[2][kTileTokens];             // K scale times scale2
-    alignas(16) uint32_t absent[2][4];                 // tokens of the tile that are not there, a bit each
+    alignas(16) uint16_t absent[2][8];                 // tokens of the tile that are not there, a bit each
     alignas(16) uint32_t signs[D / 2];                 // sign bits of two channels' signs
     uint64_t full[kRingTiles], empty[kRingTiles];
     uint64_t par_full[2], par_empty[2];
@@ -433,90 +436,69 @@ __device__ __forceinline__ uint64_t add_f2(uint64_t x, uint64_t y) {
     return r;
 }
 
-// Four 16-byte pieces of a 128-byte-swizzled tile from 32 codes of one token:
-// channels 32 quarter .. + 31 (D = 128) of row `row`.  Of eight channels the
-// halves are in the order 0 4 1 5 2 6 3 7, as the queries' and O's are.
 __device__ __forceinline__ uint32_t mul2(uint32_t x, uint32_t y) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
     return r;
 }
-template <int D>
+// Four 16-byte pieces of a 128-byte-swizzled tile from 32 codes of one token:
+// channels 32 quarter .. + 31 of row `row`.  Of eight channels the halves are
+// in the order 0 4 1 5 2 6 3 7, as the queries' and O's are.  Lanes of the
+// second 64 channels take their pieces in another order: the same places of
+// the two 64-channel halves lie in the same banks.
 __device__ __forceinline__ void store_codes(uint8_t* tile, int row, int quarter, const uint4& w, uint32_t scale) {
-    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-    uint8_t* base = tile + (quarter >> 1) * (kTileTokens * 128) + row * 128;
+    const bool upper = quarter & 2;
+    const uint32_t words[4] = {upper ? w.y : w.x, upper ? w.x : w.y, upper ? w.w : w.z, upper ? w.z : w.w};
+    uint8_t* base = tile + (upper ? kTileTokens * 128 : 0) + row * 128;
+    const int swizzle = (quarter & 1) * 4 ^ (upper ? 1 : 0) ^ (row & 7);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const uint32_t x = words[k], x8 = x >> 8;
-        const int chunk = ((quarter & 1) * 4 + k) ^ (row & 7);
-        uint4 v = make_uint4(codes_low(x), codes_upper(x), codes_low(x8), codes_upper(x8));
-        v = make_uint4(mul2(v.x, scale), mul2(v.y, scale), mul2(v.z, scale), mul2(v.w, scale));
-        *reinterpret_cast<uint4*>(base + chunk * 16) = v;
+        *reinterpret_cast<uint4*>(base + (k ^ swizzle) * 16) =
+            make_uint4(mul2(codes_low(x), scale), mul2(codes_upper(x), scale), mul2(codes_low(x8), scale),
+                       mul2(codes_upper(x8), scale));
     }
 }
 // Order of eight channels in a 16-byte piece: place p holds channel place8(p).
 __host__ __device__ constexpr int place8(int p) { return (p >> 1) + 4 * (p & 1); }
 
-// A producer group's part of the tiles: T threads (K: 128, V: 96), of which
-// this is number `me`.  Pages are looked up a tile ahead of the codes and
-// scales, which are on their way while the thread waits for the buffer.  K and
-// V share the code (K's codes are multiplied by 1): the instruction cache
-// holds the loops of all roles, and hardly more.
+// 16 tokens of a tile of K or V, by one warp: codes and scales into registers,
+// and from there, as fp16, into the tile.  K and V share the code (K's codes
+// are multiplied by 1): the instruction cache holds the loops of all roles,
+// and hardly more.
 template <int D>
-struct Producer {
-    static constexpr int kPieces = D / 32, kAll = kTileTokens * kPieces, kMost = (kAll + 95) / 96;
-    int me, T, is_v;
-    const uint8_t* codes;
-    int page[kMost], page_s;  // as the table has them: of the pieces' tokens, and of the token whose K scale this thread brings
-    uint4 w[kMost];
-    __half scale[kMost];
-    float sk;
-    bool absent;
+struct Unit {
+    static constexpr int kPieces = D / 32, kLoads = kPieces / 2;  // 16-byte pieces of a token; loads of a lane
+    uint4 w[kLoads];
+    __half scale;  // of the token that is this lane's (lanes 0 .. 15)
+    bool absent;   // which is not there
 
-    __device__ __forceinline__ void pages(const TileArgs& g, const TileItem& it, int tok0) {
-        const int* row = g.a.b.table + (long long)it.s * g.a.b.table_stride;
-        const int t0 = it.t0, t1 = it.t1;
-        const auto look = [&](int tok) { return tok >= t0 && tok < t1 ? row[tok >> g.a.p.page_log2] : 0; };
-#pragma unroll
-        for (int k = 0; k < kMost; ++k) page[k] = look(tok0 + min(me + k * T, kAll - 1) / kPieces);
-        page_s = look(tok0 + me);
-    }
-    // Index of token tok in the pool (below 2^31), or -1 (a refused page sets the error word).
-    __device__ __forceinline__ int place(const TileArgs& g, int h, int t0, int t1, int tok, int pg) const {
+    // pg: the page as the table has it.
+    __device__ __forceinline__ void fetch(const TileArgs& g, const TileItem& it, int tok, int is_v, int pg) {
         const Pool& p = g.a.p;
-        if (tok < t0 || tok >= t1) return -1;
-        if (pg >= 0 && pg < p.n_pages)
-            return ((pg * p.H + h) << p.page_log2) + (tok & ((1 << p.page_log2) - 1));
-        report_error(kErrRange);
-        return -1;
-    }
-    __device__ __forceinline__ void fetch(const TileArgs& g, int h, int t0, int t1, int tok0) {
-        const Pool& p = g.a.p;
+        const int lane = threadIdx.x & 31;
+        const bool needed = tok + 16 > it.t0 && tok < it.t1, there = needed && pg >= 0 && pg < p.n_pages;
+        if (needed && !there) report_error(kErrRange);
+        absent = !there || tok + (lane & 15) < it.t0 || tok + (lane & 15) >= it.t1;
+        scale = __ushort_as_half(0);
 #pragma unroll
-        for (int k = 0; k < kMost; ++k) {
-            const int piece = min(me + k * T, kAll - 1);
-            const int at = place(g, h, t0, t1, tok0 + piece / kPieces, page[k]);
-            w[k] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // zeros
-            scale[k] = __ushort_as_half(0x3C00);
-            if (at >= 0) {
-                w[k] = reinterpret_cast<const uint4*>(codes)[(uint32_t)at * (uint64_t)kPieces + piece % kPieces];
-                if (is_v) scale[k] = p.tok[1][at];
-            }
-        }
-        if (!is_v) {
-            const int at = place(g, h, t0, t1, tok0 + me, page_s);
-            absent = at < 0;
-            // (never 0: a score of -inf stays -inf; a zero vector's scores are 0 all the same)
-            sk = absent ? 1.0f : fmaxf(__half2float(p.tok[0][at]) * g.a.scale2, 1e-37f);
+        for (int k = 0; k < kLoads; ++k) w[k] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // zeros
+        if (there) {  // the 16 tokens lie in a row, and all may be read
+            const uint32_t at = (uint32_t)((pg * p.H + it.h) << p.page_log2) + (tok & ((1 << p.page_log2) - 1));
+            const uint4* src = reinterpret_cast<const uint4*>(p.codes[is_v]) + at * (uint64_t)kPieces + lane;
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) w[k] = src[32 * k];
+            if (!absent) scale = p.tok[is_v][at + (lane & 15)];
         }
     }
-    __device__ __forceinline__ void store(uint8_t* tile) const {
+    __device__ __forceinline__ void store(uint8_t* tile, int first_row, int is_v) const {
+        const int lane = threadIdx.x & 31;
+        const uint32_t mine = is_v ? __half_as_ushort(scale) : 0x3C00u;
 #pragma unroll
-        for (int k = 0; k < kMost; ++k) {
-            const int piece = me + k * T;
-            const __half2 two = __half2half2(scale[k]);
-            if (piece < kAll)
-                store_codes<D>(tile, piece / kPieces, piece % kPieces, w[k], *reinterpret_cast<const uint32_t*>(&two));
+        for (int k = 0; k < kLoads; ++k) {
+            const int row = k * (32 / kPieces) + lane / kPieces;
+            const uint32_t x = __shfl_sync(~0u, mine, row);
+            store_codes(tile, first_row + row, lane % kPieces, w[k], x | x << 16);
         }
     }
 };
@@ -531,15 +513,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kRingTiles; ++i) mbar_init(&sm.full[i], 4), mbar_init(&sm.empty[i], 1);
+        for (int i = 0; i < kRingTiles; ++i) mbar_init(&sm.full[i], 8), mbar_init(&sm.empty[i], 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.par_full[i], 4), mbar_init(&sm.par_empty[i], 8);
+            mbar_init(&sm.par_full[i], 8), mbar_init(&sm.par_empty[i], 8);
             mbar_init(&sm.q_full[i], 4), mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.w_full[i], 4), mbar_init(&sm.o_full[i], 1);
         }
         fence_mbar_init();
     }
-    if (warp == 12) {
+    if (warp == 15) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -689,7 +671,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                         const int from = see.t0 - tok0 - 32 * k, to_ = see.t1 - tok0 - 32 * k;  // of these 32 tokens
                         const uint32_t sees = (to_ >= 32 ? ~0u : to_ > 0 ? (1u << to_) - 1 : 0u) &
                                               (from <= 0 ? ~0u : from < 32 ? ~0u << from : 0u) &
-                                              ~sm.absent[tile & 1][k];
+                                              ~reinterpret_cast<const uint32_t*>(sm.absent[tile & 1])[k];
                         uint32_t s[32];
                         tmem_load32(s, ts + 32 * k);
                         tmem_wait_load();
@@ -828,102 +810,114 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                                                (int)(cut.of(item + kItemCost + it.units - 1) - blockIdx.x) + 1);
             }
         }
-    } else if (works) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == 12) {
-            // -------------------------------------------- products
-            if (lane == 0) {
-                constexpr uint32_t kS = mma_desc(kTileTokens, false), kO = mma_desc(D, true);
-                uint32_t seq = 0, tile = 0;  // tiles of the ring taken (K, V, K, ..); steps
-                const uint32_t ring = smem_u32(sm.ring[0]), q = smem_u32(sm.q[0][0]);
-                const auto scores = [&](int half, uint32_t buf) {
+    } else if (works && warp == 15) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+        // -------------------------------------------- products
+        if (lane == 0) {
+            constexpr uint32_t kS = mma_desc(kTileTokens, false), kO = mma_desc(D, true);
+            uint32_t seq = 0, tile = 0;  // tiles of the ring taken (K, V, K, ..); steps
+            const uint32_t ring = smem_u32(sm.ring[0]), q = smem_u32(sm.q[0][0]);
+            const auto scores = [&](int half, uint32_t buf) {
 #pragma unroll
-                    for (int part = 0; part < (HAD ? 2 : 1); ++part)
+                for (int part = 0; part < (HAD ? 2 : 1); ++part)
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t at = (k >> 2) * kSlab + (k & 3) * 32;
-                            mma_ss(tmem + half * 128, smem_desc(q + (half * (HAD ? 2 : 1) + part) * kTile + at, 16),
-                                   smem_desc(ring + buf * kTile + at, 16), kS, part + k > 0);
-                        }
-                };
-                const auto values = [&](int half, uint32_t buf, bool add) {
-#pragma unroll
-                    for (int k = 0; k < kTileTokens / 16; ++k)
-                        mma_ts(tmem + 256 + half * 128, tmem + half * 128 + 8 * k,
-                               smem_desc(ring + buf * kTile + k * 2048, kSlab), kO, add || k > 0);
-                };
-                bool ok = true;
-                for (uint32_t item = 0; ok && wk.n > 0; wk.next(g), ++item) {
-                    for (int n = 0; n <= wk.n && ok; ++n) {
-                        // O of tile n - 1, S of tile n; tile n's K is `seq`, tile n - 1's V `seq - 1`
-                        const uint32_t kb = seq % kRingTiles, vb = (seq + 2) % kRingTiles;
-                        if (n > 0) ok = wait_one(&sm.full[vb], (seq - 1) / kRingTiles & 1);
-                        for (int half = 0; half < 2 && ok; ++half) {
-                            if (n > 0) {
-                                if (!(ok = wait_one(&sm.w_full[half], (tile - 1) & 1))) break;
-                                tc_after_sync();
-                                values(half, vb, n > 1);
-                                if (half == 1) mma_commit(&sm.empty[vb]);
-                                if (n == wk.n) mma_commit(&sm.o_full[half]);
-                            }
-                            if (n < wk.n) {
-                                if (n == 0 && !(ok = wait_one(&sm.q_full[half], item & 1))) break;
-                                if (half == 0 && !(ok = wait_one(&sm.full[kb], seq / kRingTiles & 1))) break;
-                                tc_after_sync();
-                                scores(half, kb);
-                                mma_commit(&sm.s_full[half]);
-                                if (half == 1) mma_commit(&sm.empty[kb]);
-                            }
-                        }
-                        if (n < wk.n) seq += 2, ++tile;
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t at = (k >> 2) * kSlab + (k & 3) * 32;
+                        mma_ss(tmem + half * 128, smem_desc(q + (half * (HAD ? 2 : 1) + part) * kTile + at, 16),
+                               smem_desc(ring + buf * kTile + at, 16), kS, part + k > 0);
                     }
-                }
-                if (!ok) {  // products in flight end before tensor memory is given back
-                    mma_commit(&sm.o_full[0]);
-                    mma_commit(&sm.o_full[1]);
-                    mbar_wait_1s(&sm.o_full[1], 0, kTileWait);
-                    mbar_wait_1s(&sm.o_full[1], 1, kTileWait);
+            };
+            const auto values = [&](int half, uint32_t buf, bool add) {
+#pragma unroll
+                for (int k = 0; k < kTileTokens / 16; ++k)
+                    mma_ts(tmem + 256 + half * 128, tmem + half * 128 + 8 * k,
+                           smem_desc(ring + buf * kTile + k * 2048, kSlab), kO, add || k > 0);
+            };
+            bool ok = true;
+            for (uint32_t item = 0; ok && wk.n > 0; wk.next(g), ++item) {
+                for (int n = 0; n <= wk.n && ok; ++n) {
+                    // O of tile n - 1, S of tile n; tile n's K is `seq`, tile n - 1's V `seq - 1`
+                    const uint32_t kb = seq % kRingTiles, vb = (seq + 2) % kRingTiles;
+                    if (n > 0) ok = wait_one(&sm.full[vb], (seq - 1) / kRingTiles & 1);
+                    for (int half = 0; half < 2 && ok; ++half) {
+                        if (n > 0) {
+                            if (!(ok = wait_one(&sm.w_full[half], (tile - 1) & 1))) break;
+                            tc_after_sync();
+                            values(half, vb, n > 1);
+                            if (half == 1) mma_commit(&sm.empty[vb]);
+                            if (n == wk.n) mma_commit(&sm.o_full[half]);
+                        }
+                        if (n < wk.n) {
+                            if (n == 0 && !(ok = wait_one(&sm.q_full[half], item & 1))) break;
+                            if (half == 0 && !(ok = wait_one(&sm.full[kb], seq / kRingTiles & 1))) break;
+                            tc_after_sync();
+                            scores(half, kb);
+                            mma_commit(&sm.s_full[half]);
+                            if (half == 1) mma_commit(&sm.empty[kb]);
+                        }
+                    }
+                    if (n < wk.n) seq += 2, ++tile;
                 }
             }
-            __syncwarp();
-        } else {
-            // -------------------------------------------- K (warps 8 .. 11) and V (13 .. 15) tiles
-            Producer<D> pr;
-            pr.is_v = warp > 12;
-            pr.T = pr.is_v ? 96 : 128;
-            pr.me = threadIdx.x - (pr.is_v ? 13 : 8) * 32;
-            pr.codes = a.p.codes[pr.is_v];
-            int n = 0;
-            if (wk.n > 0) pr.pages(g, wk.it, (wk.it.u0 + wk.u) * kTileTokens);
-            uint32_t seq = pr.is_v;
-            for (uint32_t tile = 0; wk.n > 0; ++tile, seq += 2) {
-                const uint32_t buf = seq % kRingTiles, round = seq / kRingTiles;
-                pr.fetch(g, wk.it.h, wk.it.t0, wk.it.t1, (wk.it.u0 + wk.u + n) * kTileTokens);
+            if (!ok) {  // products in flight end before tensor memory is given back
+                mma_commit(&sm.o_full[0]);
+                mma_commit(&sm.o_full[1]);
+                mbar_wait_1s(&sm.o_full[1], 0, kTileWait);
+                mbar_wait_1s(&sm.o_full[1], 1, kTileWait);
+            }
+        }
+        __syncwarp();
+    } else if (works) {
+        // ------------------------------------------------ tiles of K and V
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+        // units of 16 tokens: eight of a step's K tile, eight of its V tile, the next step's, ..; this warp
+        // takes every kProducers-th
+        uint32_t step = 0, unit = warp - 8;
+        int n = 0;  // the step's tile in the segment
+        const auto seek = [&] {  // the walk to the unit's step; false at the end
+            for (; step < unit >> 4 && wk.n > 0; ++step)
                 if (++n == wk.n) {
                     advance();
                     n = 0;
                 }
-                if (wk.n > 0) pr.pages(g, wk.it, (wk.it.u0 + wk.u + n) * kTileTokens);
-                if (round > 0 && !wait(&sm.empty[buf], (round - 1) & 1)) break;
-                if (!pr.is_v) {
-                    if (tile >= 2 && !wait(&sm.par_empty[tile & 1], ((tile >> 1) - 1) & 1)) break;
-                    sm.par[tile & 1][pr.me] = pr.sk;
-                    const uint32_t absent = __ballot_sync(~0u, pr.absent);
-                    if (lane == 0) sm.absent[tile & 1][warp - 8] = absent;
-                }
-                pr.store(sm.ring[buf]);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&sm.full[buf], warp == 13 ? 2 : 1);
-                    if (!pr.is_v) mbar_arrive(&sm.par_full[tile & 1]);
-                }
+            return wk.n > 0;
+        };
+        const auto token = [&] { return (wk.it.u0 + wk.u + n) * kTileTokens + 16 * (int)(unit & 7); };
+        const auto look_up = [&] {  // a unit ahead of the codes
+            const int tok = token();
+            return tok + 16 > wk.it.t0 && tok < wk.it.t1
+                       ? a.b.table[(long long)wk.it.s * a.b.table_stride + (tok >> a.p.page_log2)] : 0;
+        };
+        bool more = seek();
+        int page = more ? look_up() : 0;
+        while (more) {
+            const uint32_t is_v = unit >> 3 & 1, rows = 16 * (unit & 7), stage = step & 1, turn = step >> 1;
+            const uint32_t seq = 2 * step + is_v, buf = seq % kRingTiles, round = seq / kRingTiles;
+            Unit<D> un;
+            un.fetch(g, wk.it, token(), is_v, page);
+            unit += kProducers;
+            more = seek();
+            if (more) page = look_up();
+            if (round > 0 && !wait(&sm.empty[buf], (round - 1) & 1)) break;
+            if (!is_v) {
+                if (turn > 0 && !wait(&sm.par_empty[stage], (turn - 1) & 1)) break;
+                const uint32_t absent = __ballot_sync(~0u, un.absent);
+                // (never 0: a score of -inf stays -inf; a zero vector's scores are 0 all the same)
+                if (lane < 16) sm.par[stage][rows + lane] = fmaxf(__half2float(un.scale) * a.scale2, 1e-37f);
+                if (lane == 0) sm.absent[stage][rows / 16] = (uint16_t)absent;
+            }
+            un.store(sm.ring[buf], rows, is_v);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sm.full[buf]);
+                if (!is_v) mbar_arrive(&sm.par_full[stage]);
             }
         }
     }
     tc_before_sync();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == 15) {
         tc_after_sync();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     }
