@@ -1,9 +1,9 @@
 // kvq_pages_tile.cuh -- attention of many query rows a kv head (prompts, parts
-// of prompts): tcgen05 products on tiles of 256 rows and 128 tokens.
+// of prompts): tcgen05 products on tiles of 256 rows and 64 tokens.
 //
 // Rows: row r and query head j of a kv head's group are tile row r G + j, so
 // that a kv head's codes are unpacked once for all its heads.  An item is
-// (sequence, 256 such rows, kv head); its cost is the number of 128-token
+// (sequence, 256 such rows, kv head); its cost is the number of 64-token
 // tiles that its rows see.  pages_plan lays all items end to end and cuts them
 // into one range a CTA; parts of items at the ends are merged by
 // pages_merge_kernel.
@@ -14,12 +14,13 @@
 //   warps 8 .. 14          codes from global memory to the fp16 tiles of K and V,
 //                          16 tokens at a time in turn; scales
 //   warp 15                issues the products
-// Products a step, rows X: S_X = Q_X K^T (for rotated queries twice, the high
-// and the low fp16 part: 22 bits of the query are kept), then O_X += W_X V with
-// W_X, fp16, taken from tensor memory, where it lies over S_X.  The order
-// O_A, S_A of the next tile, O_B, S_B lets the softmax of one half run while
-// the tensor core works for the other.  Tiles of K and V go through a ring of
-// three shared-memory buffers.
+// Products a step of 64 tokens, rows X: S_X = Q_X K^T (for rotated queries
+// twice, the high and the low fp16 part: 22 bits of the query are kept), then
+// O_X += W_X V with W_X, fp16, taken from tensor memory, where it lies over
+// S_X.  Each half has two S, so that the scores of the next step are there
+// when a softmax ends one; with one S of 128 tokens a half, which the tensor
+// core fills faster, softmax and products waited for each other in turn (9000
+// cycles for 128 tokens).  Tiles of K and V go through a ring of six buffers.
 // W is the probability itself here, 2^(x - M), and the V tile holds sigma q
 // rounded to fp16 (2^-12, as W is): the scheme of the step kernel, with the V
 // scale in the exponent, needs two more numbers a token in every softmax
@@ -36,12 +37,13 @@
 
 namespace kvq {
 
-constexpr int kRowsM = 128, kItemRows = 256, kTileTokens = 128;
+constexpr int kRowsM = 128, kItemRows = 256, kTileTokens = 64;
 // What an item costs besides its tiles (queries in, rows out), in tiles: with 0, the CTA of a prompt's first
 // rows, whose items are short, took twice the time of the others.
-constexpr int kItemCost = 4;
+constexpr int kItemCost = 8;
 constexpr int kTileThreads = 512;
-constexpr int kRingTiles = 3;
+constexpr int kRingTiles = 6, kParStages = 4;
+constexpr int kUnits = kTileTokens / 16;  // of 16 tokens, a tile's
 constexpr float kSlack = 8.0f;               // how far a row's maximum may pass its reference
 constexpr float kTileBias = kBias - kSlack;  // w = 2^(y - M + kTileBias) stays in fp16
 constexpr uint32_t kTileWait = 1u << 22;  // polls, of a second at most together
@@ -321,14 +323,16 @@ struct TileWalk {
 template <int D, bool HAD>
 struct TileSmem {
     static constexpr int kTile = kTileTokens * D * 2;  // bytes of a K or V tile
-    alignas(1024) uint8_t q[2][HAD ? 2 : 1][kTile];    // [half][high, low][64 channels][row]
+    static constexpr int kQuery = kRowsM * D * 2;      // of a part of a half's queries
+    alignas(1024) uint8_t q[2][HAD ? 2 : 1][kQuery];   // [half][high, low][64 channels][row]
     alignas(1024) uint8_t ring[kRingTiles][kTile];
-    alignas(16) float par[2][kTileTokens];             // K scale times scale2
-    alignas(16) uint16_t absent[2][8];                 // tokens of the tile that are not there, a bit each
+    alignas(16) float par[kParStages][kTileTokens];    // K scale times scale2
+    alignas(8) uint16_t absent[kParStages][kUnits];    // tokens of the tile that are not there, a bit each
     alignas(16) uint32_t signs[D / 2];                 // sign bits of two channels' signs
     uint64_t full[kRingTiles], empty[kRingTiles];
-    uint64_t par_full[2], par_empty[2];
-    uint64_t q_full[2], s_full[2], w_full[2], o_full[2];
+    uint64_t par_full[kParStages], par_empty[kParStages];
+    uint64_t q_full[2], s_full[2][2], w_full[2][2], o_full[2][2];  // [half], [half][tile's parity]
+    uint64_t drained;
     uint32_t tmem;
     TileWalk walk[kTileThreads / 32];                  // each warp's place in the work
 };
@@ -506,18 +510,20 @@ struct Unit {
 template <int D, bool HAD>
 __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g) {
     using S = TileSmem<D, HAD>;
-    constexpr int kTile = S::kTile, kSlab = kTileTokens * 128;
+    constexpr int kTile = S::kTile, kSlab = kTileTokens * 128, kQSlab = kRowsM * 128;  // 64 channels of a tile, of queries
     extern __shared__ __align__(1024) uint8_t tile_raw[];
     S& sm = *reinterpret_cast<S*>(tile_raw);
     const AttnArgs& a = g.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kRingTiles; ++i) mbar_init(&sm.full[i], 8), mbar_init(&sm.empty[i], 1);
+        mbar_init(&sm.drained, 1);
+        for (int i = 0; i < kRingTiles; ++i) mbar_init(&sm.full[i], kUnits), mbar_init(&sm.empty[i], 1);
+        for (int i = 0; i < kParStages; ++i) mbar_init(&sm.par_full[i], kUnits), mbar_init(&sm.par_empty[i], 8);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.par_full[i], 8), mbar_init(&sm.par_empty[i], 8);
-            mbar_init(&sm.q_full[i], 4), mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.w_full[i], 4), mbar_init(&sm.o_full[i], 1);
+            mbar_init(&sm.q_full[i], 4);
+            for (int j = 0; j < 2; ++j)
+                mbar_init(&sm.s_full[i][j], 1), mbar_init(&sm.w_full[i][j], 4), mbar_init(&sm.o_full[i][j], 1);
         }
         fence_mbar_init();
     }
@@ -562,9 +568,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int half = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
-        const uint32_t ts = tmem + lanes + half * 128, to = tmem + lanes + 256 + half * 128;
+        const uint32_t ts0 = tmem + lanes + half * 128, to = tmem + lanes + 256 + half * 128;
         uint32_t tile = 0;
         bool ok = true;
+        const auto o_done = [&](uint32_t x) { return wait(&sm.o_full[half][x & 1], x >> 1 & 1); };  // O has tile x
         for (uint32_t item = 0; ok && wk.n > 0; advance(), ++item) {
             const TileItem& it = wk.it;
             Range see{0, 0x7FFFFFFF};  // rows that are not there count as seeing all
@@ -642,9 +649,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                             wl[k] = *reinterpret_cast<const uint32_t*>(&l);
                         }
                     }
-                    const int at = (k8 >> 3) * kSlab + ((k8 & 7) ^ (r & 7)) * 16;
+                    const int at = (k8 >> 3) * kQSlab + ((k8 & 7) ^ (r & 7)) * 16;
                     *reinterpret_cast<uint4*>(hi + at) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
-                    if constexpr (HAD) *reinterpret_cast<uint4*>(hi + kTile + at) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
+                    if constexpr (HAD) *reinterpret_cast<uint4*>(hi + S::kQuery + at) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
                 }
             }
             fence_proxy_async_smem();
@@ -659,59 +666,59 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
             uint64_t l2[2] = {pair2(0.0f, 0.0f), pair2(0.0f, 0.0f)};
             for (int n = 0; n < tiles; ++n, ++tile) {
                 const int tok0 = first + n * kTileTokens;
-                if (!(ok = wait(&sm.par_full[tile & 1], tile >> 1 & 1)) || !(ok = wait(&sm.s_full[half], tile & 1))) break;
+                const uint32_t stage = tile % kParStages, ts = ts0 + (tile & 1) * kTileTokens;
+                if (!(ok = wait(&sm.par_full[stage], tile / kParStages & 1)) ||
+                    !(ok = wait(&sm.s_full[half][tile & 1], tile >> 1 & 1)) ||
+                    !(ok = n < 2 || o_done(tile - 2)))  // (done when S is; a barrier's phases are waited for in turn)
+                    break;
                 tc_after_sync();
-                const float* par = sm.par[tile & 1];
-                const uint4 absent = *reinterpret_cast<const uint4*>(sm.absent[tile & 1]);
-                if (scaled || tok0 < see_lo || tok0 + kTileTokens > see_hi ||
-                    (absent.x | absent.y | absent.z | absent.w)) {
+                const float* par = sm.par[stage];
+                uint32_t s[2][32];
+                tmem_load32(s[0], ts);
+                tmem_load32(s[1], ts + 32);
+                const uint2 gone = *reinterpret_cast<const uint2*>(sm.absent[stage]);
+                tmem_wait_load();
+                if (scaled || tok0 < see_lo || tok0 + kTileTokens > see_hi || (gone.x | gone.y)) {
                     // scores that are not plain: scaled rows, tokens that a row does not see
-#pragma unroll 1
-                    for (int k = 0; k < 4; ++k) {
-                        const int from = see.t0 - tok0 - 32 * k, to_ = see.t1 - tok0 - 32 * k;  // of these 32 tokens
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int from = see.t0 - tok0 - 32 * e, to_ = see.t1 - tok0 - 32 * e;  // of these 32 tokens
                         const uint32_t sees = (to_ >= 32 ? ~0u : to_ > 0 ? (1u << to_) - 1 : 0u) &
-                                              (from <= 0 ? ~0u : from < 32 ? ~0u << from : 0u) &
-                                              ~reinterpret_cast<const uint32_t*>(sm.absent[tile & 1])[k];
-                        uint32_t s[32];
-                        tmem_load32(s, ts + 32 * k);
-                        tmem_wait_load();
+                                              (from <= 0 ? ~0u : from < 32 ? ~0u << from : 0u) & ~(e ? gone.y : gone.x);
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
-                            s[c] = sees >> c & 1 ? __float_as_uint(__uint_as_float(s[c]) * back) : 0xFF800000u;  // -inf
-                        tmem_store32(ts + 32 * k, s);
+                            s[e][c] = sees >> c & 1 ? __float_as_uint(__uint_as_float(s[e][c]) * back)
+                                                    : 0xFF800000u;  // -inf
                     }
-                    tmem_wait_store();
                 }
-                float top = kLowest;
-#pragma unroll 1
-                for (int k = 0; k < kTileTokens; k += 64) {
-                    uint32_t s[2][32];
-                    tmem_load32(s[0], ts + k);
-                    tmem_load32(s[1], ts + k + 32);
-                    tmem_wait_load();
-                    float tops[2] = {kLowest, kLowest};
+                float tops[4] = {kLowest, kLowest, kLowest, kLowest};
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
-                        for (int c = 0; c < 32; c += 4) {  // x = S sigma scale
-                            const float4 sk = *reinterpret_cast<const float4*>(&par[k + 32 * e + c]);
-                            float x[4];
-                            unpair2(mul_f2(pair2(__uint_as_float(s[e][c]), __uint_as_float(s[e][c + 1])),
-                                           pair2(sk.x, sk.y)), x[0], x[1]);
-                            unpair2(mul_f2(pair2(__uint_as_float(s[e][c + 2]), __uint_as_float(s[e][c + 3])),
-                                           pair2(sk.z, sk.w)), x[2], x[3]);
-                            tops[e] = fmaxf(tops[e], fmaxf(x[0], x[1]));
-                            tops[e] = fmaxf(tops[e], fmaxf(x[2], x[3]));
-                        }
-                    top = fmaxf(top, fmaxf(tops[0], tops[1]));
-                }
+                    for (int c = 0; c < 32; c += 4) {  // x = S sigma scale
+                        const float4 sk = *reinterpret_cast<const float4*>(&par[32 * e + c]);
+                        float x[4];
+                        unpair2(mul_f2(pair2(__uint_as_float(s[e][c]), __uint_as_float(s[e][c + 1])), pair2(sk.x, sk.y)),
+                                x[0], x[1]);
+                        unpair2(mul_f2(pair2(__uint_as_float(s[e][c + 2]), __uint_as_float(s[e][c + 3])),
+                                       pair2(sk.z, sk.w)), x[2], x[3]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s[e][c + j] = __float_as_uint(x[j]);
+                        tops[2 * e] = fmaxf(tops[2 * e], fmaxf(x[0], x[1]));
+                        tops[2 * e + 1] = fmaxf(tops[2 * e + 1], fmaxf(x[2], x[3]));
+                    }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.par_empty[stage]);
+                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 if (__any_sync(~0u, top > M + kSlack)) {
                     const float m2 = fmaxf(M, top), f = ex2(M - m2);
                     const uint64_t ff = pair2(f, f);
                     M = m2;
                     l2[0] = mul_f2(l2[0], ff);
                     l2[1] = mul_f2(l2[1], ff);
-                    if (n > 0) {
+                    if (n > 0) {  // O, once the tile before is in it
+                        if (!(ok = o_done(tile - 1))) break;
+                        tc_after_sync();
 #pragma unroll 1
                         for (int k = 0; k < D; k += 32) {
                             uint32_t o[32];
@@ -724,41 +731,29 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                     }
                 }
                 const uint64_t ref = pair2(kTileBias - M, kTileBias - M);
-                // (the probabilities of 64 tokens take the place of the scores of 32 that were read before)
-#pragma unroll 1
-                for (int k = 0; k < kTileTokens; k += 64) {
-                    uint32_t s[2][32], w[32];
-                    tmem_load32(s[0], ts + k);
-                    tmem_load32(s[1], ts + k + 32);
-                    tmem_wait_load();
+                uint32_t w[32];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
-                        for (int c = 0; c < 32; c += 4) {
-                            const float4 sk = *reinterpret_cast<const float4*>(&par[k + 32 * e + c]);
-                            float p[4];
-                            unpair2(fma_f2(pair2(__uint_as_float(s[e][c]), __uint_as_float(s[e][c + 1])),
-                                           pair2(sk.x, sk.y), ref), p[0], p[1]);
-                            unpair2(fma_f2(pair2(__uint_as_float(s[e][c + 2]), __uint_as_float(s[e][c + 3])),
-                                           pair2(sk.z, sk.w), ref), p[2], p[3]);
+                    for (int c = 0; c < 32; c += 4) {
+                        float p[4];
+                        unpair2(add_f2(pair2(__uint_as_float(s[e][c]), __uint_as_float(s[e][c + 1])), ref), p[0], p[1]);
+                        unpair2(add_f2(pair2(__uint_as_float(s[e][c + 2]), __uint_as_float(s[e][c + 3])), ref), p[2],
+                                p[3]);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) p[j] = ex2(p[j]);
-                            l2[0] = add_f2(l2[0], pair2(p[0], p[1]));
-                            l2[1] = add_f2(l2[1], pair2(p[2], p[3]));
-                            w[16 * e + c / 2] = Elem<__half>::pack(p[0], p[1]);
-                            w[16 * e + c / 2 + 1] = Elem<__half>::pack(p[2], p[3]);
-                        }
-                    tmem_store32(ts + k / 2, w);
-                }
+                        for (int j = 0; j < 4; ++j) p[j] = ex2(p[j]);
+                        l2[0] = add_f2(l2[0], pair2(p[0], p[1]));
+                        l2[1] = add_f2(l2[1], pair2(p[2], p[3]));
+                        w[16 * e + c / 2] = Elem<__half>::pack(p[0], p[1]);
+                        w[16 * e + c / 2 + 1] = Elem<__half>::pack(p[2], p[3]);
+                    }
+                tmem_store32(ts, w);
                 tmem_wait_store();
                 tc_before_sync();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&sm.w_full[half]);
-                    mbar_arrive(&sm.par_empty[tile & 1]);
-                }
+                if (lane == 0) mbar_arrive(&sm.w_full[half][tile & 1]);
             }
-            if (!ok || !(ok = wait(&sm.o_full[half], item & 1))) break;
+            if (!ok || !(ok = (tiles < 2 || o_done(tile - 2)) && o_done(tile - 1))) break;
             tc_after_sync();
             const int i = it.c * kItemRows + half * kRowsM + r;
             const bool there = i < it.nq;
@@ -815,74 +810,69 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
         // -------------------------------------------- products
         if (lane == 0) {
             constexpr uint32_t kS = mma_desc(kTileTokens, false), kO = mma_desc(D, true);
-            uint32_t seq = 0, tile = 0;  // tiles of the ring taken (K, V, K, ..); steps
+            uint32_t tile = 0;  // the item's first, of all the CTA's
             const uint32_t ring = smem_u32(sm.ring[0]), q = smem_u32(sm.q[0][0]);
-            const auto scores = [&](int half, uint32_t buf) {
+            bool ok = true;
+            // S of a half, tile x: K is number 2 x of the ring's tiles
+            const auto scores = [&](int half, uint32_t x) {
+                const uint32_t buf = 2 * x % kRingTiles;
+                if (half == 0 && !(ok = wait_one(&sm.full[buf], 2 * x / kRingTiles & 1))) return;
+                tc_after_sync();
 #pragma unroll
                 for (int part = 0; part < (HAD ? 2 : 1); ++part)
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t at = (k >> 2) * kSlab + (k & 3) * 32;
-                        mma_ss(tmem + half * 128, smem_desc(q + (half * (HAD ? 2 : 1) + part) * kTile + at, 16),
-                               smem_desc(ring + buf * kTile + at, 16), kS, part + k > 0);
-                    }
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_ss(tmem + half * 128 + (x & 1) * kTileTokens,
+                               smem_desc(q + (half * (HAD ? 2 : 1) + part) * S::kQuery + (k >> 2) * kQSlab + (k & 3) * 32, 16),
+                               smem_desc(ring + buf * kTile + (k >> 2) * kSlab + (k & 3) * 32, 16), kS, part + k > 0);
+                mma_commit(&sm.s_full[half][x & 1]);
+                if (half == 1) mma_commit(&sm.empty[buf]);
             };
-            const auto values = [&](int half, uint32_t buf, bool add) {
+            // O of a half, tile x: V is number 2 x + 1
+            const auto values = [&](int half, uint32_t x, bool add) {
+                const uint32_t buf = (2 * x + 1) % kRingTiles;
+                if (half == 0 && !(ok = wait_one(&sm.full[buf], (2 * x + 1) / kRingTiles & 1))) return;
+                if (!(ok = wait_one(&sm.w_full[half][x & 1], x >> 1 & 1))) return;
+                tc_after_sync();
 #pragma unroll
                 for (int k = 0; k < kTileTokens / 16; ++k)
-                    mma_ts(tmem + 256 + half * 128, tmem + half * 128 + 8 * k,
+                    mma_ts(tmem + 256 + half * 128, tmem + half * 128 + (x & 1) * kTileTokens + 8 * k,
                            smem_desc(ring + buf * kTile + k * 2048, kSlab), kO, add || k > 0);
+                mma_commit(&sm.o_full[half][x & 1]);
+                if (half == 1) mma_commit(&sm.empty[buf]);
             };
-            bool ok = true;
-            for (uint32_t item = 0; ok && wk.n > 0; wk.next(g), ++item) {
-                for (int n = 0; n <= wk.n && ok; ++n) {
-                    // O of tile n - 1, S of tile n; tile n's K is `seq`, tile n - 1's V `seq - 1`
-                    const uint32_t kb = seq % kRingTiles, vb = (seq + 2) % kRingTiles;
-                    if (n > 0) ok = wait_one(&sm.full[vb], (seq - 1) / kRingTiles & 1);
+            for (uint32_t item = 0; ok && wk.n > 0; tile += wk.n, wk.next(g), ++item) {
+                const int tiles = wk.n;
+                for (int n = -2; n < tiles && ok; ++n)  // O of tile n, S of tile n + 2
+#pragma unroll 1
                     for (int half = 0; half < 2 && ok; ++half) {
-                        if (n > 0) {
-                            if (!(ok = wait_one(&sm.w_full[half], (tile - 1) & 1))) break;
-                            tc_after_sync();
-                            values(half, vb, n > 1);
-                            if (half == 1) mma_commit(&sm.empty[vb]);
-                            if (n == wk.n) mma_commit(&sm.o_full[half]);
-                        }
-                        if (n < wk.n) {
-                            if (n == 0 && !(ok = wait_one(&sm.q_full[half], item & 1))) break;
-                            if (half == 0 && !(ok = wait_one(&sm.full[kb], seq / kRingTiles & 1))) break;
-                            tc_after_sync();
-                            scores(half, kb);
-                            mma_commit(&sm.s_full[half]);
-                            if (half == 1) mma_commit(&sm.empty[kb]);
-                        }
+                        if (n == -2) ok = wait_one(&sm.q_full[half], item & 1);
+                        if (n >= 0) values(half, tile + n, n > 0);
+                        if (ok && n + 2 < tiles) scores(half, tile + n + 2);
                     }
-                    if (n < wk.n) seq += 2, ++tile;
-                }
             }
             if (!ok) {  // products in flight end before tensor memory is given back
-                mma_commit(&sm.o_full[0]);
-                mma_commit(&sm.o_full[1]);
-                mbar_wait_1s(&sm.o_full[1], 0, kTileWait);
-                mbar_wait_1s(&sm.o_full[1], 1, kTileWait);
+                mma_commit(&sm.drained);
+                mbar_wait_1s(&sm.drained, 0, kTileWait);
             }
         }
         __syncwarp();
     } else if (works) {
         // ------------------------------------------------ tiles of K and V
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
-        // units of 16 tokens: eight of a step's K tile, eight of its V tile, the next step's, ..; this warp
+        // units of 16 tokens: those of a step's K tile, of its V tile, of the next step's, ..; this warp
         // takes every kProducers-th
         uint32_t step = 0, unit = warp - 8;
         int n = 0;  // the step's tile in the segment
         const auto seek = [&] {  // the walk to the unit's step; false at the end
-            for (; step < unit >> 4 && wk.n > 0; ++step)
+            for (; step < unit / (2 * kUnits) && wk.n > 0; ++step)
                 if (++n == wk.n) {
                     advance();
                     n = 0;
                 }
             return wk.n > 0;
         };
-        const auto token = [&] { return (wk.it.u0 + wk.u + n) * kTileTokens + 16 * (int)(unit & 7); };
+        const auto token = [&] { return (wk.it.u0 + wk.u + n) * kTileTokens + 16 * (int)(unit % kUnits); };
         const auto look_up = [&] {  // a unit ahead of the codes
             const int tok = token();
             return tok + 16 > wk.it.t0 && tok < wk.it.t1
@@ -891,7 +881,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
         bool more = seek();
         int page = more ? look_up() : 0;
         while (more) {
-            const uint32_t is_v = unit >> 3 & 1, rows = 16 * (unit & 7), stage = step & 1, turn = step >> 1;
+            const uint32_t is_v = unit / kUnits & 1, rows = 16 * (unit % kUnits);
+            const uint32_t stage = step % kParStages, turn = step / kParStages;
             const uint32_t seq = 2 * step + is_v, buf = seq % kRingTiles, round = seq / kRingTiles;
             Unit<D> un;
             un.fetch(g, wk.it, token(), is_v, page);

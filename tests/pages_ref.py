@@ -92,9 +92,10 @@ def gather(codes, tok, b: Seqs, s: int, n: int):
     return q, sc, there
 
 
-def attention(k, v, b: Seqs, q: np.ndarray, signs, scale, causal, window, half_step):
+def attention(k, v, b: Seqs, q: np.ndarray, signs, scale, causal, window, half_step, only=None):
     """Attention in 64 bits over k, v = (codes, tok), and the bounds of the
-    kernels' errors: {row: (out [Hq, d], lse [Hq], out bound, lse bound)}.
+    kernels' errors: {row: (out [Hq, d], lse [Hq], out bound, lse bound)}, of
+    all rows or of those in `only`.
 
     Roundings of the kernels, each relative to what it rounds:
       scores  the query keeps 22 bits, the products with codes e = q + 8 <= 15
@@ -113,6 +114,8 @@ def attention(k, v, b: Seqs, q: np.ndarray, signs, scale, causal, window, half_s
     scale = scale if scale > 0 else 1.0 / math.sqrt(d)
     res, cache = {}, {}
     for r, s, pos in b.rows():
+        if only is not None and r not in only:
+            continue
         n = max(int(b.length[s]), 0)
         if s not in cache:
             cache[s] = (gather(*k, b, s, n), gather(*v, b, s, n))

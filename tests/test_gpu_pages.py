@@ -86,12 +86,12 @@ class Setup:
         torch.cuda.synchronize()
         return out, l
 
-    def check(self, q, out, lse, dtype, scale=0.0, causal=True, window=0):
+    def check(self, q, out, lse, dtype, scale=0.0, causal=True, window=0, only=None):
         want = ref.attention((self.codes[0], self.tok[0]), (self.codes[1], self.tok[1]), self.b, host(q), self.signs,
-                             scale, causal, window, HALF[dtype])
+                             scale, causal, window, HALF[dtype], only)
         out, l = host(out), None if lse is None else lse.cpu().numpy()
         assert np.isfinite(out).all()
-        for r in range(q.shape[0]):
+        for r in range(q.shape[0]) if only is None else sorted(only):
             if r not in want:
                 assert (out[r] == 7).all() and (l is None or (l[r] == 7).all()), f"row {r} belongs to nobody"
                 continue
@@ -264,6 +264,17 @@ def test_attention_of_prompts(d, G, dtype, rotated):
     q = s.tensor(G, dtype)
     s.check(q, *s.attend(q), dtype)
     s.check(q, *s.attend(q, window=77), dtype, window=77)
+
+
+@pytest.mark.parametrize("d,G,dtype,rotated", [(128, 4, "fp16", True), (128, 2, "bf16", False), (64, 4, "bf16", True),
+                                               (64, 1, "fp16", False)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 700), (False, 0)])
+def test_attention_of_long_prompts(d, G, dtype, rotated, causal, window):
+    """Enough rows that one CTA takes many tiles and several items; a sample of the rows."""
+    s = Setup([(2300, 2300), (1500, 700), (90, 90), (1700, 1)], d=d, H=2, page=32, rotated=rotated)
+    q = s.tensor(2 * G, dtype, scale=1.3)
+    only = {int(r) for r in s.rng.integers(0, s.rows, 60)} | {0, 63, 64, 65, 2299, 2300, 2999, 3000, 3089, 3090}
+    s.check(q, *s.attend(q, causal=causal, window=window), dtype, causal=causal, window=window, only=only)
 
 
 def test_attention_with_a_wrong_row_hint_and_without_lse():
