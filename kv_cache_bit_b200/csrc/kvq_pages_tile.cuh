@@ -363,6 +363,13 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
 __device__ __forceinline__ void tc_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// One lane of a warp that is together.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
+}
+
 // Shared-memory descriptor of a 128-byte-swizzled operand.  K-major (queries,
 // K): 8-row groups 1024 bytes apart (stride offset); the other offset is not
 // used.  MN-major (V, channels contiguous): 8-token groups 1024 bytes apart,
@@ -807,54 +814,66 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
         }
     } else if (works && warp == 15) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
-        // -------------------------------------------- products
-        if (lane == 0) {
-            constexpr uint32_t kS = mma_desc(kTileTokens, false), kO = mma_desc(D, true);
-            uint32_t tile = 0;  // the item's first, of all the CTA's
-            const uint32_t ring = smem_u32(sm.ring[0]), q = smem_u32(sm.q[0][0]);
-            bool ok = true;
-            // S of a half, tile x: K is number 2 x of the ring's tiles
-            const auto scores = [&](int half, uint32_t x) {
-                const uint32_t buf = 2 * x % kRingTiles;
-                if (half == 0 && !(ok = wait_one(&sm.full[buf], 2 * x / kRingTiles & 1))) return;
-                tc_after_sync();
+        // ------------------------------------------------ products
+        // All lanes walk along, so that addresses and descriptors stay in uniform registers; one issues.  (With
+        // one lane in the loop an issue took 80 cycles, longer than the product itself.)
+        constexpr uint32_t kS = mma_desc(kTileTokens, false), kO = mma_desc(D, true);
+        const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+        const uint64_t ring = smem_desc(smem_u32(sm.ring[0]), 16), ring_v = smem_desc(smem_u32(sm.ring[0]), kSlab);
+        const uint64_t q = smem_desc(smem_u32(sm.q[0][0]), 16);
+        uint32_t tile = 0;  // the item's first, of all the CTA's
+        bool ok = true;
+        // S of a half, tile x: K is number 2 x of the ring's tiles
+        const auto scores = [&](uint32_t half, uint32_t x) {
+            const uint32_t buf = 2 * x % kRingTiles;
+            if (half == 0 && !(ok = wait(&sm.full[buf], 2 * x / kRingTiles & 1))) return;
+            tc_after_sync();
+            const uint32_t d = tm + half * 128 + (x & 1) * kTileTokens;
+            const uint64_t qd = q + half * ((HAD ? 2 : 1) * S::kQuery >> 4), kd = ring + buf * (kTile >> 4);
+            if (elect_one()) {
 #pragma unroll
                 for (int part = 0; part < (HAD ? 2 : 1); ++part)
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
-                        mma_ss(tmem + half * 128 + (x & 1) * kTileTokens,
-                               smem_desc(q + (half * (HAD ? 2 : 1) + part) * S::kQuery + (k >> 2) * kQSlab + (k & 3) * 32, 16),
-                               smem_desc(ring + buf * kTile + (k >> 2) * kSlab + (k & 3) * 32, 16), kS, part + k > 0);
+                        mma_ss(d, qd + ((part * S::kQuery + (k >> 2) * kQSlab + (k & 3) * 32) >> 4),
+                               kd + (((k >> 2) * kSlab + (k & 3) * 32) >> 4), kS, part + k > 0);
                 mma_commit(&sm.s_full[half][x & 1]);
                 if (half == 1) mma_commit(&sm.empty[buf]);
-            };
-            // O of a half, tile x: V is number 2 x + 1
-            const auto values = [&](int half, uint32_t x, bool add) {
-                const uint32_t buf = (2 * x + 1) % kRingTiles;
-                if (half == 0 && !(ok = wait_one(&sm.full[buf], (2 * x + 1) / kRingTiles & 1))) return;
-                if (!(ok = wait_one(&sm.w_full[half][x & 1], x >> 1 & 1))) return;
-                tc_after_sync();
+            }
+            __syncwarp();
+        };
+        // O of a half, tile x: V is number 2 x + 1
+        const auto values = [&](uint32_t half, uint32_t x, bool add) {
+            const uint32_t buf = (2 * x + 1) % kRingTiles;
+            if (half == 0 && !(ok = wait(&sm.full[buf], (2 * x + 1) / kRingTiles & 1))) return;
+            if (!(ok = wait(&sm.w_full[half][x & 1], x >> 1 & 1))) return;
+            tc_after_sync();
+            const uint32_t d = tm + 256 + half * 128, w = tm + half * 128 + (x & 1) * kTileTokens;
+            const uint64_t vd = ring_v + buf * (kTile >> 4);
+            if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < kTileTokens / 16; ++k)
-                    mma_ts(tmem + 256 + half * 128, tmem + half * 128 + (x & 1) * kTileTokens + 8 * k,
-                           smem_desc(ring + buf * kTile + k * 2048, kSlab), kO, add || k > 0);
+                for (int k = 0; k < kTileTokens / 16; ++k) mma_ts(d, w + 8 * k, vd + (k * 2048 >> 4), kO, add || k > 0);
                 mma_commit(&sm.o_full[half][x & 1]);
                 if (half == 1) mma_commit(&sm.empty[buf]);
-            };
-            for (uint32_t item = 0; ok && wk.n > 0; tile += wk.n, wk.next(g), ++item) {
-                const int tiles = wk.n;
-                for (int n = -2; n < tiles && ok; ++n)  // O of tile n, S of tile n + 2
+            }
+            __syncwarp();
+        };
+        for (uint32_t item = 0; ok; ++item) {
+            const int tiles = __shfl_sync(~0u, wk.n, 0);
+            if (tiles == 0) break;
+            for (int n = -2; n < tiles && ok; ++n)  // O of tile n, S of tile n + 2
 #pragma unroll 1
-                    for (int half = 0; half < 2 && ok; ++half) {
-                        if (n == -2) ok = wait_one(&sm.q_full[half], item & 1);
-                        if (n >= 0) values(half, tile + n, n > 0);
-                        if (ok && n + 2 < tiles) scores(half, tile + n + 2);
-                    }
-            }
-            if (!ok) {  // products in flight end before tensor memory is given back
-                mma_commit(&sm.drained);
-                mbar_wait_1s(&sm.drained, 0, kTileWait);
-            }
+                for (uint32_t half = 0; half < 2 && ok; ++half) {
+                    if (n == -2) ok = wait(&sm.q_full[half], item & 1);
+                    if (n >= 0) values(half, tile + n, n > 0);
+                    if (ok && n + 2 < tiles) scores(half, tile + n + 2);
+                }
+            tile += tiles;
+            advance();
+        }
+        if (!ok && elect_one()) {  // products in flight end before tensor memory is given back
+            mma_commit(&sm.drained);
+            mbar_wait_1s(&sm.drained, 0, kTileWait);
         }
         __syncwarp();
     } else if (works) {
