@@ -11,9 +11,9 @@
 // A CTA (one an SM):
 //   warps 0 .. 3, 4 .. 7   softmax of the lower and the upper 128 rows, one row a
 //                          thread; they also bring in the queries and finish rows
-//   warps 8 .. 14          codes from global memory to the fp16 tiles of K and V,
+//   warps 8 .. 13          codes from global memory to the fp16 tiles of K and V,
 //                          16 tokens at a time in turn; scales
-//   warp 15                issues the products
+//   warps 14, 15           issue the products of a half each
 // Products a step of 64 tokens, rows X: S_X = Q_X K^T (for rotated queries
 // twice, the high and the low fp16 part: 22 bits of the query are kept), then
 // O_X += W_X V with W_X, fp16, taken from tensor memory, where it lies over
@@ -50,7 +50,7 @@ constexpr uint32_t kTileWait = 1u << 22;  // polls, of a second at most together
 // Registers a thread; the launch gives 128.
 constexpr int kLaunchRegs = 128, kSoftmaxRegs = 160, kProducerRegs = 96;
 static_assert(256 * (kSoftmaxRegs + kProducerRegs) <= kTileThreads * kLaunchRegs);
-constexpr int kProducers = 7;
+constexpr int kProducers = 6;
 
 struct TileArgs {
     AttnArgs a;
@@ -332,7 +332,7 @@ struct TileSmem {
     uint64_t full[kRingTiles], empty[kRingTiles];
     uint64_t par_full[kParStages], par_empty[kParStages];
     uint64_t q_full[2], s_full[2][2], w_full[2][2], o_full[2][2];  // [half], [half][tile's parity]
-    uint64_t drained;
+    uint64_t drained[2];
     uint32_t tmem;
     TileWalk walk[kTileThreads / 32];                  // each warp's place in the work
 };
@@ -524,11 +524,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        mbar_init(&sm.drained, 1);
-        for (int i = 0; i < kRingTiles; ++i) mbar_init(&sm.full[i], kUnits), mbar_init(&sm.empty[i], 1);
+        for (int i = 0; i < kRingTiles; ++i) mbar_init(&sm.full[i], kUnits), mbar_init(&sm.empty[i], 2);
         for (int i = 0; i < kParStages; ++i) mbar_init(&sm.par_full[i], kUnits), mbar_init(&sm.par_empty[i], 8);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.q_full[i], 4);
+            mbar_init(&sm.q_full[i], 4), mbar_init(&sm.drained[i], 1);
             for (int j = 0; j < 2; ++j)
                 mbar_init(&sm.s_full[i][j], 1), mbar_init(&sm.w_full[i][j], 4), mbar_init(&sm.o_full[i][j], 1);
         }
@@ -812,7 +811,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                                                (int)(cut.of(item + kItemCost + it.units - 1) - blockIdx.x) + 1);
             }
         }
-    } else if (works && warp == 15) {
+    } else if (works && warp >= 14) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
         // ------------------------------------------------ products
         // All lanes walk along, so that addresses and descriptors stay in uniform registers; one issues.  (With
@@ -821,12 +820,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
         const uint32_t tm = __shfl_sync(~0u, tmem, 0);
         const uint64_t ring = smem_desc(smem_u32(sm.ring[0]), 16), ring_v = smem_desc(smem_u32(sm.ring[0]), kSlab);
         const uint64_t q = smem_desc(smem_u32(sm.q[0][0]), 16);
+        const uint32_t half = __shfl_sync(~0u, warp & 1, 0);
         uint32_t tile = 0;  // the item's first, of all the CTA's
         bool ok = true;
-        // S of a half, tile x: K is number 2 x of the ring's tiles
-        const auto scores = [&](uint32_t half, uint32_t x) {
+        // S of tile x: K is number 2 x of the ring's tiles
+        const auto scores = [&](uint32_t x) {
             const uint32_t buf = 2 * x % kRingTiles;
-            if (half == 0 && !(ok = wait(&sm.full[buf], 2 * x / kRingTiles & 1))) return;
+            if (!(ok = wait(&sm.full[buf], 2 * x / kRingTiles & 1))) return;
             tc_after_sync();
             const uint32_t d = tm + half * 128 + (x & 1) * kTileTokens;
             const uint64_t qd = q + half * ((HAD ? 2 : 1) * S::kQuery >> 4), kd = ring + buf * (kTile >> 4);
@@ -838,14 +838,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                         mma_ss(d, qd + ((part * S::kQuery + (k >> 2) * kQSlab + (k & 3) * 32) >> 4),
                                kd + (((k >> 2) * kSlab + (k & 3) * 32) >> 4), kS, part + k > 0);
                 mma_commit(&sm.s_full[half][x & 1]);
-                if (half == 1) mma_commit(&sm.empty[buf]);
+                mma_commit(&sm.empty[buf]);
             }
             __syncwarp();
         };
-        // O of a half, tile x: V is number 2 x + 1
-        const auto values = [&](uint32_t half, uint32_t x, bool add) {
+        // O of tile x: V is number 2 x + 1
+        const auto values = [&](uint32_t x, bool add) {
             const uint32_t buf = (2 * x + 1) % kRingTiles;
-            if (half == 0 && !(ok = wait(&sm.full[buf], (2 * x + 1) / kRingTiles & 1))) return;
+            if (!(ok = wait(&sm.full[buf], (2 * x + 1) / kRingTiles & 1))) return;
             if (!(ok = wait(&sm.w_full[half][x & 1], x >> 1 & 1))) return;
             tc_after_sync();
             const uint32_t d = tm + 256 + half * 128, w = tm + half * 128 + (x & 1) * kTileTokens;
@@ -854,26 +854,24 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
 #pragma unroll
                 for (int k = 0; k < kTileTokens / 16; ++k) mma_ts(d, w + 8 * k, vd + (k * 2048 >> 4), kO, add || k > 0);
                 mma_commit(&sm.o_full[half][x & 1]);
-                if (half == 1) mma_commit(&sm.empty[buf]);
+                mma_commit(&sm.empty[buf]);
             }
             __syncwarp();
         };
         for (uint32_t item = 0; ok; ++item) {
             const int tiles = __shfl_sync(~0u, wk.n, 0);
             if (tiles == 0) break;
-            for (int n = -2; n < tiles && ok; ++n)  // O of tile n, S of tile n + 2
-#pragma unroll 1
-                for (uint32_t half = 0; half < 2 && ok; ++half) {
-                    if (n == -2) ok = wait(&sm.q_full[half], item & 1);
-                    if (n >= 0) values(half, tile + n, n > 0);
-                    if (ok && n + 2 < tiles) scores(half, tile + n + 2);
-                }
+            ok = wait(&sm.q_full[half], item & 1);
+            for (int n = -2; n < tiles && ok; ++n) {  // O of tile n, S of tile n + 2
+                if (n >= 0) values(tile + n, n > 0);
+                if (ok && n + 2 < tiles) scores(tile + n + 2);
+            }
             tile += tiles;
             advance();
         }
         if (!ok && elect_one()) {  // products in flight end before tensor memory is given back
-            mma_commit(&sm.drained);
-            mbar_wait_1s(&sm.drained, 0, kTileWait);
+            mma_commit(&sm.drained[half]);
+            mbar_wait_1s(&sm.drained[half], 0, kTileWait);
         }
         __syncwarp();
     } else if (works) {
