@@ -12,7 +12,7 @@
 //   warps 0 .. 3, 4 .. 7   softmax of the lower and the upper 128 rows, one row a
 //                          thread; they also bring in the queries and finish rows
 //   warps 8 .. 13          codes from global memory to the fp16 tiles of K and V,
-//                          16 tokens at a time in turn; scales
+//                          32 tokens at a time in turn; scales
 //   warps 14, 15           issue the products of a half each
 // Products a step of 64 tokens, rows X: S_X = Q_X K^T (for rotated queries
 // twice, the high and the low fp16 part: 22 bits of the query are kept), then
@@ -43,7 +43,7 @@ constexpr int kRowsM = 128, kItemRows = 256, kTileTokens = 64;
 constexpr int kItemCost = 8;
 constexpr int kTileThreads = 512;
 constexpr int kRingTiles = 6, kParStages = 4;
-constexpr int kUnits = kTileTokens / 16;  // of 16 tokens, a tile's
+constexpr int kUnitTokens = 32, kUnits = kTileTokens / kUnitTokens;  // units of a tile
 constexpr float kSlack = 8.0f;               // how far a row's maximum may pass its reference
 constexpr float kTileBias = kBias - kSlack;  // w = 2^(y - M + kTileBias) stays in fp16
 constexpr uint32_t kTileWait = 1u << 22;  // polls, of a second at most together
@@ -326,8 +326,8 @@ struct TileSmem {
     static constexpr int kQuery = kRowsM * D * 2;      // of a part of a half's queries
     alignas(1024) uint8_t q[2][HAD ? 2 : 1][kQuery];   // [half][high, low][64 channels][row]
     alignas(1024) uint8_t ring[kRingTiles][kTile];
-    alignas(16) float par[kParStages][kTileTokens];    // K scale times scale2
-    alignas(8) uint16_t absent[kParStages][kUnits];    // tokens of the tile that are not there, a bit each
+    alignas(16) __half par[kParStages][kTileTokens];   // K scales
+    alignas(8) uint32_t absent[kParStages][kUnits];    // tokens of the tile that are not there, a bit each
     alignas(16) uint32_t signs[D / 2];                 // sign bits of two channels' signs
     uint64_t full[kRingTiles], empty[kRingTiles];
     uint64_t par_full[kParStages], par_empty[kParStages];
@@ -473,33 +473,40 @@ __device__ __forceinline__ void store_codes(uint8_t* tile, int row, int quarter,
 // Order of eight channels in a 16-byte piece: place p holds channel place8(p).
 __host__ __device__ constexpr int place8(int p) { return (p >> 1) + 4 * (p & 1); }
 
-// 16 tokens of a tile of K or V, by one warp: codes and scales into registers,
+// 32 tokens of a tile of K or V, by one warp: codes and scales into registers,
 // and from there, as fp16, into the tile.  K and V share the code (K's codes
 // are multiplied by 1): the instruction cache holds the loops of all roles,
 // and hardly more.
 template <int D>
 struct Unit {
-    static constexpr int kPieces = D / 32, kLoads = kPieces / 2;  // 16-byte pieces of a token; loads of a lane
+    static constexpr int kPieces = D / 32, kLoads = kPieces;  // 16-byte pieces of a token; loads of a lane
     uint4 w[kLoads];
-    __half scale;  // of the token that is this lane's (lanes 0 .. 15)
+    __half scale;  // of the token that is this lane's
     bool absent;   // which is not there
 
-    // pg: the page as the table has it.
-    __device__ __forceinline__ void fetch(const TileArgs& g, const TileItem& it, int tok, int is_v, int pg) {
+    // pg: the pages of the two halves as the table has them.
+    __device__ __forceinline__ void fetch(const TileArgs& g, int h, int t0, int t1, int tok, int is_v, int pg0, int pg1) {
         const Pool& p = g.a.p;
         const int lane = threadIdx.x & 31;
-        const bool needed = tok + 16 > it.t0 && tok < it.t1, there = needed && pg >= 0 && pg < p.n_pages;
-        if (needed && !there) report_error(kErrRange);
-        absent = !there || tok + (lane & 15) < it.t0 || tok + (lane & 15) >= it.t1;
+        absent = tok + lane < t0 || tok + lane >= t1;
         scale = __ushort_as_half(0);
 #pragma unroll
-        for (int k = 0; k < kLoads; ++k) w[k] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // zeros
-        if (there) {  // the 16 tokens lie in a row, and all may be read
-            const uint32_t at = (uint32_t)((pg * p.H + it.h) << p.page_log2) + (tok & ((1 << p.page_log2) - 1));
-            const uint4* src = reinterpret_cast<const uint4*>(p.codes[is_v]) + at * (uint64_t)kPieces + lane;
+        for (int hf = 0; hf < 2; ++hf) {
+            const int t = tok + 16 * hf, pg = hf ? pg1 : pg0;
+            const bool needed = t + 16 > t0 && t < t1, there = needed && pg >= 0 && pg < p.n_pages;
 #pragma unroll
-            for (int k = 0; k < kLoads; ++k) w[k] = src[32 * k];
-            if (!absent) scale = p.tok[is_v][at + (lane & 15)];
+            for (int k = 0; k < kLoads / 2; ++k)
+                w[hf * (kLoads / 2) + k] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // zeros
+            if (there) {  // the 16 tokens lie in a row, and all may be read
+                const uint32_t at = (uint32_t)((pg * p.H + h) << p.page_log2) + (t & ((1 << p.page_log2) - 1));
+                const uint4* src = reinterpret_cast<const uint4*>(p.codes[is_v]) + at * (uint64_t)kPieces + lane;
+#pragma unroll
+                for (int k = 0; k < kLoads / 2; ++k) w[hf * (kLoads / 2) + k] = src[32 * k];
+                if ((lane >> 4) == hf && !absent) scale = p.tok[is_v][at + (lane & 15)];
+            } else {
+                absent |= (lane >> 4) == hf;
+                if (needed) report_error(kErrRange);
+            }
         }
     }
     __device__ __forceinline__ void store(uint8_t* tile, int first_row, int is_v) const {
@@ -678,7 +685,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                     !(ok = n < 2 || o_done(tile - 2)))  // (done when S is; a barrier's phases are waited for in turn)
                     break;
                 tc_after_sync();
-                const float* par = sm.par[stage];
+                const __half* par = sm.par[stage];
                 uint32_t s[2][32];
                 tmem_load32(s[0], ts);
                 tmem_load32(s[1], ts + 32);
@@ -697,25 +704,26 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                                                     : 0xFF800000u;  // -inf
                     }
                 }
-                float tops[4] = {kLowest, kLowest, kLowest, kLowest};
+                float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4) {  // x = S sigma scale
-                        const float4 sk = *reinterpret_cast<const float4*>(&par[32 * e + c]);
-                        float x[4];
-                        unpair2(mul_f2(pair2(__uint_as_float(s[e][c]), __uint_as_float(s[e][c + 1])), pair2(sk.x, sk.y)),
-                                x[0], x[1]);
-                        unpair2(mul_f2(pair2(__uint_as_float(s[e][c + 2]), __uint_as_float(s[e][c + 3])),
-                                       pair2(sk.z, sk.w)), x[2], x[3]);
+                    for (int c = 0; c < 32; c += 8) {  // S sigma (a scale of 0 counts as the smallest: -inf stays)
+                        const uint4 sk = *reinterpret_cast<const uint4*>(&par[32 * e + c]);
+                        const uint32_t two[4] = {sk.x, sk.y, sk.z, sk.w};
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) s[e][c + j] = __float_as_uint(x[j]);
-                        tops[2 * e] = fmaxf(tops[2 * e], fmaxf(x[0], x[1]));
-                        tops[2 * e + 1] = fmaxf(tops[2 * e + 1], fmaxf(x[2], x[3]));
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two[j]));
+                            uint32_t* x = &s[e][c + 2 * j];
+                            float x0, x1;
+                            unpair2(mul_f2(pair2(__uint_as_float(x[0]), __uint_as_float(x[1])), pair2(f.x, f.y)), x0, x1);
+                            x[0] = __float_as_uint(x0), x[1] = __float_as_uint(x1);
+                            tops[j] = fmaxf(tops[j], fmaxf(x0, x1));
+                        }
                     }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.par_empty[stage]);
-                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a.scale2;
                 if (__any_sync(~0u, top > M + kSlack)) {
                     const float m2 = fmaxf(M, top), f = ex2(M - m2);
                     const uint64_t ff = pair2(f, f);
@@ -736,15 +744,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                         }
                     }
                 }
-                const uint64_t ref = pair2(kTileBias - M, kTileBias - M);
+                const uint64_t ref = pair2(kTileBias - M, kTileBias - M), scale2 = pair2(a.scale2, a.scale2);
                 uint32_t w[32];
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
                     for (int c = 0; c < 32; c += 4) {
                         float p[4];
-                        unpair2(add_f2(pair2(__uint_as_float(s[e][c]), __uint_as_float(s[e][c + 1])), ref), p[0], p[1]);
-                        unpair2(add_f2(pair2(__uint_as_float(s[e][c + 2]), __uint_as_float(s[e][c + 3])), ref), p[2],
+                        unpair2(fma_f2(pair2(__uint_as_float(s[e][c]), __uint_as_float(s[e][c + 1])), scale2, ref), p[0],
+                                p[1]);
+                        unpair2(fma_f2(pair2(__uint_as_float(s[e][c + 2]), __uint_as_float(s[e][c + 3])), scale2, ref), p[2],
                                 p[3]);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) p[j] = ex2(p[j]);
@@ -877,7 +886,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
     } else if (works) {
         // ------------------------------------------------ tiles of K and V
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
-        // units of 16 tokens: those of a step's K tile, of its V tile, of the next step's, ..; this warp
+        // units of 32 tokens: those of a step's K tile, of its V tile, of the next step's, ..; this warp
         // takes every kProducers-th
         uint32_t step = 0, unit = warp - 8;
         int n = 0;  // the step's tile in the segment
@@ -889,30 +898,31 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                 }
             return wk.n > 0;
         };
-        const auto token = [&] { return (wk.it.u0 + wk.u + n) * kTileTokens + 16 * (int)(unit % kUnits); };
+        const auto token = [&] { return (wk.it.u0 + wk.u + n) * kTileTokens + kUnitTokens * (int)(unit % kUnits); };
+        int page0 = 0, page1 = 0;
         const auto look_up = [&] {  // a unit ahead of the codes
-            const int tok = token();
-            return tok + 16 > wk.it.t0 && tok < wk.it.t1
-                       ? a.b.table[(long long)wk.it.s * a.b.table_stride + (tok >> a.p.page_log2)] : 0;
+            const int tok = token(), t0 = wk.it.t0, t1 = wk.it.t1;
+            const int* row = a.b.table + (long long)wk.it.s * a.b.table_stride;
+            page0 = tok + 16 > t0 && tok < t1 ? row[tok >> a.p.page_log2] : 0;
+            page1 = tok + 32 > t0 && tok + 16 < t1 ? row[(tok + 16) >> a.p.page_log2] : 0;
         };
         bool more = seek();
-        int page = more ? look_up() : 0;
+        if (more) look_up();
         while (more) {
-            const uint32_t is_v = unit / kUnits & 1, rows = 16 * (unit % kUnits);
+            const uint32_t is_v = unit / kUnits & 1, rows = kUnitTokens * (unit % kUnits);
             const uint32_t stage = step % kParStages, turn = step / kParStages;
             const uint32_t seq = 2 * step + is_v, buf = seq % kRingTiles, round = seq / kRingTiles;
             Unit<D> un;
-            un.fetch(g, wk.it, token(), is_v, page);
+            un.fetch(g, wk.it.h, wk.it.t0, wk.it.t1, token(), is_v, page0, page1);
             unit += kProducers;
             more = seek();
-            if (more) page = look_up();
+            if (more) look_up();
             if (round > 0 && !wait(&sm.empty[buf], (round - 1) & 1)) break;
             if (!is_v) {
                 if (turn > 0 && !wait(&sm.par_empty[stage], (turn - 1) & 1)) break;
                 const uint32_t absent = __ballot_sync(~0u, un.absent);
-                // (never 0: a score of -inf stays -inf; a zero vector's scores are 0 all the same)
-                if (lane < 16) sm.par[stage][rows + lane] = fmaxf(__half2float(un.scale) * a.scale2, 1e-37f);
-                if (lane == 0) sm.absent[stage][rows / 16] = (uint16_t)absent;
+                sm.par[stage][rows + lane] = __hmax(un.scale, __ushort_as_half(1));
+                if (lane == 0) sm.absent[stage][rows / kUnitTokens] = absent;
             }
             un.store(sm.ring[buf], rows, is_v);
             fence_proxy_async_smem();
