@@ -21,6 +21,8 @@ namespace {
 
 constexpr int64_t kMaxIndex = int64_t(1) << 31;
 constexpr int kMaxGroup = 256;  // query heads per kv head
+// Sequences of more query rows a kv head than this go to the tile kernel.
+constexpr int kMany = 32;
 
 struct NvtxRange {
     explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
@@ -196,9 +198,6 @@ struct StepShape {
     static constexpr int kWarps = NQ == 16 ? 4 : 8, kPerSm = NQ == 16 ? 3 : 2;
 };
 
-// Sequences of more query rows a kv head than this go to the tile kernel.
-constexpr int kMany = 32;
-
 // Which kernels a call needs, from what the host knows of it.
 struct AttnPlan {
     bool tiles;        // some sequence may have more than kMany query rows a kv head
@@ -303,7 +302,8 @@ kvq_status check_attention(const kvq_config* cfg, const kvq_pages* p, const kvq_
     const kvq_status s = check_paged(cfg, p, b, rows);
     if (s != KVQ_OK) return s;
     if (q_heads < p->kv_heads || q_heads % p->kv_heads != 0) return KVQ_ERR_INVALID_ARG;
-    if (q_heads / p->kv_heads > kMaxGroup || q_heads > 65535 || rows >= kMaxIndex / q_heads)
+    if (q_heads / p->kv_heads > kMaxGroup || q_heads > 65535 || rows >= kMaxIndex / q_heads ||
+        b->n_seqs >= kMaxIndex / (kMany * (int64_t)q_heads))  // prepared queries are counted in 32 bits
         return KVQ_ERR_UNSUPPORTED;
     return KVQ_OK;
 }

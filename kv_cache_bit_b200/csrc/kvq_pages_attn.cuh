@@ -38,21 +38,25 @@ struct AttnArgs {
     int4* meta;          // [CTA]: sequence, head, first query, merged slots (0: nothing to merge)
 };
 
-// Tokens [t0, t1) that rows lo .. hi - 1 of sequence s see between them.
+// Tokens [t0, t1) that rows lo .. hi - 1 of a sequence see between them; its
+// rows end before row `end` (hi <= end) and it has len >= 0 tokens.
 struct Range {
     int t0, t1;
 };
+__device__ __forceinline__ Range seen_by(const AttnArgs& a, int len, int first, int last) {  // rows' tokens
+    const int t1 = a.causal ? min(last + 1, len) : len;
+    const int t0 = a.causal && a.window > 0 && first >= a.window ? first - a.window + 1 : 0;
+    return t0 < t1 ? Range{t0, t1} : Range{0, 0};
+}
 __device__ __forceinline__ Range range_of(const AttnArgs& a, int len, int end, int lo, int hi) {
-    const long long n = max(len, 0), first = (long long)len - end + lo, last = (long long)len - end + hi;
-    long long t1 = a.causal ? min(last, n) : n;
-    const long long t0 = a.causal && a.window > 0 ? max(first - a.window + 1, 0ll) : 0;
-    const long long cap = (long long)a.b.max_pages << a.p.page_log2;
-    if (t1 > cap) {
-        if (t0 < t1) report_error(kErrRange);
-        t1 = cap;
+    Range r = seen_by(a, len, len + (lo - end), len + (hi - 1 - end));
+    const int cap = a.b.max_pages << a.p.page_log2;  // below 2^31
+    if (r.t1 > cap) {
+        report_error(kErrRange);
+        r.t1 = cap;
+        if (r.t0 >= cap) r = Range{0, 0};
     }
-    if (t1 <= t0) return Range{0, 0};
-    return Range{(int)t0, (int)t1};
+    return r;
 }
 
 __device__ __forceinline__ float ex2(float x) {

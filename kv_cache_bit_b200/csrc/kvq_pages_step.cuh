@@ -58,9 +58,6 @@ struct StepArgs {
     float4* scal;
     int stretch;
 };
-__device__ __forceinline__ long long place_of(const StepArgs& g, int s, int lo, int r) {
-    return g.many > 0 ? (long long)s * g.stretch + r : (long long)lo + r;
-}
 
 // A sequence's share of the work.
 struct Item {
@@ -72,29 +69,22 @@ struct Item {
 template <int NQ>
 __device__ __forceinline__ Item item_of(const StepArgs& g, int s, int H) {
     Item it;
-    const int end = g.a.b.start[s + 1];
+    const int from = g.a.b.start[s], end = g.a.b.start[s + 1], len = max(g.a.b.len[s], 0);
     const int hi = min(end, g.a.rows);
     it.s = s;
-    it.lo = max(g.a.b.start[s], 0);
-    const int rows = hi - it.lo;
-    it.cost = 0;
-    it.nq = 0;
-    if (rows <= 0) return it;
-    it.nq = rows * g.a.G;
-    if (g.many > 0 && it.nq > g.many) {
-        it.nq = 0;
-        return it;
-    }
-    const int len = g.a.b.len[s];
-    it.len = max(len, 0);
+    it.lo = max(from, 0);
+    it.nq = max(hi - it.lo, 0) * g.a.G;
+    it.len = len;
     it.base = len - end;
+    it.cost = 0;
+    if (it.nq == 0 || (g.many > 0 && it.nq > g.many)) return it;
     const Range r = range_of(g.a, len, end, it.lo, hi);
     it.t0 = r.t0;
     it.t1 = r.t1;
     it.u0 = r.t0 / kUnit;
     it.units = max((r.t1 + kUnit - 1) / kUnit - it.u0, 1);  // rows that see nothing need an owner too
     it.chunks = (it.nq + NQ - 1) / NQ;
-    it.cost = (long long)H * it.chunks * it.units;
+    it.cost = (long long)(H * it.chunks) * it.units;
     return it;
 }
 
@@ -172,7 +162,7 @@ struct StepSmem {
         Part part[2];         // of the range's first item and of its last
     };
     Warp warp[NW];
-    long long sums[NW];
+    long long sums[NW], before[NW * 32];
 };
 
 __device__ __forceinline__ float max_or_nan(float x, float y) { return x != x || y <= x ? x : y; }
@@ -243,13 +233,12 @@ __device__ __forceinline__ int query_of(int v, int t) {
     return HAD ? 4 * v + t : 8 * (v >> 1) + 2 * t + (v & 1);
 }
 
-// Tokens that query i of an item sees.
-__device__ __forceinline__ Range query_range(const AttnArgs& a, const Item& it, int i) {
-    if (i >= it.nq) return Range{0, 0};
-    const long long pos = (long long)it.base + it.lo + i / a.G;
-    const long long hi = min(a.causal ? pos + 1 : (long long)it.len, (long long)it.t1);
-    const long long lo = a.causal && a.window > 0 ? max(pos - a.window + 1, 0ll) : 0;
-    return lo < hi ? Range{(int)lo, (int)hi} : Range{0, 0};
+// Tokens that a row of an item sees, the r-th of the sequence's.
+__device__ __forceinline__ Range row_range(const AttnArgs& a, const Item& it, int r) {
+    const int pos = it.base + it.lo + r;
+    Range see = seen_by(a, it.len, pos, pos);
+    see.t1 = min(see.t1, it.t1);
+    return see;
 }
 
 template <int D, int NQ, bool HAD, int NW, int PER_SM>
@@ -271,12 +260,8 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
 
     // ---- the warps' ranges: prefix sums of the sequences' costs, a run of `per` sequences a thread
     const int per = (a.b.n_seqs + NW * 32 - 1) / (NW * 32), s0 = threadIdx.x * per;
-    Item first;
     long long mine = 0;
-    for (int s = min(s0 + per, a.b.n_seqs) - 1; s >= s0; --s) {  // the last one read is the run's first
-        first = item_of<NQ>(g, s, H);
-        mine += first.cost;
-    }
+    for (int s = s0; s < min(s0 + per, a.b.n_seqs); ++s) mine += item_of<NQ>(g, s, H).cost;
     long long sum = mine;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
@@ -301,33 +286,30 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
     const int extra = (int)(total - share * workers);
     const auto begin_of = [&](int worker) { return share * worker + min(worker, extra); };
     const int me = blockIdx.x * NW + warp;
-    for (int w = 0; w < NW; ++w) {  // the thread whose run holds a range's first unit publishes the run
-        const long long x = begin_of(blockIdx.x * NW + w);
-        if (blockIdx.x * NW + w < workers && before <= x && x < before + mine) {
-            sh.warp[w].own.x = x - before;
-            sh.warp[w].own.it = first;
-        }
-    }
+    sh.before[threadIdx.x] = before;
     __syncthreads();
-    if (lane == 0) {
-        if (me < workers) {
-            long long off = wk.x;
-            while (off >= wk.it.cost && wk.it.s + 1 < a.b.n_seqs) {
-                off -= wk.it.cost;
-                wk.it = item_of<NQ>(g, wk.it.s + 1, H);
-            }
-            wk.x = begin_of(me);
-            wk.end = begin_of(me + 1);
-            wk.place(off);
-        } else {
-            wk.n = 0;
-        }
-    }
-    __syncwarp();
     {
-        constexpr int kWords = sizeof(Walk<NQ>) / 4;
-        static_assert(sizeof(Walk<NQ>) % 4 == 0 && kWords <= 32);
-        if (lane < kWords) reinterpret_cast<int*>(&pw)[lane] = reinterpret_cast<const int*>(&wk)[lane];
+        Walk<NQ> w;
+        w.n = 0;
+        if (me < workers) {
+            w.x = begin_of(me);
+            w.end = begin_of(me + 1);
+            int lo = 0, hi = NW * 32;  // the run that holds the range's first unit
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (sh.before[mid] <= w.x) lo = mid;
+                else hi = mid;
+            }
+            long long off = w.x - sh.before[lo];
+            w.it = item_of<NQ>(g, lo * per, H);
+            while (off >= w.it.cost && w.it.s + 1 < a.b.n_seqs) {
+                off -= w.it.cost;
+                w.it = item_of<NQ>(g, w.it.s + 1, H);
+            }
+            w.place(off);
+        }
+        if (lane == 0) wk = w;
+        if (lane == 1) pw = w;
     }
     __syncwarp();
 
@@ -394,16 +376,35 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
         const bool final = wk.x + wk.n >= wk.end;  // the range's last segment
         float M[NV], l[NV], cq[NV], c_init[QT][2];
         float o[NP][NJ][4], sums[NP][4];  // sums: of w
+        const int i0 = wk.c * NQ, lo = wk.it.lo, nq = wk.it.nq;
+        // index of query i of the item among the prepared ones
+        const int query0 = (g.many > 0 ? wk.it.s * g.stretch : lo) * a.Hq + wk.h * a.G;
+        const auto prepared = [&](int i, int r) { return query0 + r * a.Hq + i - r * a.G; };
+        constexpr bool kHold = QT * (D / 32) <= 4;  // few enough fragments to stay in registers
+        uint4 qf[QT][D / 32];
+#pragma unroll
+        for (int n = 0; n < QT; ++n) {  // column r8 of tile n
+            const int i = i0 + (HAD ? 4 * n + (r8 >> 1) : 8 * n + r8);
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) qf[n][k] = make_uint4(0, 0, 0, 0);
+            if (i < nq) {
+                const long long at = prepared(i, i / a.G);
+                const uint4* src = reinterpret_cast<const uint4*>(g.frag + (HAD ? 2 * at + (r8 & 1) : at) * D) + t;
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) qf[n][k] = src[4 * k];
+            }
+        }
         int lo_max = 0, hi_min = 0x7FFFFFFF;  // tokens that all of the chunk's rows see
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             M[v] = kLowest;
             l[v] = 0.0f;
-            const int i = wk.c * NQ + query_of<HAD>(v, t), r = i / a.G;
+            const int i = i0 + query_of<HAD>(v, t);
             float4 sc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (i < wk.it.nq) {
-                sc = g.scal[place_of(g, wk.it.s, wk.it.lo, r) * a.Hq + wk.h * a.G + i - r * a.G];
-                const Range see = query_range(a, wk.it, i);
+            if (i < nq) {
+                const int r = i / a.G;
+                sc = g.scal[prepared(i, r)];
+                const Range see = row_range(a, wk.it, r);
                 lo_max = max(lo_max, see.t0);
                 hi_min = min(hi_min, see.t1);
             }
@@ -422,25 +423,13 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
 #pragma unroll
             for (int k = 0; k < 4; ++k) sums[n][k] = 0.0f;
         }
-        constexpr bool kHold = QT * (D / 32) <= 4;  // few enough fragments to stay in registers
-        uint4 qf[kHold ? QT : 1][kHold ? D / 32 : 1];
+        if constexpr (!kHold) {
 #pragma unroll
-        for (int n = 0; n < QT; ++n) {  // column r8 of tile n
-            const int i = wk.c * NQ + (HAD ? 4 * n + (r8 >> 1) : 8 * n + r8), r = i / a.G;
-            uint4 w[D / 32] = {};
-            if (i < wk.it.nq) {
-                const long long at = place_of(g, wk.it.s, wk.it.lo, r) * a.Hq + wk.h * a.G + i - r * a.G;
-                const uint4* src = reinterpret_cast<const uint4*>(g.frag + (HAD ? 2 * at + (r8 & 1) : at) * D) + t;
+            for (int n = 0; n < QT; ++n)
 #pragma unroll
-                for (int k = 0; k < D / 32; ++k) w[k] = src[4 * k];
-            }
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-                if constexpr (kHold) qf[n][k] = w[k];
-                else *reinterpret_cast<uint4*>(sm.q[n][k][lane]) = w[k];
-            }
+                for (int k = 0; k < D / 32; ++k) *reinterpret_cast<uint4*>(sm.q[n][k][lane]) = qf[n][k];
+            __syncwarp();
         }
-        __syncwarp();
 
         for (int off = 0; off < units; ++off) {
             const int tok0 = (unit0 + off) * kUnit;
@@ -482,7 +471,7 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
                     }
 #pragma unroll
                     for (int n = 0; n < QT; ++n) {
-                        const uint4 f = kHold ? qf[n * kHold][i * kHold]
+                        const uint4 f = kHold ? qf[n][i]
                                               : *reinterpret_cast<const uint4*>(sm.q[n][i][lane]);
                         mma(s[n], x[0], f.x, f.y);
                         mma(s[n], x[1], f.z, f.w);
@@ -501,7 +490,8 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
             if (tok0 < lo_max || tok0 + kUnit > hi_min) {
 #pragma unroll
                 for (int v = 0; v < NV; ++v) {
-                    const Range see = query_range(a, wk.it, wk.c * NQ + query_of<HAD>(v, t));
+                    const int i = i0 + query_of<HAD>(v, t);
+                    const Range see = i < nq ? row_range(a, wk.it, i / a.G) : Range{0, 0};
 #pragma unroll
                     for (int mt = 0; mt < 2; ++mt)
 #pragma unroll

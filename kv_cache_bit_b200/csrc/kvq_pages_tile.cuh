@@ -74,7 +74,7 @@ __device__ __forceinline__ bool tile_seq(const TileArgs& g, int s, TileItem& it)
     it.nq = max(hi - lo, 0) * g.a.G;
     it.chunks = 0;
     if (it.nq <= g.many) return false;
-    const int len = g.a.b.len[s];
+    const int len = max(g.a.b.len[s], 0);
     it.len = len;
     it.base = len - end;
     it.chunks = (it.nq + kItemRows - 1) / kItemRows;
@@ -597,10 +597,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                 const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + row * a.q_row +
                                                                   head * a.q_head);
                 if (there) {
-                    const long long n = max(it.len, 0), pos = (long long)it.base + row;
-                    const long long t1 = min(a.causal ? min(pos + 1, n) : n, (long long)it.t1);
-                    const long long t0 = a.causal && a.window > 0 ? max(pos - a.window + 1, 0ll) : 0;
-                    see = t0 < t1 ? Range{(int)t0, (int)t1} : Range{0, 0};
+                    see = seen_by(a, it.len, it.base + row, it.base + row);
+                    see.t1 = min(see.t1, it.t1);
                 }
 #pragma unroll
                 for (int k = 0; k < D / 8; ++k) {
