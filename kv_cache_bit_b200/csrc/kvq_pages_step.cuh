@@ -44,6 +44,9 @@ namespace kvq {
 
 constexpr int kUnit = 32;  // tokens of a ring slot: one a lane
 constexpr int kRingPages = 2;
+// What an item costs a warp besides its units (queries, the state's way out), in units: the kernel ends with
+// the warps that have two items.
+constexpr int kStepCost = 2;
 
 template <int D>
 constexpr int slot_bytes() { return kUnit * (D + 4); }  // K codes, V codes, K scales, V scales
@@ -84,7 +87,7 @@ __device__ __forceinline__ Item item_of(const StepArgs& g, int s, int H) {
     it.u0 = r.t0 / kUnit;
     it.units = max((r.t1 + kUnit - 1) / kUnit - it.u0, 1);  // rows that see nothing need an owner too
     it.chunks = (it.nq + NQ - 1) / NQ;
-    it.cost = (long long)(H * it.chunks) * it.units;
+    it.cost = (long long)(H * it.chunks) * (it.units + kStepCost);
     return it;
 }
 
@@ -93,42 +96,51 @@ __device__ __forceinline__ long long quotient(long long x, long long y) {
     return (x | y) >> 32 ? x / y : (long long)((uint32_t)x / (uint32_t)y);
 }
 
-// A walk over the segments of [x, end) of the work.
+// A walk over the segments of [x, end) of the work.  An item takes
+// kStepCost + units positions, of which the first kStepCost hold no unit.
 template <int NQ>
 struct Walk {
     long long x, end;  // the current segment begins at x
     Item it;
-    int h, c, u, n;    // head, chunk, first unit and units of the segment
+    int h, c, u, n;    // head, chunk, first unit and units of the segment; n = 0: the end
+    int pos, span;     // where in the item the segment begins, and its positions
 
-    // x, inside sequence it.s at offset `off` from its first unit.
-    __device__ __forceinline__ void place(long long off) {
-        const long long k = quotient(off, it.units), kh = quotient(k, it.chunks);
-        u = (int)(off - k * it.units);
+    __device__ __forceinline__ void cut() {
+        span = (int)min((long long)(it.units + kStepCost - pos), end - x);
+        u = max(pos - kStepCost, 0);
+        n = max(pos + span - kStepCost, 0) - u;
+    }
+    // x, inside sequence it.s at offset `off` from its first item.
+    __device__ __forceinline__ void place(const StepArgs& g, int H, long long off) {
+        const int all = it.units + kStepCost;
+        const long long k = quotient(off, all), kh = quotient(k, it.chunks);
+        pos = (int)(off - k * all);
         c = (int)(k - kh * it.chunks);
         h = (int)kh;
-        n = (int)min((long long)(it.units - u), end - x);
+        cut();
+        if (n == 0) next(g, H);
     }
     __device__ __forceinline__ void next(const StepArgs& g, int H) {
-        x += n;
-        if (x >= end) {
+        do {
+            x += span;
             n = 0;
-            return;
-        }
-        u = 0;
-        if (++c == it.chunks) {
-            c = 0;
-            if (++h == H) {
-                h = 0;
-                do {
-                    if (it.s + 1 >= g.a.b.n_seqs) {
-                        n = 0, end = x;
-                        return;
-                    }
-                    it = item_of<NQ>(g, it.s + 1, H);
-                } while (it.cost == 0);
+            if (x >= end) return;
+            pos = 0;
+            if (++c == it.chunks) {
+                c = 0;
+                if (++h == H) {
+                    h = 0;
+                    do {
+                        if (it.s + 1 >= g.a.b.n_seqs) {
+                            end = x;
+                            return;
+                        }
+                        it = item_of<NQ>(g, it.s + 1, H);
+                    } while (it.cost == 0);
+                }
             }
-        }
-        n = (int)min((long long)it.units, end - x);
+            cut();
+        } while (n == 0);
     }
 };
 
@@ -306,7 +318,7 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
                 off -= w.it.cost;
                 w.it = item_of<NQ>(g, w.it.s + 1, H);
             }
-            w.place(off);
+            w.place(g, H, off);
         }
         if (lane == 0) wk = w;
         if (lane == 1) pw = w;
@@ -373,7 +385,7 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
     while (wk.n > 0) {
         const bool begins = wk.u == 0, ends = wk.u + wk.n == wk.it.units;
         const int units = wk.n, unit0 = wk.it.u0 + wk.u, seen0 = wk.it.t0, seen1 = wk.it.t1;
-        const bool final = wk.x + wk.n >= wk.end;  // the range's last segment
+        const bool final = wk.x + wk.span >= wk.end;  // the range's last segment
         float M[NV], l[NV], cq[NV], c_init[QT][2];
         float o[NP][NJ][4], sums[NP][4];  // sums: of w
         const int i0 = wk.c * NQ, lo = wk.it.lo, nq = wk.it.nq;
@@ -592,7 +604,7 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
         if (!whole && lane == 0) {
             int ctas = 1;
             if (begins) {
-                const long long last = wk.x + wk.it.units - 1, longer = (share + 1) * extra;
+                const long long last = wk.x - wk.pos + wk.it.units + kStepCost - 1, longer = (share + 1) * extra;
                 const int worker = (int)(last < longer ? quotient(last, share + 1) : extra + quotient(last - longer, share));
                 ctas = worker / NW - (int)blockIdx.x + 1;
             }
