@@ -101,6 +101,14 @@ Pool pool_of(const kvq_pages* p) {
 
 float rsqd_of(int d) { return (float)(1.0 / std::sqrt((double)d)); }
 
+// Heads of a row that a quad of lanes takes in turn: one while that leaves quads for every SM's schedulers
+// (a generation step), eight at most.
+int heads_a_quad(int64_t rows, int H) {
+    int per = 1;
+    while (per < 8 && per * 2 <= H && rows * H >= (int64_t)per * 2 * 148 * 512) per *= 2;
+    return per;
+}
+
 // Compile-time dispatch over (head_dim, element type, rotation).
 template <int D, typename T, typename Fn>
 kvq_status dispatch_had(bool had, Fn& fn) {
@@ -112,28 +120,6 @@ kvq_status dispatch(int d, int dtype, bool had, Fn& fn) {
     if (dtype == KVQ_F16) return d == 64 ? dispatch_had<64, __half>(had, fn) : dispatch_had<128, __half>(had, fn);
     return d == 64 ? dispatch_had<64, __nv_bfloat16>(had, fn) : dispatch_had<128, __nv_bfloat16>(had, fn);
 }
-
-struct WriteLaunch {
-    WriteArgs a;
-    unsigned grid;
-    cudaStream_t st;
-    template <int D, typename T, bool HAD>
-    kvq_status run() {
-        pages_write_kernel<D, T, HAD><<<dim3(grid, 2), kWriteThreads, 0, st>>>(a);
-        return launch_status();
-    }
-};
-
-struct ReadLaunch {
-    ReadArgs a;
-    unsigned grid;
-    cudaStream_t st;
-    template <int D, typename T, bool HAD>
-    kvq_status run() {
-        pages_read_kernel<D, T, HAD><<<dim3(grid, a.only >= 0 ? 1 : 2), kWriteThreads, 0, st>>>(a);
-        return launch_status();
-    }
-};
 
 // Launch as a programmatic dependent of the kernel ahead of it in the stream:
 // the kernels wait for that one (grid_dep_wait) before they read anything.
@@ -155,6 +141,26 @@ kvq_status launch(void (*kernel)(A...), dim3 grid, int threads, int smem, cudaSt
     }
     return launch_status();
 }
+
+struct WriteLaunch {
+    WriteArgs a;
+    unsigned grid;
+    cudaStream_t st;
+    template <int D, typename T, bool HAD>
+    kvq_status run() {
+        return launch(pages_write_kernel<D, T, HAD>, dim3(grid, 2), kWriteThreads, 0, st, a);
+    }
+};
+
+struct ReadLaunch {
+    ReadArgs a;
+    unsigned grid;
+    cudaStream_t st;
+    template <int D, typename T, bool HAD>
+    kvq_status run() {
+        return launch(pages_read_kernel<D, T, HAD>, dim3(grid, a.only >= 0 ? 1 : 2), kWriteThreads, 0, st, a);
+    }
+};
 
 // Dynamic shared memory and the largest carveout, once per kernel and device
 // (racing callers set the same attributes, which is harmless).
@@ -338,7 +344,8 @@ kvq_status kvq_pages_write(const kvq_config* cfg, const kvq_pages* pages, const 
     L.a.signs = cfg->signs;
     L.a.rows = (int)rows;
     L.a.rsqd = rsqd_of(d);
-    L.grid = (unsigned)((rows * H * 4 + kWriteThreads - 1) / kWriteThreads);
+    L.a.per = heads_a_quad(rows, H);
+    L.grid = (unsigned)((rows * ((H + L.a.per - 1) / L.a.per) * 4 + kWriteThreads - 1) / kWriteThreads);
     L.st = static_cast<cudaStream_t>(stream);
     return dispatch(d, k->dtype, cfg->flags == KVQ_HADAMARD, L);
 }
@@ -369,7 +376,8 @@ kvq_status kvq_pages_read(const kvq_config* cfg, const kvq_pages* pages, const k
     L.a.rows = (int)rows;
     L.a.only = k_out == nullptr ? 1 : v_out == nullptr ? 0 : -1;
     L.a.rsqd = rsqd_of(d);
-    L.grid = (unsigned)((rows * H * 4 + kWriteThreads - 1) / kWriteThreads);
+    L.a.per = heads_a_quad(rows, H);
+    L.grid = (unsigned)((rows * ((H + L.a.per - 1) / L.a.per) * 4 + kWriteThreads - 1) / kWriteThreads);
     L.st = static_cast<cudaStream_t>(stream);
     const bool had = cfg->flags == KVQ_HADAMARD;
     const int dtype = (k_out ? k_out : v_out)->dtype;

@@ -2,10 +2,18 @@
 // reading them back.
 //
 // One vector (a row's head of K or V) belongs to a quad of lanes; lane t of
-// the quad holds its channels [t D/4, (t + 1) D/4), so that a lane's codes are
-// one 16-byte (D = 128) or 8-byte store and a vector's codes one contiguous
-// run.  Butterflies of strides below D/4 stay in the lane's registers, the
-// last two exchange with lanes t ^ 1 and t ^ 2.
+// the quad holds its eight-channel pieces t, t + 4, .., so that a quad's loads
+// and stores of 16-bit values are 64 bytes in a row.  Butterflies of strides
+// 1, 2, 4 and 32, 64 stay in the lane's registers, those of strides 8 and 16
+// exchange with lanes t ^ 1 and t ^ 2.  Where there are enough vectors to fill
+// the GPU a quad takes several heads of its row: the search for the row's
+// sequence and page, about as many instructions as half a vector, is then made
+// once for them.
+//
+// Both are bound by HBM when they are long.  Instructions a vector (D = 128,
+// rotated): writing, in packed fp32 pairs, about 90 a lane of which 24 are
+// shuffles; reading, whose butterflies are exact in fp16 pairs (sums of codes
+// stay below 1024), about 75.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -114,6 +122,70 @@ __device__ __forceinline__ void lane_stages(float (&v)[N]) {
     if constexpr (2 * H < N) lane_stages<2 * H, N>(v);
 }
 
+// Packed fp32 pairs.
+__device__ __forceinline__ uint64_t pair2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpair2(uint64_t v, float& x, float& y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f2(uint64_t x, uint64_t y, uint64_t z) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul_f2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+// Packed fp16 pairs.
+__device__ __forceinline__ uint32_t add_h2(uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
+}
+__device__ __forceinline__ uint32_t sub_h2(uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
+}
+__device__ __forceinline__ uint32_t fma_h2(uint32_t x, uint32_t y, uint32_t z) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
+    return r;
+}
+template <uint32_t MASK, uint32_t BASE>
+__device__ __forceinline__ uint32_t in_mantissa(uint32_t w) {  // (w & MASK) | BASE: one lop3
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "r"(BASE));
+    return r;
+}
+// The codes of nibbles 0 and 4 of a word as two fp16, exactly.
+__device__ __forceinline__ uint32_t codes_low(uint32_t w) {  // (1024 + e) - 1032
+    return add_h2(in_mantissa<0x000F000Fu, 0x64006400u>(w), 0xE408E408u);
+}
+// Those of nibbles 1 and 5: (1024 + 16 e) / 16 - 72.
+__device__ __forceinline__ uint32_t codes_upper(uint32_t w) {
+    return fma_h2(in_mantissa<0x00F000F0u, 0x64006400u>(w), 0x2C002C00u, 0xD480D480u);
+}
+
+// A row's sequence, page and slot (head 0), or -1.
+__device__ __forceinline__ long long slot_of_row(const Batch& b, const Pool& p, const int* start, int row, int* seq) {
+    const int s = owner_of(start, b.n_seqs, row);
+    *seq = s;
+    if (s < 0) return -1;
+    const int pos = b.len[s] - (start[s + 1] - start[s]) + (row - start[s]);
+    return pos >= 0 ? slot_of(b, p, s, pos) : -1;
+}
+
 struct WriteArgs {
     Batch b;
     Pool p;
@@ -121,99 +193,165 @@ struct WriteArgs {
     long long row_stride[2], head_stride[2];  // elements
     const int8_t* signs;
     int rows;
+    int per;  // heads a quad takes
     float rsqd;
 };
 
 constexpr int kWriteThreads = 256;
 
-// blockIdx.y: K or V; a quad of lanes per (row, head) vector.
+// blockIdx.y: K or V.
 template <int D, typename T, bool HAD>
 __global__ void __launch_bounds__(kWriteThreads) pages_write_kernel(WriteArgs a) {
-    constexpr int N = D / 4;  // channels a lane
+    constexpr int KC = D / 32;  // pieces a lane
     __shared__ int s_start[kStartStage];
-    const int i = blockIdx.y, t = threadIdx.x & 3;
+    __shared__ alignas(16) uint32_t s_sign[D / 2];  // sign bits of two neighbouring channels' signs
+    const int i = blockIdx.y, t = threadIdx.x & 3, H = a.p.H;
+    grid_dep_wait();
+    grid_dep_launch();
     const int* start = stage_start(a.b, s_start);
-    const int vec = (int)((blockIdx.x * (unsigned)kWriteThreads + threadIdx.x) >> 2);
-    const int row = vec / a.p.H, h = vec - row * a.p.H;
-    uint32_t u[N / 2];
-    if (row < a.rows) {
-        const T* src = static_cast<const T*>(a.x[i]) + row * a.row_stride[i] + h * a.head_stride[i] + t * N;
+    if (HAD && threadIdx.x < D / 2)
+        s_sign[threadIdx.x] = a.signs == nullptr ? 0u
+                                                 : (a.signs[2 * threadIdx.x] < 0 ? 0x8000u : 0u) |
+                                                       (a.signs[2 * threadIdx.x + 1] < 0 ? 0x80000000u : 0u);
+    const int groups = (H + a.per - 1) / a.per;
+    const int quad = (int)((blockIdx.x * (unsigned)kWriteThreads + threadIdx.x) >> 2);
+    const int row = quad / groups, h0 = (quad - row * groups) * a.per, h1 = min(h0 + a.per, H);
+    const T* src = static_cast<const T*>(a.x[i]) + row * a.row_stride[i] + t * 8;
+    uint4 next[KC];
+    const auto load = [&](int h) {
 #pragma unroll
-        for (int k = 0; k < N / 8; ++k) {
-            const uint4 w = reinterpret_cast<const uint4*>(src)[k];
-            u[4 * k] = w.x, u[4 * k + 1] = w.y, u[4 * k + 2] = w.z, u[4 * k + 3] = w.w;
-        }
-    }
+        for (int k = 0; k < KC; ++k)
+            next[k] = *reinterpret_cast<const uint4*>(src + h * a.head_stride[i] + 32 * k);
+    };
+    if (row < a.rows) load(h0);
     __syncthreads();
-    int s = -1;
-    if (row < a.rows) s = owner_of(start, a.b.n_seqs, row);
-    long long slot = -1;
-    if (s >= 0) {
-        const int pos = a.b.len[s] - (start[s + 1] - start[s]) + (row - start[s]);
-        if (pos >= 0) slot = slot_of(a.b, a.p, s, pos);
-    }
-    if (slot < 0) return;  // the four lanes of a quad agree
+    if (row >= a.rows) return;
+    int seq;
+    const long long slot0 = slot_of_row(a.b, a.p, start, row, &seq);
+    if (slot0 < 0) return;  // the four lanes of a quad agree
 
-    const uint32_t quad = 0xFu << (threadIdx.x & 28);
-    uint32_t big = 0;
+    const uint32_t lanes = 0xFu << (threadIdx.x & 28);
+#pragma unroll 1
+    for (int h = h0; h < h1; ++h) {
+        uint32_t u[4 * KC], big = 0;
 #pragma unroll
-    for (int k = 0; k < N / 2; ++k) big = max_u16x2(big, u[k] & 0x7FFF7FFFu);
-    float v[N];
+        for (int k = 0; k < KC; ++k) {
+            u[4 * k] = next[k].x, u[4 * k + 1] = next[k].y, u[4 * k + 2] = next[k].z, u[4 * k + 3] = next[k].w;
 #pragma unroll
-    for (int k = 0; k < N / 2; ++k) {
-        const float2 f = Elem<T>::wide(u[k]);
-        v[2 * k] = f.x, v[2 * k + 1] = f.y;
-    }
-    if ((big & 0xFFFFu) >= Elem<T>::kSpecial || (big >> 16) >= Elem<T>::kSpecial) {
+            for (int j = 0; j < 4; ++j) big = max_u16x2(big, u[4 * k + j] & 0x7FFF7FFFu);
+        }
+        if (h + 1 < h1) load(h + 1);
+        float v[8 * KC];  // piece k's channels at 8 k
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = clean(v[k]);
-    }
-    if constexpr (HAD) {
-        if (a.signs != nullptr) {
+        for (int k = 0; k < 4 * KC; ++k) {
+            const float2 f = Elem<T>::wide(u[k]);
+            v[2 * k] = f.x, v[2 * k + 1] = f.y;
+        }
+        if ((big & 0xFFFFu) >= Elem<T>::kSpecial || (big >> 16) >= Elem<T>::kSpecial) {
 #pragma unroll
-            for (int k = 0; k < N / 4; ++k) {
-                const char4 c = reinterpret_cast<const char4*>(a.signs + t * N)[k];
-                v[4 * k] *= c.x, v[4 * k + 1] *= c.y, v[4 * k + 2] *= c.z, v[4 * k + 3] *= c.w;
+            for (int k = 0; k < 8 * KC; ++k) v[k] = clean(v[k]);
+        }
+        if constexpr (HAD) {
+            if (a.signs != nullptr) {
+#pragma unroll
+                for (int k = 0; k < KC; ++k) {
+                    const uint4 sg = *reinterpret_cast<const uint4*>(&s_sign[(4 * k + t) * 4]);
+                    const uint32_t w[4] = {sg.x, sg.y, sg.z, sg.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float* x = &v[8 * k + 2 * j];
+                        x[0] = __uint_as_float(__float_as_uint(x[0]) ^ (w[j] << 16));
+                        x[1] = __uint_as_float(__float_as_uint(x[1]) ^ (w[j] & 0x80000000u));
+                    }
+                }
             }
         }
-        lane_stages<1, N>(v);
+        // pairs of pieces KC / 2 apart, so that all strides but the last are whole pairs'
+        constexpr int NP = 4 * KC, KH = KC / 2;
+        uint64_t p[NP];
 #pragma unroll
-        for (int x = 1; x <= 2; x <<= 1) {
-            const float sg = (t & x) ? -1.0f : 1.0f;
+        for (int k = 0; k < KH; ++k)
 #pragma unroll
-            for (int k = 0; k < N; ++k) v[k] = __fmaf_rn(v[k], sg, __shfl_xor_sync(quad, v[k], x));
+            for (int e = 0; e < 8; ++e) p[8 * k + e] = pair2(v[8 * k + e], v[8 * (k + KH) + e]);
+        if constexpr (HAD) {
+            const uint64_t minus = pair2(-1.0f, -1.0f);
+            const auto stage = [&](int x) {
+#pragma unroll
+                for (int k = 0; k < NP; ++k)
+                    if (!(k & x)) {
+                        const uint64_t lo = p[k], hi = p[k + x];
+                        p[k] = add_f2(lo, hi);
+                        p[k + x] = fma_f2(hi, minus, lo);
+                    }
+            };
+            stage(1);
+            stage(2);
+            stage(4);
+#pragma unroll
+            for (int x = 1; x <= 2; x <<= 1) {
+                const float sg = (t & x) ? -1.0f : 1.0f;
+                const uint64_t sg2 = pair2(sg, sg);
+#pragma unroll
+                for (int k = 0; k < NP; ++k) {
+                    float f, g;
+                    unpair2(p[k], f, g);
+                    p[k] = fma_f2(p[k], sg2,
+                                  pair2(__shfl_xor_sync(lanes, f, x), __shfl_xor_sync(lanes, g, x)));
+                }
+            }
+            if constexpr (KH == 2) stage(8);
+            const uint64_t rs = pair2(a.rsqd, a.rsqd);
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                float f, g;
+                unpair2(p[k], f, g);
+                p[k] = mul_f2(pair2(__fadd_rn(f, g), __fsub_rn(f, g)), rs);
+            }
         }
+        float m = 0.0f;
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = __fmul_rn(v[k], a.rsqd);
+        for (int k = 0; k < NP; ++k) {
+            float f, g;
+            unpair2(p[k], f, g);
+            m = fmaxf(m, fmaxf(fabsf(f), fabsf(g)));
+        }
+        m = fmaxf(m, __shfl_xor_sync(lanes, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(lanes, m, 2));
+        const __half sigma = __float2half_rn(fminf(__fdiv_rn(m, 7.0f), 65504.0f));
+        const float sf = __half2float(sigma);
+        const float r = sf > 0.0f ? __frcp_rn(sf) : 0.0f;
+        // Codes from the low mantissa bits of fma(y, r, 1.5 2^23 + 8): the FMA
+        // rounds the exact product once, half to even.  Only a subnormal or
+        // saturated scale can send a product past 7.5.
+        if (__fmul_rn(m, r) > 7.25f) {
+            const float top = 7.0f / r;  // any |y| in [7 sigma, 7.5 sigma) has the code 7
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                float f, g;
+                unpair2(p[k], f, g);
+                p[k] = pair2(fminf(fmaxf(f, -top), top), fminf(fmaxf(g, -top), top));
+            }
+        }
+        const uint64_t r2 = pair2(r, r), magic = pair2(12582912.0f + 8.0f, 12582912.0f + 8.0f);
+        const long long slot = slot0 + ((long long)h << a.p.page_log2);
+        uint32_t* dst = reinterpret_cast<uint32_t*>(a.p.codes[i] + slot * (D / 2)) + t;
+#pragma unroll
+        for (int k = 0; k < KH; ++k) {
+            // sum of 16^e times the bits, 0x4B400000 + code each, modulo 2^32
+            uint32_t lo = 0, hi = 0;
+#pragma unroll
+            for (int e = 7; e >= 0; --e) {
+                float f, g;
+                unpair2(fma_f2(p[8 * k + e], r2, magic), f, g);
+                lo = lo * 16u + __float_as_uint(f);
+                hi = hi * 16u + __float_as_uint(g);
+            }
+            constexpr uint32_t kBase = 0x4B400000u * 0x11111111u;
+            dst[4 * k] = lo - kBase;
+            dst[4 * (k + KH)] = hi - kBase;
+        }
+        if (t == 0) a.p.tok[i][slot] = sigma;
     }
-    float m = 0.0f;
-#pragma unroll
-    for (int k = 0; k < N; ++k) m = fmaxf(m, fabsf(v[k]));
-    m = fmaxf(m, __shfl_xor_sync(quad, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(quad, m, 2));
-    const __half sigma = __float2half_rn(fminf(__fdiv_rn(m, 7.0f), 65504.0f));
-    const float sf = __half2float(sigma);
-    const float r = sf > 0.0f ? __frcp_rn(sf) : 0.0f;
-    // Codes from the low mantissa bits of fma(y, r, 1.5 2^23 + 8): the FMA
-    // rounds the exact product once, half to even.  Only a subnormal or
-    // saturated scale can send a product past 7.5.
-    if (__fmul_rn(m, r) > 7.25f) {
-        const float top = 7.0f / r;  // any |y| in [7 sigma, 7.5 sigma) has the code 7
-#pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = fminf(fmaxf(v[k], -top), top);
-    }
-    constexpr float kMagic = 12582912.0f + 8.0f;
-    uint32_t w[N / 8];
-#pragma unroll
-    for (int k = 0; k < N / 8; ++k) {
-        uint32_t x = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x |= (__float_as_uint(__fmaf_rn(v[8 * k + j], r, kMagic)) & 15u) << (4 * j);
-        w[k] = x;
-    }
-    slot += (long long)h << a.p.page_log2;
-    store_words(a.p.codes[i] + slot * (D / 2) + t * (N / 2), w);
-    if (t == 0) a.p.tok[i][slot] = sigma;
 }
 
 struct ReadArgs {
@@ -223,76 +361,119 @@ struct ReadArgs {
     long long row_stride[2], head_stride[2];  // elements
     const int8_t* signs;
     int rows;
+    int per;   // heads a quad takes
     int only;  // 0 or 1: that tensor alone; -1: both (blockIdx.y)
     float rsqd;
 };
 
-// Stores N consecutive values of type T at a 16-byte aligned place.
-template <typename T, int N>
-__device__ __forceinline__ void store_values(T* dst, const float (&v)[N]) {
+// Eight values at a 16-byte aligned place.
+template <typename T>
+__device__ __forceinline__ void store8(T* dst, const float (&v)[8]) {
     if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int k = 0; k < N / 4; ++k)
-            reinterpret_cast<float4*>(dst)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
     } else {
-#pragma unroll
-        for (int k = 0; k < N / 8; ++k)
-            reinterpret_cast<uint4*>(dst)[k] =
-                make_uint4(Elem<T>::pack(v[8 * k], v[8 * k + 1]), Elem<T>::pack(v[8 * k + 2], v[8 * k + 3]),
-                           Elem<T>::pack(v[8 * k + 4], v[8 * k + 5]), Elem<T>::pack(v[8 * k + 6], v[8 * k + 7]));
+        *reinterpret_cast<uint4*>(dst) = make_uint4(Elem<T>::pack(v[0], v[1]), Elem<T>::pack(v[2], v[3]),
+                                                    Elem<T>::pack(v[4], v[5]), Elem<T>::pack(v[6], v[7]));
     }
 }
 
 template <int D, typename T, bool HAD>
 __global__ void __launch_bounds__(kWriteThreads) pages_read_kernel(ReadArgs a) {
-    constexpr int N = D / 4;
+    constexpr int KC = D / 32, NP = 4 * KC;
     __shared__ int s_start[kStartStage];
-    const int i = a.only >= 0 ? a.only : blockIdx.y, t = threadIdx.x & 3;
+    __shared__ alignas(16) uint32_t s_sign[D / 2];  // sign bits of the signs of channels e and e + 4 of a piece
+    const int i = a.only >= 0 ? a.only : blockIdx.y, t = threadIdx.x & 3, H = a.p.H;
+    grid_dep_wait();
+    grid_dep_launch();
     const int* start = stage_start(a.b, s_start);
+    if (HAD && threadIdx.x < D / 2) {
+        const int c = (threadIdx.x >> 2) * 8 + (threadIdx.x & 3);
+        s_sign[threadIdx.x] = a.signs == nullptr
+                                  ? 0u : (a.signs[c] < 0 ? 0x8000u : 0u) | (a.signs[c + 4] < 0 ? 0x80000000u : 0u);
+    }
     __syncthreads();
-    const int vec = (int)((blockIdx.x * (unsigned)kWriteThreads + threadIdx.x) >> 2);
-    const int row = vec / a.p.H, h = vec - row * a.p.H;
+    const int groups = (H + a.per - 1) / a.per;
+    const int quad = (int)((blockIdx.x * (unsigned)kWriteThreads + threadIdx.x) >> 2);
+    const int row = quad / groups, h0 = (quad - row * groups) * a.per, h1 = min(h0 + a.per, H);
     if (row >= a.rows) return;
-    const int s = owner_of(start, a.b.n_seqs, row);
-    if (s < 0) return;
-    const int pos = a.b.len[s] - (start[s + 1] - start[s]) + (row - start[s]);
-    const long long slot = pos >= 0 ? slot_of(a.b, a.p, s, pos) : -1;
-    float v[N];
-    if (slot >= 0) {
-        const long long at = slot + ((long long)h << a.p.page_log2);
-        uint32_t w[N / 8];
-        load_words(a.p.codes[i] + at * (D / 2) + t * (N / 2), w);
-        const float sf = __half2float(a.p.tok[i][at]);
+    int seq;
+    const long long slot0 = slot_of_row(a.b, a.p, start, row, &seq);
+    if (seq < 0) return;
+    T* dst = static_cast<T*>(a.out[i]) + row * a.row_stride[i] + t * 8;
+    if (slot0 < 0) {
+        const float zero[8] = {};
+        for (int h = h0; h < h1; ++h)
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = (float)((int)((w[k >> 3] >> (4 * (k & 7))) & 15u) - 8);
+            for (int k = 0; k < KC; ++k) store8<T>(dst + h * a.head_stride[i] + 32 * k, zero);
+        return;
+    }
+    const uint32_t lanes = 0xFu << (threadIdx.x & 28);
+    uint32_t next[KC];
+    __half next_sigma;
+    const auto load = [&](int h) {
+        const long long at = slot0 + ((long long)h << a.p.page_log2);
+#pragma unroll
+        for (int k = 0; k < KC; ++k)
+            next[k] = reinterpret_cast<const uint32_t*>(a.p.codes[i] + at * (D / 2))[4 * k + t];
+        next_sigma = a.p.tok[i][at];
+    };
+    load(h0);
+#pragma unroll 1
+    for (int h = h0; h < h1; ++h) {
+        uint32_t p[NP];  // channels e and e + 4 of piece k at 4 k + e
+#pragma unroll
+        for (int k = 0; k < KC; ++k) {
+            const uint32_t w = next[k], w8 = w >> 8;
+            p[4 * k] = codes_low(w);
+            p[4 * k + 1] = codes_upper(w);
+            p[4 * k + 2] = codes_low(w8);
+            p[4 * k + 3] = codes_upper(w8);
+        }
+        const float sf = __half2float(next_sigma);
+        if (h + 1 < h1) load(h + 1);
+        float f = sf;
         if constexpr (HAD) {
-            const uint32_t quad = 0xFu << (threadIdx.x & 28);
-            lane_stages<1, N>(v);  // sums of at most 128 codes: exact
+            f = __fmul_rn(sf, a.rsqd);
+            const auto stage = [&](int x) {
+#pragma unroll
+                for (int k = 0; k < NP; ++k)
+                    if (!(k & x)) {
+                        const uint32_t lo = p[k], hi = p[k + x];
+                        p[k] = add_h2(lo, hi);
+                        p[k + x] = sub_h2(lo, hi);
+                    }
+            };
+            stage(1);
+            stage(2);
+#pragma unroll
+            for (int k = 0; k < NP; ++k)  // (x, y) to (x + y, x - y)
+                p[k] = fma_h2(p[k], 0xBC003C00u, __byte_perm(p[k], p[k], 0x1032));
 #pragma unroll
             for (int x = 1; x <= 2; x <<= 1) {
-                const float sg = (t & x) ? -1.0f : 1.0f;
+                const uint32_t sg = (t & x) ? 0xBC00BC00u : 0x3C003C00u;
 #pragma unroll
-                for (int k = 0; k < N; ++k) v[k] = __fmaf_rn(v[k], sg, __shfl_xor_sync(quad, v[k], x));
+                for (int k = 0; k < NP; ++k) p[k] = fma_h2(p[k], sg, __shfl_xor_sync(lanes, p[k], x));
             }
-            const float f = __fmul_rn(sf, a.rsqd);
-            if (a.signs != nullptr) {
+            stage(4);
+            if constexpr (KC == 4) stage(8);
 #pragma unroll
-                for (int k = 0; k < N / 4; ++k) {
-                    const char4 c = reinterpret_cast<const char4*>(a.signs + t * N)[k];
-                    v[4 * k] *= c.x, v[4 * k + 1] *= c.y, v[4 * k + 2] *= c.z, v[4 * k + 3] *= c.w;
-                }
+            for (int k = 0; k < KC; ++k) {
+                const uint4 sg = *reinterpret_cast<const uint4*>(&s_sign[(4 * k + t) * 4]);
+                p[4 * k] ^= sg.x, p[4 * k + 1] ^= sg.y, p[4 * k + 2] ^= sg.z, p[4 * k + 3] ^= sg.w;
             }
-#pragma unroll
-            for (int k = 0; k < N; ++k) v[k] *= f;
-        } else {
-#pragma unroll
-            for (int k = 0; k < N; ++k) v[k] *= sf;
         }
-    } else {
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = 0.0f;
+        for (int k = 0; k < KC; ++k) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&p[4 * k + e]));
+                v[e] = x.x * f, v[e + 4] = x.y * f;
+            }
+            store8<T>(dst + h * a.head_stride[i] + 32 * k, v);
+        }
     }
-    store_values(static_cast<T*>(a.out[i]) + row * a.row_stride[i] + h * a.head_stride[i] + t * N, v);
 }
 
 }  // namespace kvq

@@ -184,33 +184,9 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ uint32_t add2(uint32_t x, uint32_t y) {
-    uint32_t r;
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
-    return r;
-}
-template <uint32_t MASK, uint32_t BASE>
-__device__ __forceinline__ uint32_t in_mantissa(uint32_t w) {  // (w & MASK) | BASE: one lop3
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "r"(BASE));
-    return r;
-}
-// The codes of nibbles 0 and 4 of a word as two fp16: q, exactly.
-__device__ __forceinline__ uint32_t codes_low(uint32_t w) {  // (1024 + e) - 1032
-    return add2(in_mantissa<0x000F000Fu, 0x64006400u>(w), 0xE408E408u);
-}
-// Those of nibbles 1 and 5: 64 + e = q + kHigh, without arithmetic.
+// The codes of nibbles 1 and 5 as 64 + e = q + kHigh, without arithmetic.
 constexpr float kHigh = 72.0f;
 __device__ __forceinline__ uint32_t codes_high(uint32_t w) { return in_mantissa<0x00F000F0u, 0x54005400u>(w); }
-
-// Those as q, exactly: (1024 + 16 e) / 16 - 72.
-__device__ __forceinline__ uint32_t codes_upper(uint32_t w) {
-    uint32_t r;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;"
-        : "=r"(r)
-        : "r"(in_mantissa<0x00F000F0u, 0x64006400u>(w)), "r"(0x2C002C00u), "r"(0xD480D480u));
-    return r;
-}
 
 // 16 bytes to shared memory: `n` (16 or 0) of them from src, zeros for the rest.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n) {

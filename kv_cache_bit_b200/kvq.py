@@ -260,16 +260,24 @@ def _rows(x, call: str):
     return kvq_rows(x.data_ptr() or 16, stride[0], stride[1], kind, 0)
 
 
+_torch = None  # torch and its raw accessors, once a paged call needs them
+
+
 def _on(pages: "PagedCache", stream, call: str, fn, *args):
     """fn(*args, stream) with the cache's device current; stream None: the
     current stream of that device."""
-    import torch
+    global _torch
+    if _torch is None:
+        import torch
+        torch.cuda.init()
+        _torch = (torch, torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+    torch, raw_stream, current = _torch
     index = pages.device.index
     if stream is None:
-        stream = torch.cuda.current_stream(index).cuda_stream
+        stream = raw_stream(index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == index:
+    if current() == index:
         status = fn(*args, stream)
     else:
         with torch.cuda.device(index):
