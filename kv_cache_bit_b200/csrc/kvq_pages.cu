@@ -105,7 +105,7 @@ float rsqd_of(int d) { return (float)(1.0 / std::sqrt((double)d)); }
 // (a generation step), eight at most.
 int heads_a_quad(int64_t rows, int H) {
     int per = 1;
-    while (per < 8 && per * 2 <= H && rows * H >= (int64_t)per * 2 * 148 * 512) per *= 2;
+    while (per < 8 && per * 2 <= H && rows * H >= (int64_t)per * 2 * 148 * 128) per *= 2;
     return per;
 }
 

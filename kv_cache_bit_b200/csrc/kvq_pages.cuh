@@ -197,7 +197,7 @@ struct WriteArgs {
     float rsqd;
 };
 
-constexpr int kWriteThreads = 256;
+constexpr int kWriteThreads = 128;
 
 // blockIdx.y: K or V.
 template <int D, typename T, bool HAD>
@@ -239,6 +239,10 @@ __global__ void __launch_bounds__(kWriteThreads) pages_write_kernel(WriteArgs a)
             u[4 * k] = next[k].x, u[4 * k + 1] = next[k].y, u[4 * k + 2] = next[k].z, u[4 * k + 3] = next[k].w;
 #pragma unroll
             for (int j = 0; j < 4; ++j) big = max_u16x2(big, u[4 * k + j] & 0x7FFF7FFFu);
+            if constexpr (HAD) {  // signs, on the inputs' own bits
+                const uint4 sg = *reinterpret_cast<const uint4*>(&s_sign[(4 * k + t) * 4]);
+                u[4 * k] ^= sg.x, u[4 * k + 1] ^= sg.y, u[4 * k + 2] ^= sg.z, u[4 * k + 3] ^= sg.w;
+            }
         }
         if (h + 1 < h1) load(h + 1);
         float v[8 * KC];  // piece k's channels at 8 k
@@ -250,21 +254,6 @@ __global__ void __launch_bounds__(kWriteThreads) pages_write_kernel(WriteArgs a)
         if ((big & 0xFFFFu) >= Elem<T>::kSpecial || (big >> 16) >= Elem<T>::kSpecial) {
 #pragma unroll
             for (int k = 0; k < 8 * KC; ++k) v[k] = clean(v[k]);
-        }
-        if constexpr (HAD) {
-            if (a.signs != nullptr) {
-#pragma unroll
-                for (int k = 0; k < KC; ++k) {
-                    const uint4 sg = *reinterpret_cast<const uint4*>(&s_sign[(4 * k + t) * 4]);
-                    const uint32_t w[4] = {sg.x, sg.y, sg.z, sg.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float* x = &v[8 * k + 2 * j];
-                        x[0] = __uint_as_float(__float_as_uint(x[0]) ^ (w[j] << 16));
-                        x[1] = __uint_as_float(__float_as_uint(x[1]) ^ (w[j] & 0x80000000u));
-                    }
-                }
-            }
         }
         // pairs of pieces KC / 2 apart, so that all strides but the last are whole pairs'
         constexpr int NP = 4 * KC, KH = KC / 2;
