@@ -21,8 +21,11 @@ namespace {
 
 constexpr int64_t kMaxIndex = int64_t(1) << 31;
 constexpr int kMaxGroup = 256;  // query heads per kv head
-// Sequences of more query rows a kv head than this go to the tile kernel.
-constexpr int kMany = 32;
+// Sequences of more query rows a kv head than this go to the tile kernel.  The generation-step kernel reads the
+// cache once for 16 rows (28 query heads over 4 kv heads, 16 x 300 .. 3001 tokens, D = 128: 48 us at 35 rows, 62
+// at 63, 99 at 98; 32 over 8, D = 64: 44, 65 and 90), the tile kernel once for 256 (57, 58, 60; 78, 79, 78).
+constexpr int many_rows(int d) { return d == 128 ? 48 : 80; }
+constexpr int kManyMost = 80;
 
 struct NvtxRange {
     explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
@@ -201,21 +204,21 @@ int sm_count() {
 // Generation-step kernel: CTAs of a single wave, and query rows an item.
 template <int NQ>
 struct StepShape {
-    static constexpr int kWarps = NQ == 16 ? 4 : 8, kPerSm = NQ == 16 ? 3 : 2;
+    static constexpr int kWarps = NQ == 16 ? 8 : 4, kPerSm = NQ == 16 ? 1 : 3;
 };
 
 // Which kernels a call needs, from what the host knows of it.
 struct AttnPlan {
-    bool tiles;        // some sequence may have more than kMany query rows a kv head
+    bool tiles;        // some sequence may have more than many_rows() query rows a kv head
     int stretch;       // with tiles: rows of a sequence that has not
     long long places;  // rows that the step kernel's queries are prepared for
     long long queries; // query rows a kv head of the sequences that are the step kernel's
 };
-AttnPlan attn_plan(const kvq_batch* b, long long rows, int G) {
+AttnPlan attn_plan(const kvq_batch* b, long long rows, int G, int d) {
     AttnPlan p;
     const long long most = (long long)G * b->max_rows;
-    p.tiles = b->max_rows == 0 || most > kMany;
-    p.stretch = p.tiles ? kMany / G : 0;
+    p.tiles = b->max_rows == 0 || most > many_rows(d);
+    p.stretch = p.tiles ? many_rows(d) / G : 0;
     p.places = p.tiles ? (long long)b->n_seqs * p.stretch : rows;
     p.queries = p.tiles ? G : most;
     return p;
@@ -269,7 +272,7 @@ kvq_status launch_step(const StepArgs& g, int sms, cudaStream_t st) {
     const int grid = sms * Sh::kPerSm;
     const kvq_status s = launch(kernel, dim3(grid), Sh::kWarps * 32, smem, st, g);
     if (s != KVQ_OK) return s;
-    return launch(pages_merge_kernel<D, NQ, HAD>, dim3(grid), kMergeWarps * 32, 0, st, g.a);
+    return launch(pages_merge_kernel<D, NQ, HAD>, dim3(grid, NQ / merge_queries(NQ)), kMergeWarps * 32, 0, st, g.a);
 }
 
 template <int D, bool HAD>
@@ -287,7 +290,7 @@ kvq_status launch_tiles(const TileArgs& t, int sms, cudaStream_t st) {
     if (!fits) return KVQ_ERR_CUDA;
     const kvq_status s = launch(kernel, dim3(sms), kTileThreads, smem, st, t);
     if (s != KVQ_OK) return s;
-    return launch(pages_merge_kernel<D, kItemRows, HAD>, dim3(sms, kItemRows / kMergeWarps), kMergeWarps * 32, 0,
+    return launch(pages_merge_kernel<D, kItemRows, HAD>, dim3(sms, kItemRows / merge_queries(kItemRows)), kMergeWarps * 32, 0,
                   st, t.a);
 }
 
@@ -309,7 +312,7 @@ kvq_status check_attention(const kvq_config* cfg, const kvq_pages* p, const kvq_
     if (s != KVQ_OK) return s;
     if (q_heads < p->kv_heads || q_heads % p->kv_heads != 0) return KVQ_ERR_INVALID_ARG;
     if (q_heads / p->kv_heads > kMaxGroup || q_heads > 65535 || rows >= kMaxIndex / q_heads ||
-        b->n_seqs >= kMaxIndex / (kMany * (int64_t)q_heads))  // prepared queries are counted in 32 bits
+        b->n_seqs >= kMaxIndex / (kManyMost * (int64_t)q_heads))  // prepared queries are counted in 32 bits
         return KVQ_ERR_UNSUPPORTED;
     return KVQ_OK;
 }
@@ -388,7 +391,7 @@ kvq_status kvq_pages_read(const kvq_config* cfg, const kvq_pages* pages, const k
 size_t kvq_pages_attention_workspace_bytes(const kvq_config* cfg, const kvq_pages* pages, const kvq_batch* batch,
                                            int64_t rows, int32_t q_heads) {
     if (check_attention(cfg, pages, batch, rows, q_heads) != KVQ_OK) return 0;
-    const AttnPlan p = attn_plan(batch, rows, q_heads / pages->kv_heads);
+    const AttnPlan p = attn_plan(batch, rows, q_heads / pages->kv_heads, cfg->head_dim);
     return attn_workspace(p, sm_count(), cfg->head_dim, cfg->flags == KVQ_HADAMARD, q_heads, batch->n_seqs).bytes;
 }
 
@@ -414,7 +417,7 @@ kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, co
     if (!ok_ptr(ws) || ws_bytes < need) return KVQ_ERR_WORKSPACE;
     const int sms = sm_count();
     const bool had = cfg->flags == KVQ_HADAMARD;
-    const AttnPlan p = attn_plan(batch, rows, q_heads / pages->kv_heads);
+    const AttnPlan p = attn_plan(batch, rows, q_heads / pages->kv_heads, cfg->head_dim);
     const AttnWorkspace w = attn_workspace(p, sms, d, had, q_heads, batch->n_seqs);
     uint8_t* base = static_cast<uint8_t*>(ws);
     StepArgs g;
@@ -441,7 +444,7 @@ kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, co
     a.ml = reinterpret_cast<float*>(base + w.ml);
     a.part = reinterpret_cast<float*>(base + w.part);
     a.left = reinterpret_cast<float*>(base + w.left);
-    g.many = p.tiles ? kMany : 0;
+    g.many = p.tiles ? many_rows(d) : 0;
     g.stretch = p.stretch;
     g.frag = reinterpret_cast<__half*>(base + w.frag);
     g.scal = reinterpret_cast<float4*>(base + w.scal);
@@ -450,7 +453,7 @@ kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, co
     t.a.meta = reinterpret_cast<int4*>(base + w.tile_meta);
     t.a.ml = reinterpret_cast<float*>(base + w.tile_ml);
     t.a.part = reinterpret_cast<float*>(base + w.tile_part);
-    t.many = kMany;
+    t.many = many_rows(d);
     t.plan = reinterpret_cast<int4*>(base + w.plan);
     t.seq_cost = reinterpret_cast<long long*>(base + w.seq_cost);
     cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -125,9 +125,12 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, int row, int head,
 // 2b of one that it did not begin.  Warps beyond one a query share its states; the order of the sums is fixed.
 constexpr int kMergeWarps = 16;
 
+// Queries a block (blockIdx.y): items of many rows are merged of few states, those of few rows of up to one a CTA.
+constexpr int merge_queries(int nq) { return nq > 16 ? 16 : 4; }
+
 template <int D, int NQ, bool HAD>
 __global__ void __launch_bounds__(kMergeWarps * 32) pages_merge_kernel(AttnArgs a) {
-    constexpr int NB = NQ < kMergeWarps ? NQ : kMergeWarps, W = kMergeWarps / NB;  // queries a block, warps a query
+    constexpr int NB = merge_queries(NQ), W = kMergeWarps / NB;
     __shared__ float s_o[NB][W][D], s_l[NB][W];
     const int b = blockIdx.x, qb = (threadIdx.x >> 5) / W, part = (threadIdx.x >> 5) % W, lane = threadIdx.x & 31;
     const int qi = blockIdx.y * NB + qb;
