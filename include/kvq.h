@@ -339,7 +339,8 @@ typedef struct {
  * A generation step has one row a sequence, a prompt or a part of one many;
  * both may be in one batch, and a sequence may have no rows.
  * max_rows (host): the most rows one sequence has; 0 = not known.  It only
- * chooses between kernels: too small a value costs time, never results.
+ * chooses between kernels: too small a value costs time, never results (and a
+ * value that is known saves the launches for prompts in a generation step).
  * Page numbers outside [0, n_pages) and tokens past max_pages pages are never
  * followed: the token is left out, and bit 2 of the word that
  * kvq_pages_read_errors reads is set.
@@ -392,10 +393,10 @@ kvq_status kvq_pages_write(const kvq_config* cfg, const kvq_pages* pages, const 
 kvq_status kvq_pages_read(const kvq_config* cfg, const kvq_pages* pages, const kvq_batch* batch,
                           const kvq_rows* k_out, const kvq_rows* v_out, int64_t rows, void* stream);
 
-/* Workspace bytes of kvq_pages_attention for batches of at most this n_seqs,
-   `rows` and max_rows (partial softmax states of the sequence splits; it depends on the
-   current device's SM count); 0 on invalid arguments.  Contents need no
-   initialization; calls that share a workspace must not overlap in time. */
+/* Workspace bytes of kvq_pages_attention for this batch's n_seqs, `rows` and
+   max_rows (prepared queries and the partial softmax states of the ranges; it
+   depends on the current device's SM count); 0 on invalid arguments.  Contents
+   need no initialization; calls that share a workspace must not overlap in time. */
 size_t kvq_pages_attention_workspace_bytes(const kvq_config* cfg, const kvq_pages* pages, const kvq_batch* batch,
                                            int64_t rows, int32_t q_heads);
 
@@ -414,9 +415,13 @@ size_t kvq_pages_attention_workspace_bytes(const kvq_config* cfg, const kvq_page
  * A row that sees no token (padding inside a sequence, an empty sequence)
  * gives zeros and lse -inf; rows of no sequence are left as they were.
  * Scores, softmax statistics and sums are fp32; the rotated query is kept to
- * 22 bits and a token's probability times its value scale is rounded to fp16.
+ * 22 bits.  Sequences with few rows (48 query rows a kv head at head_dim 128,
+ * 80 at 64) round a token's probability times its value scale to fp16, others
+ * the probability and sigma q each (so values below 2^-14 are kept to 2^-25).
+ * A row's result depends on its own sequence only.  Runs of one call give the
+ * same bits; other batches, hints or devices may sum in another order.
  * Errors: INVALID_ARG; WORKSPACE; UNSUPPORTED (as kvq_pages_write; rows *
- * q_heads >= 2^31; q_heads / kv_heads > 256); CUDA.
+ * q_heads >= 2^31; n_seqs * q_heads >= 2^31 / 80; q_heads / kv_heads > 256); CUDA.
  */
 kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, const kvq_batch* batch,
                                const kvq_rows* q, int32_t q_heads, int64_t rows, float scale, int32_t causal,
@@ -425,9 +430,10 @@ kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, co
 
 /*
  * Read (and, if clear != 0, reset) the sticky error word of the paged calls on
- * the current device: bits 0 and 1 as in kvq_read_device_errors (which covers
- * the other calls), bit 2 = a page number or token outside its range was left
- * out.  HOST call; synchronizes the device.
+ * the current device: bit 1 = a kernel gave up waiting on a barrier (results
+ * since the last read are void; kvq_read_device_errors covers the other
+ * calls), bit 2 = a page number or token outside its range was left out.  HOST
+ * call; synchronizes the device.
  * Errors: INVALID_ARG (host_out NULL); CUDA.
  */
 kvq_status kvq_pages_read_errors(uint32_t* host_out, int32_t clear);

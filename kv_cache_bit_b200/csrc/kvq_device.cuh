@@ -54,10 +54,10 @@ __device__ __forceinline__ float dq_s1(const uint8_t* rec, int t) {
 template <int D, int MODE>
 __host__ __device__ constexpr int off_words() { return MODE == kNsnDq ? dq_record_bytes<D>() / 2 : D; }
 
-// Sticky device error word, readable with kvq_read_device_errors().
+// Sticky device error word, readable with kvq_read_device_errors() (kvq_pages_read_errors()).
 constexpr uint32_t kErrTmaTimeout = 1u;
 constexpr uint32_t kErrBarrierTimeout = 2u;
-__device__ uint32_t g_error_word = 0;  // the library is a single translation unit
+__device__ uint32_t g_error_word = 0;  // one a translation unit: block cache, paged cache
 
 // Poll limit of the bounded waits in the kernels' main loops.  A separate
 // test build of the library (KVQ_WAIT_TEST, never the product build) scales

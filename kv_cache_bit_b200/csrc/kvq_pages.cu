@@ -471,4 +471,11 @@ kvq_status kvq_pages_read_errors(uint32_t* host_out, int32_t clear) {
     return KVQ_OK;
 }
 
+#ifdef KVQ_WAIT_TEST
+// Test build only: scale of the poll limits of the paged kernels' waits (0: give up at once).
+int kvq_test_set_pages_wait_scale(uint32_t scale) {
+    return cudaMemcpyToSymbol(g_wait_scale, &scale, sizeof(scale)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+#endif
+
 }  // extern "C"

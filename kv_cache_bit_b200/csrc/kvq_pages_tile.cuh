@@ -698,7 +698,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                 if (lane == 0) mbar_arrive(&sm.par_empty[stage]);
                 const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a.scale2;
                 if (__any_sync(~0u, top > M + kSlack)) {
-                    const float m2 = fmaxf(M, top), f = ex2(M - m2);
+                    const float m2 = top > M + kSlack ? top : M, f = ex2(M - m2);  // (other rows as they were)
                     const uint64_t ff = pair2(f, f);
                     M = m2;
                     l2[0] = mul_f2(l2[0], ff);

@@ -92,21 +92,27 @@ def gather(codes, tok, b: Seqs, s: int, n: int):
     return q, sc, there
 
 
-def attention(k, v, b: Seqs, q: np.ndarray, signs, scale, causal, window, half_step, only=None):
+def attention(k, v, b: Seqs, q: np.ndarray, signs, scale, causal, window, half_step, only=None,
+              many=False):
     """Attention in 64 bits over k, v = (codes, tok), and the bounds of the
     kernels' errors: {row: (out [Hq, d], lse [Hq], out bound, lse bound)}, of
     all rows or of those in `only`.
 
     Roundings of the kernels, each relative to what it rounds:
-      scores  the query keeps 22 bits, the products with codes e = q + 8 <= 15
-              are summed in the tensor core within 2^-19 of the sum of their
-              magnitudes, or in fp32 (128 terms: 2^-17 at worst); the scaling
-              and exp2's argument add three fp32 roundings of the score.
+      scores  the query keeps 22 bits, the products with codes (of magnitude
+              15 at most, or up to 79 for half of them: 64 + e) are summed in
+              the tensor core within 2^-19 of the sum of their magnitudes, or
+              in fp32 (128 terms: 2^-17 at worst); the scaling and exp2's
+              argument add three fp32 roundings of the score.
               delta = 2^-17 sum |q~| 15 sigma scale + 4 2^-24 |score|
       p       exp(score - reference): e^(2 delta) - 1 against the others, the
-              exponential itself 2^-21; p sigma_v is rounded to fp16, 2^-11
+              exponential itself 2^-21; p sigma_v is rounded to fp16, 2^-12,
+              or p and sigma_v q are, 2^-11 together
       values  sum of p sigma_v e, |e| <= 15, again 2^-17 of its magnitudes
       result  half a step of its type
+    With `many` (sequences of many rows, where p and sigma_v q are rounded
+    apart) a value is also off by half of fp16's smallest step, 2^-25, and a
+    token's p by as much of 2^7 or more for the largest: 2^-32 each.
     The rotation back is orthogonal: each element's error is at most the
     2-norm of the errors before it."""
     H, d, Hq = k[0].shape[1], q.shape[2], q.shape[1]
@@ -142,6 +148,8 @@ def attention(k, v, b: Seqs, q: np.ndarray, signs, scale, causal, window, half_s
                 rel = 2 * delta + 2.0 ** -20 + 2.0 ** -11
                 err = rel * ((p * vs[g, sees]) @ np.abs(vq[g, sees])) / l \
                     + 2.0 ** -17 * 15 * float((p * vs[g, sees]).sum()) / l
+                if many:
+                    err = err + 2.0 ** -25 + 2.0 ** -32 * (np.abs(vq[g, sees]) * vs[g, sees, None]).sum(0) / l
                 out[j] = o @ R if signs is not None else o
                 e2 = np.linalg.norm(err) if signs is not None else err
                 tol[j] = e2 + half_step * (np.abs(out[j]) + e2) + 2.0 ** -25

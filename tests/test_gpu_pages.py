@@ -86,9 +86,9 @@ class Setup:
         torch.cuda.synchronize()
         return out, l
 
-    def check(self, q, out, lse, dtype, scale=0.0, causal=True, window=0, only=None):
+    def check(self, q, out, lse, dtype, scale=0.0, causal=True, window=0, only=None, many=False):
         want = ref.attention((self.codes[0], self.tok[0]), (self.codes[1], self.tok[1]), self.b, host(q), self.signs,
-                             scale, causal, window, HALF[dtype], only)
+                             scale, causal, window, HALF[dtype], only, many)
         out, l = host(out), None if lse is None else lse.cpu().numpy()
         assert np.isfinite(out).all()
         for r in range(q.shape[0]) if only is None else sorted(only):
@@ -285,11 +285,12 @@ def test_attention_with_a_wrong_row_hint_and_without_lse():
         s.check(q, out, None, "fp16")
 
 
-def test_attention_of_loud_and_silent_values():
+@pytest.mark.parametrize("rows", [3, 50])
+def test_attention_of_loud_and_silent_values(rows):
     """Scales over fp16's whole range: tokens of huge and tiny values in one
     sequence, zero rows, queries that single out one token or none."""
     d, H, G = 128, 1, 4
-    s = Setup([(300, 3)], d=d, H=H, page=16, rotated=False, fill=False)
+    s = Setup([(300, rows)], d=d, H=H, page=16, rotated=False, fill=False)
     r = s.rng
     mags = np.exp(r.uniform(np.log(1e-6), np.log(3e4), (300, 1, 1))).astype(np.float32)
     x = [(r.standard_normal((300, H, d)) * (1 if i == 0 else mags)).astype(np.float32) for i in range(2)]
@@ -307,13 +308,14 @@ def test_attention_of_loud_and_silent_values():
     for scale in (0.0, 1e-4, 4.0):
         q = s.tensor(G, "bf16", scale=2.0)
         q[0] = 0
-        s.check(q, *s.attend(q, scale=scale), "bf16", scale=scale)
+        s.check(q, *s.attend(q, scale=scale), "bf16", scale=scale, many=rows == 50)
 
 
+@pytest.mark.parametrize("rows", [6, 40])
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("rotated", [False, True])
-def test_attention_of_extreme_queries(dtype, rotated):
-    s = Setup([(100, 6)], rotated=rotated)
+def test_attention_of_extreme_queries(dtype, rotated, rows):
+    s = Setup([(100, rows)], rotated=rotated)
     q = s.tensor(4, dtype)
     q[0] *= 1e-6
     q[1] *= 2e3
@@ -324,8 +326,9 @@ def test_attention_of_extreme_queries(dtype, rotated):
     s.check(q, *s.attend(q, scale=0.003), dtype, scale=0.003)
 
 
-def test_a_query_that_is_not_a_number_stays_in_its_row():
-    s = Setup([(100, 4), (50, 1)])
+@pytest.mark.parametrize("rows", [4, 90])
+def test_a_query_that_is_not_a_number_stays_in_its_row(rows):
+    s = Setup([(100, rows), (50, 1)])
     q = s.tensor(4, "fp16")
     q[1, 2, 5] = float("nan")
     q[2, 1, 7] = float("inf")
@@ -339,6 +342,18 @@ def test_a_query_that_is_not_a_number_stays_in_its_row():
     q2[~keep] = 0
     out2, lse2 = s.attend(q2)
     assert torch.equal(out[keep], out2[keep]) and torch.equal(lse[keep], lse2[keep])
+
+
+def test_a_row_does_not_depend_on_its_neighbours():
+    """The same bits for rows of a sequence whatever the other rows' queries are."""
+    import torch
+    s = Setup([(700, 300), (300, 40)], page=32)
+    q = s.tensor(4, "bf16")
+    q2 = s.tensor(4, "bf16", scale=30.0)
+    q2[::3] = q[::3]
+    (a, la), (b, lb) = s.attend(q), s.attend(q2)
+    assert torch.equal(a[::3], b[::3]) and torch.equal(la[::3], lb[::3])
+    s.check(q2, b, lb, "bf16", only=set(range(0, s.rows, 17)))
 
 
 # ------------------------------------------------------------------ bad pages
@@ -450,7 +465,7 @@ def test_other_streams_and_two_calls_at_once():
     """Two calls on two streams with workspaces of their own, and the same
     results as one after the other."""
     import torch
-    s = Setup([(900, 1), (400, 20), (1300, 1)], page=64)
+    s = Setup([(900, 1), (400, 20), (1300, 1), (600, 150)], page=64)
     q = [s.tensor(8, "fp16"), s.tensor(8, "fp16")]
     want = [s.attend(x) for x in q]
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
@@ -466,11 +481,12 @@ def test_other_streams_and_two_calls_at_once():
         assert torch.equal(o, wo) and torch.equal(l, wl)
 
 
-def test_captured_steps_follow_the_batch_contents():
+@pytest.mark.parametrize("hint", [0, 1])
+def test_captured_steps_follow_the_batch_contents(hint):
     """write + attention + read in a graph, replayed while lengths, rows and
     tables change in place; a second graph shares the workspace (in order)."""
     import torch
-    s = Setup([(60, 1), (200, 1), (31, 1)], page=16, H=2, spare=12)
+    s = Setup([(60, 1), (200, 1), (31, 1)], page=16, H=2, spare=12, max_rows=hint)
     kvq = s.kvq
     used = {int(p) for q_, n in enumerate((60, 200, 31)) for p in s.b.table[q_, :-(-n // 16)]}
     s.b.table[2, 2] = next(p for p in range(s.n_pages) if p not in used)  # where sequence 2 grows to
