@@ -262,16 +262,24 @@ AttnWorkspace attn_workspace(const AttnPlan& p, int sms, int d, bool had, int q_
     return w;
 }
 
+// Caches of up to this many tokens (by the table's width) are taken whole where there is a CTA for every item.
+// In ranges with a merge, and whole, us: 1 sequence of 256 tokens, 8 heads, D = 64: 9.9 and 7.9; 4 of 256, 32
+// over 8 heads, D = 128: 11.6 and 9.2; 8 of 100 .. 512: 12.4 and 11.2; 1 of 512, 28 over 4 heads: 12.6 and 13.0.
+constexpr long long kWholeTokens = 512;
+
 template <int D, int NQ, bool HAD>
-kvq_status launch_step(const StepArgs& g, int sms, cudaStream_t st) {
+kvq_status launch_step(StepArgs g, long long tokens, int sms, cudaStream_t st) {
     using Sh = StepShape<NQ>;
     constexpr int smem = (int)sizeof(StepSmem<D, NQ, HAD, Sh::kWarps>);
     static_assert(smem * Sh::kPerSm + Sh::kPerSm * 1024 <= 228 * 1024, "shared memory of the CTAs on one SM");
     constexpr auto kernel = pages_step_kernel<D, NQ, HAD, Sh::kWarps, Sh::kPerSm>;
     if (!allow_smem<kernel>(smem)) return KVQ_ERR_CUDA;
     const int grid = sms * Sh::kPerSm;
-    const kvq_status s = launch(kernel, dim3(grid), Sh::kWarps * 32, smem, st, g);
-    if (s != KVQ_OK) return s;
+    // at most: whatever the rows are, a sequence has one chunk that is not full
+    const long long items = (long long)g.a.p.H * (g.a.rows * (long long)g.a.G / NQ + g.a.b.n_seqs);
+    g.whole = tokens <= kWholeTokens && items <= grid;
+    const kvq_status s = launch(kernel, dim3(g.whole ? (int)items : grid), Sh::kWarps * 32, smem, st, g);
+    if (s != KVQ_OK || g.whole) return s;
     return launch(pages_merge_kernel<D, NQ, HAD>, dim3(grid, NQ / merge_queries(NQ)), kMergeWarps * 32, 0, st, g.a);
 }
 
@@ -299,9 +307,10 @@ kvq_status launch_attn(const StepArgs& g, const TileArgs& t, const AttnPlan& p, 
     const unsigned ctas = (unsigned)((p.places * g.a.Hq + kQueryWarps - 1) / kQueryWarps) + (p.tiles ? 1 : 0);
     kvq_status s = launch(pages_queries_kernel<D, HAD>, dim3(ctas), kQueryWarps * 32, 0, st, g, t, p.tiles ? sms : 0);
     if (s == KVQ_OK && p.places > 0) {
-        if (HAD && p.queries <= 4) s = launch_step<D, HAD ? 4 : 8, HAD>(g, sms, st);
-        else if (p.queries <= 8) s = launch_step<D, 8, HAD>(g, sms, st);
-        else s = launch_step<D, 16, HAD>(g, sms, st);
+        const long long tokens = (long long)g.a.b.max_pages << g.a.p.page_log2;
+        if (HAD && p.queries <= 4) s = launch_step<D, HAD ? 4 : 8, HAD>(g, tokens, sms, st);
+        else if (p.queries <= 8) s = launch_step<D, 8, HAD>(g, tokens, sms, st);
+        else s = launch_step<D, 16, HAD>(g, tokens, sms, st);
     }
     if (s == KVQ_OK && p.tiles) s = launch_tiles<D, HAD>(t, sms, st);
     return s;
@@ -446,6 +455,7 @@ kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, co
     a.left = reinterpret_cast<float*>(base + w.left);
     g.many = p.tiles ? many_rows(d) : 0;
     g.stretch = p.stretch;
+    g.whole = 0;
     g.frag = reinterpret_cast<__half*>(base + w.frag);
     g.scal = reinterpret_cast<float4*>(base + w.scal);
     TileArgs t;

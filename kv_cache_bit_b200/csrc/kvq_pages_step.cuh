@@ -60,6 +60,9 @@ struct StepArgs {
     __half* frag;
     float4* scal;
     int stretch;
+    // Short caches and few items: a CTA takes one item whole, its warps equal parts of it, and nothing is left
+    // for pages_merge_kernel, which is not launched.
+    int whole;
 };
 
 // A sequence's share of the work.
@@ -89,6 +92,12 @@ __device__ __forceinline__ Item item_of(const StepArgs& g, int s, int H) {
     it.chunks = (it.nq + NQ - 1) / NQ;
     it.cost = (long long)(H * it.chunks) * (it.units + kStepCost);
     return it;
+}
+
+// What the ranges are cut from: positions, or items where CTAs take them whole.
+template <int NQ>
+__device__ __forceinline__ long long share_of(const StepArgs& g, const Item& it, int H) {
+    return g.whole && it.cost > 0 ? H * it.chunks : it.cost;
 }
 
 // x / y of non-negative numbers; 64-bit division only where 32 do not hold them.
@@ -249,7 +258,7 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
     // ---- the warps' ranges: prefix sums of the sequences' costs, a run of `per` sequences a thread
     const int per = (a.b.n_seqs + NW * 32 - 1) / (NW * 32), s0 = threadIdx.x * per;
     long long mine = 0;
-    for (int s = s0; s < min(s0 + per, a.b.n_seqs); ++s) mine += item_of<NQ>(g, s, H).cost;
+    for (int s = s0; s < min(s0 + per, a.b.n_seqs); ++s) mine += share_of<NQ>(g, item_of<NQ>(g, s, H), H);
     long long sum = mine;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
@@ -264,37 +273,50 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
         if (w < warp) before += sh.sums[w];
         total += sh.sums[w];
     }
-    const int workers = (int)min((long long)gridDim.x * NW, total);
-    if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+    const int me = blockIdx.x * NW + warp;
+    const int workers = g.whole ? (int)min((long long)gridDim.x, total) * NW : (int)min((long long)gridDim.x * NW, total);
+    if (!g.whole && threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
     if ((int)blockIdx.x * NW >= workers) {
         grid_dep_wait();  // this grid's end stands for that of the kernels before it
         return;
     }
-    const long long share = quotient(total, workers);  // the first `extra` warps have one unit more
-    const int extra = (int)(total - share * workers);
+    const long long share = g.whole ? 1 : quotient(total, workers);  // the first `extra` warps have one unit more
+    const int extra = g.whole ? 0 : (int)(total - share * workers);
     const auto begin_of = [&](int worker) { return share * worker + min(worker, extra); };
-    const int me = blockIdx.x * NW + warp;
     sh.before[threadIdx.x] = before;
     __syncthreads();
     {
         Walk<NQ> w;
         w.n = 0;
         if (me < workers) {
-            w.x = begin_of(me);
-            w.end = begin_of(me + 1);
-            int lo = 0, hi = NW * 32;  // the run that holds the range's first unit
+            const long long first = g.whole ? blockIdx.x : begin_of(me);
+            int lo = 0, hi = NW * 32;  // the run that holds the first position (or the item)
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (sh.before[mid] <= w.x) lo = mid;
+                if (sh.before[mid] <= first) lo = mid;
                 else hi = mid;
             }
-            long long off = w.x - sh.before[lo];
+            long long off = first - sh.before[lo];
             w.it = item_of<NQ>(g, lo * per, H);
-            while (off >= w.it.cost && w.it.s + 1 < a.b.n_seqs) {
-                off -= w.it.cost;
+            while (w.it.s + 1 < a.b.n_seqs) {
+                const long long of_seq = share_of<NQ>(g, w.it, H);
+                if (off < of_seq) break;
+                off -= of_seq;
                 w.it = item_of<NQ>(g, w.it.s + 1, H);
             }
-            w.place(g, H, off);
+            if (g.whole) {
+                const int part = (w.it.units + NW - 1) / NW;
+                w.h = (int)off / w.it.chunks;
+                w.c = (int)off - w.h * w.it.chunks;
+                w.pos = kStepCost + warp * part;
+                w.x = w.pos;
+                w.end = min(w.pos + part, kStepCost + w.it.units);
+                if (w.x < w.end) w.cut();
+            } else {
+                w.x = first;
+                w.end = begin_of(me + 1);
+                w.place(g, H, off);
+            }
         }
         if (lane == 0) wk = w;
         if (lane == 1) pw = w;
