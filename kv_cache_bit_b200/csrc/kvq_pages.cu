@@ -251,7 +251,7 @@ AttnWorkspace attn_workspace(const AttnPlan& p, int sms, int d, bool had, int q_
     w.part = take(2 * queries * d * 4);
     w.left = take(warps * d * 4);
     w.frag = take(size_t(p.places) * q_heads * d * (had ? 4 : 2));
-    w.scal = take(size_t(p.places) * q_heads * 16);
+    w.scal = take(size_t(p.places) * q_heads * 4);
     const size_t tiles = p.tiles ? size_t(sms) : 0;
     w.tile_meta = take(tiles * 16);
     w.tile_ml = take(2 * tiles * kItemRows * 8);
@@ -457,7 +457,7 @@ kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, co
     g.stretch = p.stretch;
     g.whole = 0;
     g.frag = reinterpret_cast<__half*>(base + w.frag);
-    g.scal = reinterpret_cast<float4*>(base + w.scal);
+    g.scal = reinterpret_cast<float*>(base + w.scal);
     TileArgs t;
     t.a = a;
     t.a.meta = reinterpret_cast<int4*>(base + w.tile_meta);

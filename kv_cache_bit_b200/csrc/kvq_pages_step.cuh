@@ -18,20 +18,21 @@
 // sequences, where a warp has one or two units.)
 //
 // Per 16 tokens, channels and tokens permuted so that unpacking is cheap:
-//   scores  A = K codes.  A nibble pair is ORed into fp16 mantissas: the lower
-//           nibble of a byte into 1024's, less 1032 (exact); the upper one into
-//           64's, which gives q + 72 without arithmetic, and the accumulator
-//           starts at -72 times the sum of those channels' queries.  (The bits
-//           taken as subnormals e 2^-24 would save the additions too, but the
-//           tensor core aligns products by their exponent fields and drops what
-//           falls below: errors of 7e-4 of the values.)
+//   scores  A = K codes, exact in fp16: a nibble pair ORed into the mantissas of
+//           1024 and less 1032 (or, from the upper nibbles, times 1 / 16 less
+//           72).
 //           B = the query, times a power of two for its row so that its
 //           largest element is near 2^15.  A rotated query is split into fp16
 //           high and low parts in neighbouring columns (22 bits of it are
 //           kept); an input that is not rotated fits fp16 exactly.
-//   values  A = V codes transposed (byte permutes pair two tokens' words),
-//           B = w from the score fragments by movmatrix.  One more product,
-//           with ones, gives the sum of w that takes the 72 out.
+//   values  A = V codes transposed (byte permutes pair two tokens' words), the
+//           upper nibbles ORed into the mantissa of 64, which gives q + 72
+//           without arithmetic; B = w from the score fragments by movmatrix.
+//           One more product, with ones, gives the sum of w that takes the 72
+//           out.  (For K the same cost 1e-6 of the logarithm of the sum.  The
+//           bits taken as subnormals e 2^-24 need no arithmetic at all, but
+//           the tensor core aligns products by their exponent fields and drops
+//           what falls below: errors of 7e-4 of the values.)
 // Instructions a 16-token tile (4 rotated queries, D = 128): about 210 against
 // 332 of the block cache's kernel, whose channel scales need arithmetic per
 // code; 88 of them on the ALU pipe (2 cycles each): 44 SM cycles, of about 90
@@ -54,11 +55,10 @@ constexpr int slot_bytes() { return kUnit * (D + 4); }  // K codes, V codes, K s
 struct StepArgs {
     AttnArgs a;
     int many;  // sequences of more query rows a kv head than this are not this kernel's (0: all are)
-    // Prepared queries: fragments [place][head][part][D] and per query the factor of its scores and what
-    // the parts' accumulators start from.  A row's place is its number, or, with `many`, its number in its
+    // Prepared queries: fragments [place][head][part][D] and per query the factor of its scores.  A row's place is its number, or, with `many`, its number in its
     // sequence behind a stretch of `stretch` places a sequence.
     __half* frag;
-    float4* scal;
+    float* scal;
     int stretch;
     // Short caches and few items: a CTA takes one item whole, its warps equal parts of it, and nothing is left
     // for pages_merge_kernel, which is not launched.
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
         const bool begins = wk.u == 0, ends = wk.u + wk.n == wk.it.units;
         const int units = wk.n, unit0 = wk.it.u0 + wk.u, seen0 = wk.it.t0, seen1 = wk.it.t1;
         const bool final = wk.x + wk.span >= wk.end;  // the range's last segment
-        float M[NV], l[NV], cq[NV], c_init[QT][2];
+        float M[NV], l[NV], cq[NV];
         float o[NP][NJ][4], sums[NP][4];  // sums: of w
         const int i0 = wk.c * NQ, lo = wk.it.lo, nq = wk.it.nq;
         // index of query i of the item among the prepared ones
@@ -410,17 +410,14 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
             M[v] = kLowest;
             l[v] = 0.0f;
             const int i = i0 + query_of<HAD>(v, t);
-            float4 sc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            cq[v] = 0.0f;
             if (i < nq) {
                 const int r = i / a.G;
-                sc = g.scal[prepared(i, r)];
+                cq[v] = g.scal[prepared(i, r)];
                 const Range see = row_range(a, wk.it, r);
                 lo_max = max(lo_max, see.t0);
                 hi_min = min(hi_min, see.t1);
             }
-            cq[v] = sc.x;
-            if constexpr (HAD) c_init[v][0] = sc.y, c_init[v][1] = sc.z;
-            else c_init[v >> 1][v & 1] = sc.y;
         }
         lo_max = __reduce_max_sync(~0u, lo_max);
         hi_min = __reduce_min_sync(~0u, hi_min);
@@ -464,10 +461,7 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
                     load_words(ring + (mt * 16 + hf * 8 + r8) * (D / 2) + t * (D / 8), kw[hf]);
                 float s[QT][4];
 #pragma unroll
-                for (int n = 0; n < QT; ++n) {
-                    s[n][0] = s[n][2] = c_init[n][0];
-                    s[n][1] = s[n][3] = c_init[n][1];
-                }
+                for (int n = 0; n < QT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
                     uint32_t x[2][4];
@@ -475,9 +469,9 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
                     for (int hf = 0; hf < 2; ++hf) {
                         const uint32_t w = kw[hf][i], w8 = w >> 8;
                         x[0][hf] = codes_low(w);
-                        x[1][hf] = codes_high(w);
+                        x[1][hf] = codes_upper(w);
                         x[0][2 + hf] = codes_low(w8);
-                        x[1][2 + hf] = codes_high(w8);
+                        x[1][2 + hf] = codes_upper(w8);
                     }
 #pragma unroll
                     for (int n = 0; n < QT; ++n) {

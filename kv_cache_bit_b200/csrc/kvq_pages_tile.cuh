@@ -242,7 +242,6 @@ __global__ void __launch_bounds__(kQueryWarps * 32) pages_queries_kernel(StepArg
 #pragma unroll
     for (int x = 16; x; x >>= 1) m = max_or_nan(m, __shfl_xor_sync(~0u, m, x));
     const float f = m > 0.0f || m != m ? query_scale(m) : 1.0f;
-    float sum[2] = {0.0f, 0.0f};  // of the channels whose codes come with kHigh
     __half* dst = g.frag + at * (HAD ? 2 : 1) * D;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -253,19 +252,9 @@ __global__ void __launch_bounds__(kQueryWarps * 32) pages_queries_kernel(StepArg
         const float x = v[k] * f;
         const __half hi = __float2half_rn(x);
         dst[place8] = hi;
-        if (k & 1) sum[0] += __half2float(hi);
-        if constexpr (HAD) {
-            const __half lo = __float2half_rn(x - __half2float(hi));
-            dst[D + place8] = lo;
-            if (k & 1) sum[1] += __half2float(lo);
-        }
+        if constexpr (HAD) dst[D + place8] = __float2half_rn(x - __half2float(hi));
     }
-#pragma unroll
-    for (int x = 16; x; x >>= 1) {
-        sum[0] += __shfl_xor_sync(~0u, sum[0], x);
-        if constexpr (HAD) sum[1] += __shfl_xor_sync(~0u, sum[1], x);
-    }
-    if (lane == 0) g.scal[at] = make_float4(a.scale2 / f, -kHigh * sum[0], -kHigh * sum[1], 0.0f);
+    if (lane == 0) g.scal[at] = a.scale2 / f;
 }
 
 // A walk over a CTA's segments; every warp has its own.  An item takes
