@@ -21,13 +21,15 @@
 // when a softmax ends one; with one S of 128 tokens a half, which the tensor
 // core fills faster, softmax and products waited for each other in turn (9000
 // cycles for 128 tokens).  Tiles of K and V go through a ring of six buffers.
-// W is the probability itself here, 2^(x - M), and the V tile holds sigma q
-// rounded to fp16 (2^-12, as W is): the scheme of the step kernel, with the V
-// scale in the exponent, needs two more numbers a token in every softmax
-// thread, and a number that all lanes read from shared memory takes it as long
-// as 32 different ones (3072 cycles a step for three numbers; the products
-// take as long).  Values below fp16's normal range are kept to 2^-25, which is
-// also what their fp16 scale was rounded to.
+// With the reference R of a row (its largest score + the largest exponent of a
+// tile's V scales, over the tiles so far, up to 2^kSlack), p = 2^(x - R + kTileBias),
+//   W = fp16(p sigma_V),  O = sum W q,  l = sum p,
+// so W is the only rounding here too, and stays in fp16's range; what is below
+// its normal range is kept to 2^-31 of the largest V scale.  (V tiles of
+// sigma q, rounded, with W = p, need no scale in the softmax threads: the same
+// time, but 3.0e-4 of the values instead of 2.3e-4.)  The scales are read in
+// fp16: a number that all lanes read from shared memory takes it as long as 32
+// different ones, and three fp32 numbers a token took as long as the products.
 // O stays in tensor memory; a row whose maximum rose by more than 2^kSlack
 // scales it there (its O is at rest between its S and its W).
 #pragma once
@@ -45,7 +47,7 @@ constexpr int kTileThreads = 512;
 constexpr int kRingTiles = 6, kParStages = 4;
 constexpr int kUnitTokens = 32, kUnits = kTileTokens / kUnitTokens;  // units of a tile
 constexpr float kSlack = 8.0f;               // how far a row's maximum may pass its reference
-constexpr float kTileBias = kBias - kSlack;  // w = 2^(y - M + kTileBias) stays in fp16
+constexpr float kTileBias = 6.0f;            // W < 2^(kSlack + kTileBias + 1), in fp16's range
 constexpr uint32_t kTileWait = 1u << 22;  // polls, of a second at most together
 // Registers a thread; the launch gives 128.
 constexpr int kLaunchRegs = 128, kSoftmaxRegs = 160, kProducerRegs = 96;
@@ -315,7 +317,8 @@ struct TileSmem {
     static constexpr int kQuery = kRowsM * D * 2;      // of a part of a half's queries
     alignas(1024) uint8_t q[2][HAD ? 2 : 1][kQuery];   // [half][high, low][64 channels][row]
     alignas(1024) uint8_t ring[kRingTiles][kTile];
-    alignas(16) __half par[kParStages][kTileTokens];   // K scales
+    alignas(16) __half par[kParStages][2][kTileTokens];  // K and V scales
+    alignas(8) int expo[kParStages][kUnits];           // largest exponent of a unit's V scales
     alignas(8) uint32_t absent[kParStages][kUnits];    // tokens of the tile that are not there, a bit each
     alignas(16) uint32_t signs[D / 2];                 // sign bits of two channels' signs
     uint64_t full[kRingTiles], empty[kRingTiles];
@@ -411,17 +414,12 @@ __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ uint32_t mul2(uint32_t x, uint32_t y) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
-    return r;
-}
 // Four 16-byte pieces of a 128-byte-swizzled tile from 32 codes of one token:
 // channels 32 quarter .. + 31 of row `row`.  Of eight channels the halves are
 // in the order 0 4 1 5 2 6 3 7, as the queries' and O's are.  Lanes of the
 // second 64 channels take their pieces in another order: the same places of
 // the two 64-channel halves lie in the same banks.
-__device__ __forceinline__ void store_codes(uint8_t* tile, int row, int quarter, const uint4& w, uint32_t scale) {
+__device__ __forceinline__ void store_codes(uint8_t* tile, int row, int quarter, const uint4& w) {
     const bool upper = quarter & 2;
     const uint32_t words[4] = {upper ? w.y : w.x, upper ? w.x : w.y, upper ? w.w : w.z, upper ? w.z : w.w};
     uint8_t* base = tile + (upper ? kTileTokens * 128 : 0) + row * 128;
@@ -430,30 +428,29 @@ __device__ __forceinline__ void store_codes(uint8_t* tile, int row, int quarter,
     for (int k = 0; k < 4; ++k) {
         const uint32_t x = words[k], x8 = x >> 8;
         *reinterpret_cast<uint4*>(base + (k ^ swizzle) * 16) =
-            make_uint4(mul2(codes_low(x), scale), mul2(codes_upper(x), scale), mul2(codes_low(x8), scale),
-                       mul2(codes_upper(x8), scale));
+            make_uint4(codes_low(x), codes_upper(x), codes_low(x8), codes_upper(x8));
     }
 }
 // Order of eight channels in a 16-byte piece: place p holds channel place8(p).
 __host__ __device__ constexpr int place8(int p) { return (p >> 1) + 4 * (p & 1); }
 
-// 32 tokens of a tile of K or V, by one warp: codes and scales into registers,
-// and from there, as fp16, into the tile.  K and V share the code (K's codes
-// are multiplied by 1): the instruction cache holds the loops of all roles,
-// and hardly more.
+// 32 tokens of a tile of K or V, by one warp: codes into registers, and from
+// there, as fp16, into the tile; with K's also the scales of both.  K and V
+// share the code: the instruction cache holds the loops of all roles, and
+// hardly more.
 template <int D>
 struct Unit {
     static constexpr int kPieces = D / 32, kLoads = kPieces;  // 16-byte pieces of a token; loads of a lane
     uint4 w[kLoads];
-    __half scale;  // of the token that is this lane's
-    bool absent;   // which is not there
+    __half scale[2];  // K's and V's of the token that is this lane's
+    bool absent;      // which is not there
 
     // pg: the pages of the two halves as the table has them.
     __device__ __forceinline__ void fetch(const TileArgs& g, int h, int t0, int t1, int tok, int is_v, int pg0, int pg1) {
         const Pool& p = g.a.p;
         const int lane = threadIdx.x & 31;
         absent = tok + lane < t0 || tok + lane >= t1;
-        scale = __ushort_as_half(0);
+        scale[0] = scale[1] = __ushort_as_half(0);
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
             const int t = tok + 16 * hf, pg = hf ? pg1 : pg0;
@@ -466,22 +463,19 @@ struct Unit {
                 const uint4* src = reinterpret_cast<const uint4*>(p.codes[is_v]) + at * (uint64_t)kPieces + lane;
 #pragma unroll
                 for (int k = 0; k < kLoads / 2; ++k) w[hf * (kLoads / 2) + k] = src[32 * k];
-                if ((lane >> 4) == hf && !absent) scale = p.tok[is_v][at + (lane & 15)];
+                if (!is_v && (lane >> 4) == hf && !absent)
+                    scale[0] = p.tok[0][at + (lane & 15)], scale[1] = p.tok[1][at + (lane & 15)];
             } else {
                 absent |= (lane >> 4) == hf;
                 if (needed) report_error(kErrRange);
             }
         }
     }
-    __device__ __forceinline__ void store(uint8_t* tile, int first_row, int is_v) const {
+    __device__ __forceinline__ void store(uint8_t* tile, int first_row) const {
         const int lane = threadIdx.x & 31;
-        const uint32_t mine = is_v ? __half_as_ushort(scale) : 0x3C00u;
 #pragma unroll
-        for (int k = 0; k < kLoads; ++k) {
-            const int row = k * (32 / kPieces) + lane / kPieces;
-            const uint32_t x = __shfl_sync(~0u, mine, row);
-            store_codes(tile, first_row + row, lane % kPieces, w[k], x | x << 16);
-        }
+        for (int k = 0; k < kLoads; ++k)
+            store_codes(tile, first_row + k * (32 / kPieces) + lane / kPieces, lane % kPieces, w[k]);
     }
 };
 
@@ -647,10 +641,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                     !(ok = n < 2 || o_done(tile - 2)))  // (done when S is; a barrier's phases are waited for in turn)
                     break;
                 tc_after_sync();
-                const __half* par = sm.par[stage];
+                const __half* par = sm.par[stage][0];
                 uint32_t s[2][32];
                 tmem_load32(s[0], ts);
                 tmem_load32(s[1], ts + 32);
+                const int2 ex = *reinterpret_cast<const int2*>(sm.expo[stage]);
                 const uint2 gone = *reinterpret_cast<const uint2*>(sm.absent[stage]);
                 tmem_wait_load();
                 if (scaled || tok0 < see_lo || tok0 + kTileTokens > see_hi || (gone.x | gone.y)) {
@@ -683,9 +678,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                             tops[j] = fmaxf(tops[j], fmaxf(x0, x1));
                         }
                     }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.par_empty[stage]);
-                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a.scale2;
+                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a.scale2 +
+                                  (float)max(ex.x, ex.y);
                 if (__any_sync(~0u, top > M + kSlack)) {
                     const float m2 = top > M + kSlack ? top : M, f = ex2(M - m2);  // (other rows as they were)
                     const uint64_t ff = pair2(f, f);
@@ -711,19 +705,23 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
-                        float p[4];
-                        unpair2(fma_f2(pair2(__uint_as_float(s[e][c]), __uint_as_float(s[e][c + 1])), scale2, ref), p[0],
-                                p[1]);
-                        unpair2(fma_f2(pair2(__uint_as_float(s[e][c + 2]), __uint_as_float(s[e][c + 3])), scale2, ref), p[2],
-                                p[3]);
+                    for (int c = 0; c < 32; c += 8) {
+                        const uint4 sv = *reinterpret_cast<const uint4*>(&par[kTileTokens + 32 * e + c]);
+                        const uint32_t two[4] = {sv.x, sv.y, sv.z, sv.w};
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) p[j] = ex2(p[j]);
-                        l2[0] = add_f2(l2[0], pair2(p[0], p[1]));
-                        l2[1] = add_f2(l2[1], pair2(p[2], p[3]));
-                        w[16 * e + c / 2] = Elem<__half>::pack(p[0], p[1]);
-                        w[16 * e + c / 2 + 1] = Elem<__half>::pack(p[2], p[3]);
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t* x = &s[e][c + 2 * j];
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two[j]));
+                            float p0, p1;
+                            unpair2(fma_f2(pair2(__uint_as_float(x[0]), __uint_as_float(x[1])), scale2, ref), p0, p1);
+                            const uint64_t p = pair2(ex2(p0), ex2(p1));
+                            l2[j & 1] = add_f2(l2[j & 1], p);
+                            unpair2(mul_f2(p, pair2(f.x, f.y)), p0, p1);
+                            w[16 * e + c / 2 + j] = Elem<__half>::pack(p0, p1);
+                        }
                     }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.par_empty[stage]);
                 tmem_store32(ts, w);
                 tmem_wait_store();
                 tc_before_sync();
@@ -768,7 +766,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                 if (there && a.lse) a.lse[(long long)row * a.Hq + head] = (M - kTileBias + lg2(l)) * kLn2;
             } else if (there) {
                 const long long at = (2ll * blockIdx.x + (begins ? 1 : 0)) * kItemRows + half * kRowsM + r;
-                reinterpret_cast<float2*>(a.ml)[at] = make_float2(M + kSlack, l);
+                reinterpret_cast<float2*>(a.ml)[at] = make_float2(M + (kBias - kTileBias), l);
                 float4* dst = reinterpret_cast<float4*>(a.part + at * D);
 #pragma unroll
                 for (int p = 0; p < D; p += 4)
@@ -883,10 +881,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
             if (!is_v) {
                 if (turn > 0 && !wait(&sm.par_empty[stage], (turn - 1) & 1)) break;
                 const uint32_t absent = __ballot_sync(~0u, un.absent);
-                sm.par[stage][rows + lane] = __hmax(un.scale, __ushort_as_half(1));
-                if (lane == 0) sm.absent[stage][rows / kUnitTokens] = absent;
+                const uint32_t expo = __reduce_max_sync(~0u, (uint32_t)__half_as_ushort(un.scale[1]) >> 10);
+                sm.par[stage][0][rows + lane] = __hmax(un.scale[0], __ushort_as_half(1));
+                sm.par[stage][1][rows + lane] = un.scale[1];
+                if (lane == 0) {
+                    sm.absent[stage][rows / kUnitTokens] = absent;
+                    sm.expo[stage][rows / kUnitTokens] = (int)max(expo, 1u) - 15;
+                }
             }
-            un.store(sm.ring[buf], rows, is_v);
+            un.store(sm.ring[buf], rows);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {

@@ -106,13 +106,13 @@ def attention(k, v, b: Seqs, q: np.ndarray, signs, scale, causal, window, half_s
               argument add three fp32 roundings of the score.
               delta = 2^-17 sum |q~| 15 sigma scale + 4 2^-24 |score|
       p       exp(score - reference): e^(2 delta) - 1 against the others, the
-              exponential itself 2^-21; p sigma_v is rounded to fp16, 2^-12,
-              or p and sigma_v q are, 2^-11 together
+              exponential itself 2^-21; p sigma_v is rounded to fp16, 2^-12
+              (2^-11 is counted)
       values  sum of p sigma_v e, |e| <= 15, again 2^-17 of its magnitudes
       result  half a step of its type
-    With `many` (sequences of many rows, where p and sigma_v q are rounded
-    apart) a value is also off by half of fp16's smallest step, 2^-25, and a
-    token's p by as much of 2^7 or more for the largest: 2^-32 each.
+    With `many` (sequences of many rows, whose p sigma_v is scaled by the
+    largest score and the largest sigma_v) it is also off by 2^-25 below
+    2^-14, of 2^6 or more for those largest: by 2^-31 of the largest sigma_v.
     The rotation back is orthogonal: each element's error is at most the
     2-norm of the errors before it."""
     H, d, Hq = k[0].shape[1], q.shape[2], q.shape[1]
@@ -149,7 +149,7 @@ def attention(k, v, b: Seqs, q: np.ndarray, signs, scale, causal, window, half_s
                 err = rel * ((p * vs[g, sees]) @ np.abs(vq[g, sees])) / l \
                     + 2.0 ** -17 * 15 * float((p * vs[g, sees]).sum()) / l
                 if many:
-                    err = err + 2.0 ** -25 + 2.0 ** -32 * (np.abs(vq[g, sees]) * vs[g, sees, None]).sum(0) / l
+                    err = err + 2.0 ** -31 * vs[g, sees].max() * np.abs(vq[g, sees]).sum(0) / l
                 out[j] = o @ R if signs is not None else o
                 e2 = np.linalg.norm(err) if signs is not None else err
                 tol[j] = e2 + half_step * (np.abs(out[j]) + e2) + 2.0 ** -25
