@@ -166,9 +166,10 @@ struct ReadLaunch {
 };
 
 // Dynamic shared memory and the largest carveout, once per kernel and device
-// (racing callers set the same attributes, which is harmless).
+// (racing callers set the same attributes, which is harmless).  regs: what the
+// kernel's register split needs the launch to give a thread.
 template <auto Kernel>
-bool allow_smem(int bytes) {
+bool allow_smem(int bytes, int regs = 0) {
     static std::atomic<uint64_t> done{0};  // one bit a device
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
@@ -179,6 +180,13 @@ bool allow_smem(int bytes) {
             cudaSuccess) {
         cudaGetLastError();
         return false;
+    }
+    if (regs > 0) {
+        cudaFuncAttributes at;
+        if (cudaFuncGetAttributes(&at, Kernel) != cudaSuccess || at.numRegs < regs) {
+            cudaGetLastError();
+            return false;
+        }
     }
     done.fetch_or(bit, std::memory_order_release);
     return true;
@@ -288,14 +296,7 @@ kvq_status launch_tiles(const TileArgs& t, int sms, cudaStream_t st) {
     constexpr auto kernel = pages_tile_kernel<D, HAD>;
     constexpr int smem = (int)sizeof(TileSmem<D, HAD>);
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
-    if (!allow_smem<kernel>(smem)) return KVQ_ERR_CUDA;
-    // the kernel's register split needs all that the launch gives it
-    static const bool fits = [&] {
-        cudaFuncAttributes at;
-        return cudaFuncGetAttributes(&at, kernel) == cudaSuccess &&
-               at.numRegs >= kLaunchRegs;
-    }();
-    if (!fits) return KVQ_ERR_CUDA;
+    if (!allow_smem<kernel>(smem, kLaunchRegs)) return KVQ_ERR_CUDA;
     const kvq_status s = launch(kernel, dim3(sms), kTileThreads, smem, st, t);
     if (s != KVQ_OK) return s;
     return launch(pages_merge_kernel<D, kItemRows, HAD>, dim3(sms, kItemRows / merge_queries(kItemRows)), kMergeWarps * 32, 0,
@@ -416,7 +417,7 @@ kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, co
     if ((s = check_rows(out, rows, q_heads, d, true, false)) != KVQ_OK) return s;
     if (q->dtype != out->dtype || window < 0 || (window > 0 && causal == 0)) return KVQ_ERR_INVALID_ARG;
     if (lse != nullptr && !ok_ints(lse)) return KVQ_ERR_INVALID_ARG;
-    if (!(scale <= 3.0e38f)) return KVQ_ERR_INVALID_ARG;  // infinite or NaN
+    if (!(scale <= 2.0e38f)) return KVQ_ERR_INVALID_ARG;  // infinite or NaN, or times log2 e infinite
     if (rows == 0 || batch->n_seqs == 0) return KVQ_OK;
     intptr_t ql, qh, ol, oh;
     extent(q, rows, q_heads, d, &ql, &qh);

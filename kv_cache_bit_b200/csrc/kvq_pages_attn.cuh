@@ -3,14 +3,15 @@
 // row), and the merge of partial states.
 //
 // The softmax with the value scale inside.  With x_t the score of token t in
-// the log2 domain and sigma_t its value scale, the kernels form
+// the log2 domain and sigma_t its value scale, the generation-step kernel forms
 //   y_t = x_t + log2 sigma_t,   w_t = 2^(y_t - M + kBias),   M >= max y_t
 //   o = sum_t w_t q^V_t,        l = sum_t w_t / sigma_t
 // so that o / l is the softmax average and M + log2 l - kBias its logarithm
 // (base 2).  w is the only value that is rounded to fp16, at most 2^kBias and
 // normal down to 2^-29 of the largest, whatever the scales are; one addition
 // replaces the product with sigma.  A scale of 0 (a zero vector) counts as
-// 2^-24 in y and 1 / sigma: its codes are all 0.
+// 2^-24 in y and 1 / sigma: its codes are all 0.  (The tile kernel's form
+// stands there; it leaves the same M, l and o.)
 #pragma once
 
 #include "kvq_pages.cuh"

@@ -277,6 +277,36 @@ def test_attention_of_long_prompts(d, G, dtype, rotated, causal, window):
     s.check(q, *s.attend(q, causal=causal, window=window), dtype, causal=causal, window=window, only=only)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_of_many_rows_over_few_tokens(causal):
+    """Empty sequences and paddings with as many rows as a prompt."""
+    s = Setup([(0, 100), (5, 90), (1, 64), (64, 300), (128, 128), (-3, 70)], page=16)
+    q = s.tensor(4, "fp16")
+    s.check(q, *s.attend(q, causal=causal), "fp16", causal=causal)
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    import subprocess
+    import sys
+    code = '''
+import torch
+from tests.test_gpu_pages import Setup
+s = Setup([(300, 150), (90, 1)], page=16)
+q = s.tensor(8, "fp16")
+out, ws = torch.zeros_like(q), torch.empty(
+    s.kvq.kvq_pages_attention_workspace_bytes(s.cfg, s.pages, s.batch, s.rows, 8), dtype=torch.uint8, device="cuda")
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    s.kvq.kvq_pages_attention(s.cfg, s.pages, s.batch, q, out, ws=ws)
+g.replay()
+torch.cuda.synchronize()
+s.check(q, out, None, "fp16", only={0, 80, 149, 150})
+print("captured")
+'''
+    done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=240)
+    assert done.returncode == 0 and "captured" in done.stdout, done.stderr[-2000:]
+
+
 def test_attention_with_a_wrong_row_hint_and_without_lse():
     for hint in (0, 1, 7, 10 ** 6):
         s = Setup([(150, 40), (20, 1), (90, 90)], max_rows=hint)
