@@ -10,10 +10,10 @@
 // sequence and page, about as many instructions as half a vector, is then made
 // once for them.
 //
-// Both are bound by HBM when they are long.  Instructions a vector (D = 128,
-// rotated): writing, in packed fp32 pairs, about 90 a lane of which 24 are
-// shuffles; reading, whose butterflies are exact in fp16 pairs (sums of codes
-// stay below 1024), about 75.
+// A warp's instructions for eight vectors (D = 128, rotated): 518 writing, in
+// packed fp32 pairs, 66 of them shuffles; 410 reading, whose butterflies are
+// exact in fp16 pairs (sums of codes stay below 1024).  32 x 4096 rows, 8 kv
+// heads: 177 us to write (HBM would take 103), 126 us to read back (103).
 #pragma once
 
 #include <cuda_bf16.h>

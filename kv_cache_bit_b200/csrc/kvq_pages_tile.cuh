@@ -31,7 +31,11 @@
 // fp16: a number that all lanes read from shared memory takes it as long as 32
 // different ones, and three fp32 numbers a token took as long as the products.
 // O stays in tensor memory; a row whose maximum rose by more than 2^kSlack
-// scales it there (its O is at rest between its S and its W).
+// scales it there, once the step before is in it.
+// Measured (8192 rows and tokens, 32 query heads over 8, rotated, D = 128):
+// 1000 us, 550 TFLOP/s of 4 D a (row, token, head); the products and their
+// reads of shared memory (a 64-token product of 128 rows reads 6 KB in the 32
+// cycles that it computes) are busy 60% of it, the exponentials a third.
 #pragma once
 
 #include "kvq_pages_attn.cuh"
