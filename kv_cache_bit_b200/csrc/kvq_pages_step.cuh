@@ -253,23 +253,34 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
     // pages_queries_kernel let this kernel start once all before it was done; what it writes itself is
     // waited for below
 
-    // ---- the warps' ranges: prefix sums of the sequences' costs, a run of `per` sequences a thread
-    const int per = (a.b.n_seqs + NW * 32 - 1) / (NW * 32), s0 = threadIdx.x * per;
+    // ---- the warps' ranges: prefix sums of the sequences' costs, a run of `per` sequences a thread; up to two a
+    // lane, every warp by itself
+    const bool alone = a.b.n_seqs <= 64;
+    const int runs = alone ? 32 : NW * 32, run = alone ? lane : threadIdx.x;
+    const int per = (a.b.n_seqs + runs - 1) / runs, s0 = run * per;
+    Item mine0;  // of the run's first sequence
+    mine0.cost = 0;
     long long mine = 0;
-    for (int s = s0; s < min(s0 + per, a.b.n_seqs); ++s) mine += share_of<NQ>(g, item_of<NQ>(g, s, H), H);
+    for (int s = min(s0 + per, a.b.n_seqs) - 1; s >= s0; --s) {
+        mine0 = item_of<NQ>(g, s, H);
+        mine += share_of<NQ>(g, mine0, H);
+    }
     long long sum = mine;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
         const long long o = __shfl_up_sync(~0u, sum, x);
         if (lane >= x) sum += o;
     }
-    if (lane == 31) sh.sums[warp] = sum;
-    __syncthreads();
-    long long before = sum - mine, total = 0;
+    long long before = sum - mine, total = __shfl_sync(~0u, sum, 31);
+    if (!alone) {
+        if (lane == 31) sh.sums[warp] = sum;
+        __syncthreads();
+        total = 0;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-        if (w < warp) before += sh.sums[w];
-        total += sh.sums[w];
+        for (int w = 0; w < NW; ++w) {
+            if (w < warp) before += sh.sums[w];
+            total += sh.sums[w];
+        }
     }
     const int me = blockIdx.x * NW + warp;
     const int workers = g.whole ? (int)min((long long)gridDim.x, total) * NW : (int)min((long long)gridDim.x * NW, total);
@@ -281,21 +292,37 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
     const long long share = g.whole ? 1 : quotient(total, workers);  // the first `extra` warps have one unit more
     const int extra = g.whole ? 0 : (int)(total - share * workers);
     const auto begin_of = [&](int worker) { return share * worker + min(worker, extra); };
-    sh.before[threadIdx.x] = before;
-    __syncthreads();
+    if (!alone) {
+        sh.before[threadIdx.x] = before;
+        __syncthreads();
+    }
     {
         Walk<NQ> w;
         w.n = 0;
         if (me < workers) {
             const long long first = g.whole ? blockIdx.x : begin_of(me);
-            int lo = 0, hi = NW * 32;  // the run that holds the first position (or the item)
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (sh.before[mid] <= first) lo = mid;
-                else hi = mid;
+            long long off;
+            if (alone) {  // the lane whose run holds the first position (or the item)
+                const uint32_t owner = __ballot_sync(~0u, before <= first && first < before + mine);
+                const int src = max(__ffs(owner) - 1, 0);
+                off = first - __shfl_sync(~0u, before, src);
+                constexpr int kWords = sizeof(Item) / 4;
+                static_assert(sizeof(Item) % 4 == 0);
+                int words[kWords];
+                memcpy(words, &mine0, sizeof(Item));
+#pragma unroll
+                for (int k = 0; k < kWords; ++k) words[k] = __shfl_sync(~0u, words[k], src);
+                memcpy(&w.it, words, sizeof(Item));
+            } else {
+                int lo = 0, hi = NW * 32;
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (sh.before[mid] <= first) lo = mid;
+                    else hi = mid;
+                }
+                off = first - sh.before[lo];
+                w.it = item_of<NQ>(g, lo * per, H);
             }
-            long long off = first - sh.before[lo];
-            w.it = item_of<NQ>(g, lo * per, H);
             while (w.it.s + 1 < a.b.n_seqs) {
                 const long long of_seq = share_of<NQ>(g, w.it, H);
                 if (off < of_seq) break;
@@ -372,8 +399,8 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
         }
         copies_commit();
     };
-    for (int i = 0; i < kRingPages; ++i) produce(i);
     grid_dep_wait();
+    bool primed = false;
 
     int slot = 0;
 
@@ -401,6 +428,10 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k) qf[n][k] = src[4 * k];
             }
+        }
+        if (!primed) {  // (behind the loads of the first queries)
+            primed = true;
+            for (int i = 0; i < kRingPages; ++i) produce(i);
         }
         int lo_max = 0, hi_min = 0x7FFFFFFF;  // tokens that all of the chunk's rows see
 #pragma unroll
