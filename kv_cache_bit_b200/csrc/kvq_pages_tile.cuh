@@ -538,9 +538,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
     __syncwarp();
     const auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(~0u, wait_one(bar, parity)) != 0; };
 
+    // All warps of a warpgroup (0 .. 3, 4 .. 7, 8 .. 11, 12 .. 15) have to run one and the same setmaxnreg: the
+    // roles part behind it, since producers and issuers share a warpgroup.
+    if (works) {
+        if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+    }
     if (works && warp < 8) {
         // ------------------------------------------------ softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int half = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
         const uint32_t ts0 = tmem + lanes + half * 128, to = tmem + lanes + 256 + half * 128;
@@ -785,7 +790,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
             }
         }
     } else if (works && warp >= 14) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
         // ------------------------------------------------ products
         // All lanes walk along, so that addresses and descriptors stay in uniform registers; one issues.  (With
         // one lane in the loop an issue took 80 cycles, longer than the product itself.)
@@ -849,7 +853,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
         __syncwarp();
     } else if (works) {
         // ------------------------------------------------ tiles of K and V
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
         // units of 32 tokens: those of a step's K tile, of its V tile, of the next step's, ..; this warp
         // takes every kProducers-th
         uint32_t step = 0, unit = warp - 8;
