@@ -24,14 +24,15 @@
 //           largest element is near 2^15.  A rotated query is split into fp16
 //           high and low parts in neighbouring columns (22 bits of it are
 //           kept); an input that is not rotated fits fp16 exactly.
-//   values  A = V codes transposed (byte permutes pair two tokens' words), the
-//           upper nibbles ORed into the mantissa of 64, which gives q + 72
-//           without arithmetic; B = w from the score fragments by movmatrix.
-//           One more product, with ones, gives the sum of w that takes the 72
-//           out.  (For K the same cost 1e-6 of the logarithm of the sum.  The
-//           bits taken as subnormals e 2^-24 need no arithmetic at all, but
-//           the tensor core aligns products by their exponent fields and drops
-//           what falls below: errors of 7e-4 of the values.)
+//   values  A = V codes transposed (byte permutes pair two tokens' words), exact
+//           as K's; B = w from the score fragments by movmatrix.  (Codes with a
+//           bias, which save the addition, are no good: the sum of w (q + 72)
+//           grows with the number of tokens, that of w q with its root, and the
+//           72 sum w taken away at the end leaves the accumulator's rounding,
+//           3e-2 of the outputs after 4800 tokens of equal weights.  The bits
+//           taken as subnormals e 2^-24 need no arithmetic at all, but the
+//           tensor core aligns products by their exponent fields and drops what
+//           falls below: errors of 7e-4 of the values.)
 // Measured at 64 x 500 .. 8192 tokens, 32 query heads over 8, rotated, D = 128:
 // 304 warp instructions a 16-token tile, set-up and merging included (the
 // block cache's kernel: 332), 78 us; the loop itself reads at 5.8 TB/s.
@@ -191,9 +192,6 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// The codes of nibbles 1 and 5 as 64 + e = q + kHigh, without arithmetic.
-constexpr float kHigh = 72.0f;
-__device__ __forceinline__ uint32_t codes_high(uint32_t w) { return in_mantissa<0x00F000F0u, 0x54005400u>(w); }
 
 // 16 bytes to shared memory: `n` (16 or 0) of them from src, zeros for the rest.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n) {
@@ -410,7 +408,7 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
         const int units = wk.n, unit0 = wk.it.u0 + wk.u, seen0 = wk.it.t0, seen1 = wk.it.t1;
         const bool final = wk.x + wk.span >= wk.end;  // the range's last segment
         float M[NV], l[NV], cq[NV];
-        float o[NP][NJ][4], sums[NP][4];  // sums: of w
+        float o[NP][NJ][4];
         const int i0 = wk.c * NQ, lo = wk.it.lo, nq = wk.it.nq;
         // index of query i of the item among the prepared ones
         const int query0 = (g.many > 0 ? wk.it.s * g.stretch : lo) * a.Hq + wk.h * a.G;
@@ -451,14 +449,11 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
         lo_max = __reduce_max_sync(~0u, lo_max);
         hi_min = __reduce_min_sync(~0u, hi_min);
 #pragma unroll
-        for (int n = 0; n < NP; ++n) {
+        for (int n = 0; n < NP; ++n)
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o[n][j][k] = 0.0f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) sums[n][k] = 0.0f;
-        }
         if constexpr (!kHold) {
 #pragma unroll
             for (int n = 0; n < QT; ++n)
@@ -554,7 +549,6 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
                         o[v >> 1][j][v & 1] *= f;
                         o[v >> 1][j][2 + (v & 1)] *= f;
                     }
-                    sums[v >> 1][v & 1] *= f;
                 }
             }
 #pragma unroll
@@ -592,18 +586,15 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
                             const bool up = D == 128 ? j0 != 0 : k != 0;
                             const uint32_t p = perm(vw[hf][0][wd], vw[hf][1][wd], up ? 0x7632u : 0x5410u), p8 = p >> 8;
                             z[0][2 * hf + k] = codes_low(p);
-                            z[1][2 * hf + k] = codes_high(p);
+                            z[1][2 * hf + k] = codes_upper(p);
                             z[2][2 * hf + k] = codes_low(p8);
-                            z[3][2 * hf + k] = codes_high(p8);
+                            z[3][2 * hf + k] = codes_upper(p8);
                         }
 #pragma unroll
                     for (int n = 0; n < NP; ++n)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) mma(o[n][j0 + j], z[j], bw[n][0], bw[n][1]);
                 }
-                const uint32_t one[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
-#pragma unroll
-                for (int n = 0; n < NP; ++n) mma(sums[n], one, bw[n][0], bw[n][1]);
             }
             __syncwarp();  // the slot has been read
             produce(slot);
@@ -644,8 +635,7 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) pages_step_kernel(StepArgs g)
                 for (int j = 0; j < NJ; ++j)
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf)
-                        dst[(2 * j + hf) * 8 + r8] = j & 1 ? __fmaf_rn(-kHigh, sums[n][k], o[n][j][2 * hf + k])
-                                                           : o[n][j][2 * hf + k];
+                        dst[(2 * j + hf) * 8 + r8] = o[n][j][2 * hf + k];
             }
             __syncwarp();
             if (whole || !final) {

@@ -99,11 +99,11 @@ def attention(k, v, b: Seqs, q: np.ndarray, signs, scale, causal, window, half_s
     all rows or of those in `only`.
 
     Roundings of the kernels, each relative to what it rounds:
-      scores  the query keeps 22 bits, the products with codes (of magnitude
-              15 at most, or up to 79 for half of them: 64 + e) are summed in
-              the tensor core within 2^-19 of the sum of their magnitudes, or
-              in fp32 (128 terms: 2^-17 at worst); the scaling and exp2's
-              argument add three fp32 roundings of the score.
+      scores  the query keeps 22 bits, the products with codes (exact, 15 is
+              counted for their magnitude) are summed in the tensor core
+              within 2^-19 of the sum of their magnitudes, or in fp32 (128
+              terms: 2^-17 at worst); the scaling and exp2's argument add
+              three fp32 roundings of the score.
               delta = 2^-17 sum |q~| 15 sigma scale + 4 2^-24 |score|
       p       exp(score - reference): e^(2 delta) - 1 against the others, the
               exponential itself 2^-21; p sigma_v is rounded to fp16, 2^-12

@@ -1,0 +1,72 @@
+"""Paged attention on the GPU to within the averages that its roundings leave
+(tests/pages_precision.py): long ranges of tokens, equal weights, ordinary
+batches of few and of many rows."""
+import numpy as np
+import pytest
+
+from tests import pages_precision as prec
+from tests import pages_ref as ref
+from tests.test_gpu_pages import Setup, host
+
+pytestmark = pytest.mark.gpu
+
+
+def shared(n_seqs, tokens, G, d, rotated, page, sharp, ragged=False):
+    """One stored sequence that all sequences of a batch share, a query row each:
+    (setup, q, out, lse, exact out, exact lse)."""
+    import torch
+    s = Setup([(tokens, 1)], d=d, H=1, page=page, rotated=rotated)
+    k, v = prec.stored(s, 0, tokens)
+    length = np.full(n_seqs, tokens, np.int32)
+    if ragged:
+        length = s.rng.integers(1, tokens + 1, n_seqs).astype(np.int32)
+    dev = lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda()  # noqa: E731
+    s.batch = s.kvq.Batch(dev(np.arange(n_seqs + 1, dtype=np.int32)), dev(length),
+                          s.batch.table.repeat(n_seqs, 1).contiguous(), max_rows=1)
+    s.rows = n_seqs
+    q = s.tensor(G, "fp16", scale=sharp)
+    out, lse = s.attend(q)
+    assert s.kvq.kvq_pages_read_errors() == 0
+    return s, q, out, lse, prec.exact(q, k, v, s.signs, length.astype(np.int64) - 1, length.astype(np.int64))
+
+
+@pytest.mark.parametrize("d,G,rotated,page", [(128, 4, True, 16), (128, 8, False, 64), (128, 12, True, 32),
+                                              (64, 2, True, 128), (64, 16, False, 16)])
+def test_nearly_equal_weights_over_thousands_of_tokens_a_warp(d, G, rotated, page):
+    """1040 sequences of 8192 tokens and one kv head are some 4800 tokens a warp
+    of the generation-step kernel, in one sum: what the sum rounds must not grow
+    with its length, in any channel."""
+    s, q, out, lse, (want, want_lse) = shared(1040, 8192, G, d, rotated, page, 0.1)
+    assert not prec.faults(out, lse, want, want_lse, "fp16")
+    # All rows have nearly the same output, the values' mean, so that a channel's may be far from the rms of all.
+    # Of the two roundings the weights' is 2^-11 / sqrt 3 of the rms of all channels (values of one size), the
+    # output's 2^-11 / sqrt 3 of the channel's own: together 2^-11 sqrt((rms^2 + rms_c^2) / 3); / 2 is allowed,
+    # which is the limit of all channels where rms_c = rms.
+    err, size = (out.double() - want).square().mean((0, 1)), want.square().mean((0, 1))
+    assert bool((err.sqrt() <= prec.LIMITS["fp16"][0] * ((size.mean() + size) / 2).sqrt()).all())
+
+
+@pytest.mark.parametrize("d,G,rotated,page", [(128, 4, True, 16), (64, 8, False, 32), (128, 16, False, 128)])
+def test_many_units_a_warp_of_ragged_sequences(d, G, rotated, page):
+    """Segments of more than 32 units, whose pages a warp looks up 32 at a time,
+    beginning anywhere in a sequence."""
+    s, q, out, lse, want = shared(900, 6000, G, d, rotated, page, 1.0, ragged=True)
+    assert not prec.faults(out, lse, *want, "fp16")
+
+
+@pytest.mark.parametrize("d,G,dtype,rotated", [(128, 4, "fp16", True), (128, 4, "bf16", True), (128, 7, "fp16", False),
+                                               (64, 1, "fp16", True), (64, 8, "bf16", False)])
+@pytest.mark.parametrize("rows", [1, 5, 300])
+def test_ordinary_batches(d, G, dtype, rotated, rows):
+    import torch
+    H = 2
+    s = Setup([(2300, rows), (700, rows), (1111, rows)], d=d, H=H, page=16, rotated=rotated)
+    q = s.tensor(H * G, dtype, scale=1.5)
+    out, lse = s.attend(q)
+    assert s.kvq.kvq_pages_read_errors() == 0
+    want, want_lse = torch.empty(q.shape, dtype=torch.float64, device="cuda"), \
+        torch.empty(q.shape[:2], dtype=torch.float64, device="cuda")
+    for i, (n, m) in enumerate(s.counts):
+        at = slice(int(s.b.start[i]), int(s.b.start[i + 1]))
+        want[at], want_lse[at] = prec.exact(q[at], *prec.stored(s, i, n), s.signs, np.arange(n - m, n), np.full(m, n))
+    assert not prec.faults(out, lse, want, want_lse, dtype)
