@@ -21,8 +21,8 @@
 // when a softmax ends one; with one S of 128 tokens a half, which the tensor
 // core fills faster, softmax and products waited for each other in turn (9000
 // cycles for 128 tokens).  Tiles of K and V go through a ring of six buffers.
-// With the reference R of a row (its largest score + the largest exponent of a
-// tile's V scales, over the tiles so far, up to 2^kSlack), p = 2^(x - R + kTileBias),
+// With the reference R of a row (its largest score + the largest exponent of the
+// V scales that it sees of a tile, over the tiles so far, up to 2^kSlack), p = 2^(x - R + kTileBias),
 //   W = fp16(p sigma_V),  O = sum W q,  l = sum p,
 // so W is the only rounding here too, and stays in fp16's range; what is below
 // its normal range is kept to 2^-31 of the largest V scale.  (V tiles of
@@ -651,13 +651,32 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                     break;
                 tc_after_sync();
                 const __half* par = sm.par[stage][0];
+                const int2 ex = *reinterpret_cast<const int2*>(sm.expo[stage]);
+                const uint2 gone = *reinterpret_cast<const uint2*>(sm.absent[stage]);
+                const bool plain = !(scaled || tok0 < see_lo || tok0 + kTileTokens > see_hi || (gone.x | gone.y));
+                int expo = max(ex.x, ex.y);  // of the largest V scale that the row sees
+                if (!plain) {
+                    // a huge one that it does not see would push the row's W below fp16's range (tokens that are not
+                    // there have 0).  A short loop ahead of the scores: among them its registers cost a prompt 9%.
+                    uint32_t most = 0;
+#pragma unroll 1
+                    for (int c = 0; c < kTileTokens; c += 8) {
+                        const uint4 sv = *reinterpret_cast<const uint4*>(&par[kTileTokens + c]);
+                        const uint32_t two[4] = {sv.x, sv.y, sv.z, sv.w};
+                        const int t = tok0 + c;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            most = max_u16x2(most, two[j] & ((t + 2 * j >= see.t0 && t + 2 * j < see.t1 ? 0xFFFFu : 0u) |
+                                                             (t + 2 * j + 1 >= see.t0 && t + 2 * j + 1 < see.t1
+                                                                  ? 0xFFFF0000u : 0u)));
+                    }
+                    expo = (int)max(max(most & 0xFFFFu, most >> 16) >> 10, 1u) - 15;
+                }
                 uint32_t s[2][32];
                 tmem_load32(s[0], ts);
                 tmem_load32(s[1], ts + 32);
-                const int2 ex = *reinterpret_cast<const int2*>(sm.expo[stage]);
-                const uint2 gone = *reinterpret_cast<const uint2*>(sm.absent[stage]);
                 tmem_wait_load();
-                if (scaled || tok0 < see_lo || tok0 + kTileTokens > see_hi || (gone.x | gone.y)) {
+                if (!plain) {
                     // scores that are not plain: scaled rows, tokens that a row does not see
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -687,8 +706,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) pages_tile_kernel(TileArgs g)
                             tops[j] = fmaxf(tops[j], fmaxf(x0, x1));
                         }
                     }
-                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a.scale2 +
-                                  (float)max(ex.x, ex.y);
+                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a.scale2 + (float)expo;
                 if (__any_sync(~0u, top > M + kSlack)) {
                     const float m2 = top > M + kSlack ? top : M, f = ex2(M - m2);  // (other rows as they were)
                     const uint64_t ff = pair2(f, f);

@@ -70,3 +70,63 @@ def test_ordinary_batches(d, G, dtype, rotated, rows):
         at = slice(int(s.b.start[i]), int(s.b.start[i + 1]))
         want[at], want_lse[at] = prec.exact(q[at], *prec.stored(s, i, n), s.signs, np.arange(n - m, n), np.full(m, n))
     assert not prec.faults(out, lse, want, want_lse, dtype)
+
+def values_of(s, mags, keep=None):
+    """New stored values of the setup's only sequence, of magnitudes mags
+    [tokens]; `keep`: tokens whose values stay."""
+    import torch
+    n = len(mags)
+    x = (s.rng.standard_normal((n, s.H, s.d)) * mags[:, None, None]).astype(np.float32)
+    c, t = ref.pack(x, s.signs)
+    for k in range(n):
+        if keep is None or k >= keep:
+            p, o = s.b.slot(0, k, s.page, s.n_pages)
+            s.codes[1][p, :, o], s.tok[1][p, :, o] = c[k], t[k]
+    s.pages.codes[1].copy_(torch.from_numpy(s.codes[1]))
+    s.pages.tok[1].copy_(torch.from_numpy(s.tok[1]))
+
+
+@pytest.mark.parametrize("rotated", [False, True])
+@pytest.mark.parametrize("silent", [1e-3, 1e-4, 1e-5])
+@pytest.mark.parametrize("d,G,window", [(128, 4, 0), (64, 8, 0), (128, 1, 20)])
+def test_loud_values_that_a_row_does_not_see(d, G, window, silent, rotated):
+    """A prompt whose first tokens of every 64 have small values and whose later
+    ones have huge ones: rows that see only small ones are as exact as rows
+    without the huge ones behind them."""
+    n = 300
+    s = Setup([(n, n)], d=d, H=1, page=16, rotated=rotated)
+    mags = np.where(np.arange(n) % 64 < 40, silent, 2e4)
+    values_of(s, mags)
+    q = s.tensor(G, "fp16")
+    quiet = {r for r in range(n) if mags[max(0, r - window + 1) if window else 0:r + 1].max() == silent}
+    assert len(quiet) >= 40
+    out, lse = s.attend(q, window=window)
+    s.check(q, out, lse, "fp16", window=window, many=True)
+    k, v = prec.stored(s, 0, n)
+    want, _ = prec.exact(q, k, v, s.signs, np.arange(n), np.full(n, n), window=window)
+    rows = sorted(quiet)
+    # the weights' rounding, the output's, and half a step of fp16's smallest numbers
+    off = (out.double() - want)[rows].square().mean(-1).sqrt()
+    assert bool((off <= prec.LIMITS["fp16"][1] * want[rows].square().mean(-1).sqrt() + 2.0 ** -25).all())
+
+
+@pytest.mark.parametrize("d,G,rotated", [(128, 4, True), (64, 8, False), (128, 1, False)])
+def test_a_row_does_not_depend_on_later_tokens(d, G, rotated):
+    """The same bits for the first rows of a prompt whatever K and V the tokens
+    behind them have."""
+    import torch
+    n, first = 300, 75
+    s = Setup([(n, n)], d=d, H=1, page=16, rotated=rotated)
+    q = s.tensor(G, "fp16")
+    got = []
+    for loud in (1.0, 1e-4, 3e4):
+        values_of(s, np.full(n, loud), keep=first)
+        for k in range(first, n):
+            p, o = s.b.slot(0, k, s.page, s.n_pages)
+            s.codes[0][p, :, o] = s.rng.integers(16, 256, (s.H, d // 2))
+            s.tok[0][p, :, o] = np.float16(loud)
+        s.pages.codes[0].copy_(torch.from_numpy(s.codes[0]))
+        s.pages.tok[0].copy_(torch.from_numpy(s.tok[0]))
+        got.append(s.attend(q))
+    for out, lse in got[1:]:
+        assert torch.equal(out[:first], got[0][0][:first]) and torch.equal(lse[:first], got[0][1][:first])
