@@ -434,7 +434,8 @@ kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, co
  * the current device: bit 1 = a kernel gave up waiting on a barrier (results
  * since the last read are void; kvq_read_device_errors covers the other
  * calls), bit 2 = a page number or token outside its range was left out.  HOST
- * call; synchronizes the device.
+ * call; waits for all that was enqueued on the device, on whatever stream.
+ * What calls of other threads set after that stays for the next read.
  * Errors: INVALID_ARG (host_out NULL); CUDA.
  */
 kvq_status kvq_pages_read_errors(uint32_t* host_out, int32_t clear);
@@ -443,7 +444,9 @@ kvq_status kvq_pages_read_errors(uint32_t* host_out, int32_t clear);
  * Read (and, if clear != 0, reset) the sticky device error word of the
  * current device: bit 0 = a kernel gave up waiting for a TMA tile, bit 1 = a
  * kernel gave up waiting on a barrier.  Kernels that give up leave the
- * results of that call undefined.  HOST call; synchronizes the device.
+ * results of that call undefined.  HOST call; waits for all that was enqueued
+ * on the device, on whatever stream.  What calls of other threads set after
+ * that stays for the next read.
  * Errors: INVALID_ARG (host_out NULL); CUDA.
  */
 kvq_status kvq_read_device_errors(uint32_t* host_out, int32_t clear);

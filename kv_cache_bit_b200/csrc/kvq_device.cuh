@@ -144,6 +144,23 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 
 __device__ __forceinline__ void report_error(uint32_t bit) { atomicOr(&g_error_word, bit); }
 
+// The error word once all that was enqueued on the current device is done (the
+// copies alone would not wait for non-blocking streams).  clear: the bits that
+// were read are taken out, on the device, so that one that another thread's
+// call sets meanwhile stays for the next read.
+static __global__ void clear_error_bits(uint32_t bits) { atomicAnd(&g_error_word, ~bits); }
+static inline bool read_error_word(uint32_t* out, bool clear) {
+    uint32_t word = 0;
+    if (cudaDeviceSynchronize() != cudaSuccess) return false;
+    if (cudaMemcpyFromSymbol(&word, g_error_word, sizeof(word)) != cudaSuccess) return false;
+    if (clear && word != 0) {
+        clear_error_bits<<<1, 1>>>(word);
+        if (cudaGetLastError() != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) return false;
+    }
+    *out = word;
+    return true;
+}
+
 // Programmatic dependent launch.  A kernel launched with programmatic stream
 // serialization may start before the kernel ahead of it in the stream has
 // finished; grid_dep_wait() returns once that kernel has completed and its

@@ -474,12 +474,7 @@ kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, co
 
 kvq_status kvq_pages_read_errors(uint32_t* host_out, int32_t clear) {
     if (host_out == nullptr) return KVQ_ERR_INVALID_ARG;
-    if (cudaMemcpyFromSymbol(host_out, g_error_word, sizeof(uint32_t)) != cudaSuccess) return KVQ_ERR_CUDA;
-    if (clear) {
-        const uint32_t zero = 0;
-        if (cudaMemcpyToSymbol(g_error_word, &zero, sizeof(uint32_t)) != cudaSuccess) return KVQ_ERR_CUDA;
-    }
-    return KVQ_OK;
+    return read_error_word(host_out, clear != 0) ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 #ifdef KVQ_WAIT_TEST
