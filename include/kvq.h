@@ -412,13 +412,15 @@ size_t kvq_pages_attention_workspace_bytes(const kvq_config* cfg, const kvq_page
  *   out   the type of q (fp16 saturates at +-65504); must not overlap q
  *   lse   fp32 [rows][q_heads], the natural logarithm of the sum of
  *         exp(scale * q . k_hat), or NULL
- * A row that sees no token (padding inside a sequence, an empty sequence)
- * gives zeros and lse -inf; rows of no sequence are left as they were.
+ * A row that sees no token gives zeros and lse -inf: one of an empty sequence,
+ * with causal also one whose own token is negative (more rows than tokens;
+ * without a mask it sees all len[s] tokens as every row does).  Rows of no
+ * sequence are left as they were.
  * Scores, softmax statistics and sums are fp32; the rotated query is kept to
  * 22 bits and a token's probability times its value scale is rounded to fp16
  * (for sequences of many rows, more than 48 query rows a kv head at head_dim
  * 128 or 80 at 64, numbers below 2^-14 of the largest to 2^-31 of the largest
- * value scale).
+ * value scale that the row sees).
  * A row's result depends on its own sequence only.  Runs of one call give the
  * same bits; other batches, hints or devices may sum in another order.
  * Errors: INVALID_ARG; WORKSPACE; UNSUPPORTED (as kvq_pages_write; rows *
