@@ -376,7 +376,7 @@ typedef struct {
  * (other slots are not affected).
  * rows == 0 or n_seqs == 0 enqueue nothing.
  * Errors: INVALID_ARG; UNSUPPORTED (flags, bits, head_dim, page_tokens,
- * dtype, sizes past the limits above, rows * kv_heads >= 2^31); CUDA.
+ * dtype, sizes past the limits above, rows * kv_heads >= 2^29); CUDA.
  */
 kvq_status kvq_pages_write(const kvq_config* cfg, const kvq_pages* pages, const kvq_batch* batch,
                            const kvq_rows* k, const kvq_rows* v, int64_t rows, void* stream);
@@ -423,8 +423,9 @@ size_t kvq_pages_attention_workspace_bytes(const kvq_config* cfg, const kvq_page
  * value scale that the row sees).
  * A row's result depends on its own sequence only.  Runs of one call give the
  * same bits; other batches, hints or devices may sum in another order.
- * Errors: INVALID_ARG; WORKSPACE; UNSUPPORTED (as kvq_pages_write; rows *
- * q_heads >= 2^31; n_seqs * q_heads >= 2^31 / 80; q_heads / kv_heads > 256); CUDA.
+ * Errors: INVALID_ARG; WORKSPACE; UNSUPPORTED (flags, bits, head_dim,
+ * page_tokens, dtype, sizes past the limits above; rows * q_heads >= 2^31;
+ * 80 * n_seqs * q_heads >= 2^31; q_heads > 65535; q_heads / kv_heads > 256); CUDA.
  */
 kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, const kvq_batch* batch,
                                const kvq_rows* q, int32_t q_heads, int64_t rows, float scale, int32_t causal,

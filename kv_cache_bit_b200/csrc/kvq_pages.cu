@@ -20,6 +20,7 @@ namespace kvq {
 namespace {
 
 constexpr int64_t kMaxIndex = int64_t(1) << 31;
+constexpr int64_t kMaxVectors = int64_t(1) << 29;  // rows x heads of a write or read: lanes, four each, are counted in 32 bits
 constexpr int kMaxGroup = 256;  // query heads per kv head
 // Sequences of more query rows a kv head than this go to the tile kernel.  The generation-step kernel reads the
 // cache once for 16 rows (28 query heads over 4 kv heads, 16 x 300 .. 3001 tokens, D = 128: 48 us at 35 rows, 62
@@ -33,6 +34,9 @@ struct NvtxRange {
     NvtxRange(const NvtxRange&) = delete;
     NvtxRange& operator=(const NvtxRange&) = delete;
 };
+
+// a * b >= limit, for a, b >= 0 and b < 2^31.
+bool reaches(int64_t a, int64_t b, int64_t limit) { return a >= kMaxIndex || a * b >= limit; }
 
 bool ok_ptr(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool ok_ints(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -321,8 +325,8 @@ kvq_status check_attention(const kvq_config* cfg, const kvq_pages* p, const kvq_
     const kvq_status s = check_paged(cfg, p, b, rows);
     if (s != KVQ_OK) return s;
     if (q_heads < p->kv_heads || q_heads % p->kv_heads != 0) return KVQ_ERR_INVALID_ARG;
-    if (q_heads / p->kv_heads > kMaxGroup || q_heads > 65535 || rows >= kMaxIndex / q_heads ||
-        b->n_seqs >= kMaxIndex / (kManyMost * (int64_t)q_heads))  // prepared queries are counted in 32 bits
+    if (q_heads / p->kv_heads > kMaxGroup || q_heads > 65535 || reaches(rows, q_heads, kMaxIndex) ||
+        reaches(b->n_seqs, kManyMost * (int64_t)q_heads, kMaxIndex))  // prepared queries are counted in 32 bits
         return KVQ_ERR_UNSUPPORTED;
     return KVQ_OK;
 }
@@ -340,7 +344,7 @@ kvq_status kvq_pages_write(const kvq_config* cfg, const kvq_pages* pages, const 
     kvq_status s = check_paged(cfg, pages, batch, rows);
     if (s != KVQ_OK) return s;
     const int H = pages->kv_heads, d = cfg->head_dim;
-    if (rows >= kMaxIndex / H / 4) return KVQ_ERR_UNSUPPORTED;  // lanes are counted in 32 bits
+    if (reaches(rows, H, kMaxVectors)) return KVQ_ERR_UNSUPPORTED;
     if ((s = check_rows(k, rows, H, d, false, false)) != KVQ_OK) return s;
     if ((s = check_rows(v, rows, H, d, false, false)) != KVQ_OK) return s;
     if (k->dtype != v->dtype) return KVQ_ERR_INVALID_ARG;
@@ -369,7 +373,7 @@ kvq_status kvq_pages_read(const kvq_config* cfg, const kvq_pages* pages, const k
     kvq_status s = check_paged(cfg, pages, batch, rows);
     if (s != KVQ_OK) return s;
     const int H = pages->kv_heads, d = cfg->head_dim;
-    if (rows >= kMaxIndex / H / 4) return KVQ_ERR_UNSUPPORTED;
+    if (reaches(rows, H, kMaxVectors)) return KVQ_ERR_UNSUPPORTED;
     if (k_out == nullptr && v_out == nullptr) return KVQ_ERR_INVALID_ARG;
     const kvq_rows* x[2] = {k_out, v_out};
     for (int i = 0; i < 2; ++i)

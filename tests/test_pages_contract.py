@@ -1,8 +1,11 @@
 """Paged cache: what the sources and the host checks have to keep to (CPU only;
 every library call made here with placeholder addresses fails a host check or
 has nothing to do)."""
+import ctypes
 import os
 import re
+
+import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "kv_cache_bit_b200", "csrc")
 
@@ -19,3 +22,56 @@ def test_register_split_is_one_instruction_a_warpgroup():
                       r"\s*else asm volatile\(\"setmaxnreg\.dec[^;]*;\" ::\"n\"\(kProducerRegs\)\);\s*\}", text)
     assert split and int(split.group(1)) % 4 == 0
     assert split.end() < text.index("warp >= 14")
+
+
+A = 1 << 20  # placeholder address, 16-byte aligned, never dereferenced
+P2 = ctypes.c_void_p * 2
+
+
+@pytest.fixture(scope="module")
+def kvq():
+    from kv_cache_bit_b200 import build
+    build.build()
+    from kv_cache_bit_b200 import kvq as mod
+    return mod
+
+
+class Call:
+    """Arguments of the paged calls: with `n_seqs` 0 write and read pass all
+    checks and do nothing, attention without a workspace ends at that check."""
+
+    def __init__(self, kvq, d=128, heads=2, page=16, pages=4, n_seqs=0):
+        self.kvq, self.L, self.heads = kvq, kvq.lib, heads
+        self.cfg = kvq.kvq_config(d, 4, 0, 0, None)
+        self.pool = kvq.kvq_pages(10, heads, d, page, P2(A, A), P2(A, A))
+        self.batch = kvq.kvq_batch(n_seqs, pages, pages, 0, A, A, A)
+
+    def x(self, rs, hs, data=A, dt=0):
+        return self.kvq.kvq_rows(data, rs, hs, dt, 0)
+
+    def write(self, k, v, rows):
+        return self.L.kvq_pages_write(self.cfg, self.pool, self.batch, k, v, rows, None)
+
+    def read(self, k, v, rows):
+        return self.L.kvq_pages_read(self.cfg, self.pool, self.batch, k, v, rows, None)
+
+    def attend(self, q, out, rows, heads=None):
+        return self.L.kvq_pages_attention(self.cfg, self.pool, self.batch, q, heads or self.heads, rows, 0.0, 1, 0,
+                                          out, None, None, 0, None)
+
+
+@pytest.mark.parametrize("heads", [1, 3, 8, 28])
+def test_row_limits_are_the_documented_ones(kvq, heads):
+    """rows * kv_heads < 2^29 of a write and a read, rows * q_heads < 2^31 and
+    80 * n_seqs * q_heads < 2^31 of an attention call; both sides of each."""
+    OK, UNS, WS = kvq.KVQ_OK, kvq.KVQ_ERR_UNSUPPORTED, kvq.KVQ_ERR_WORKSPACE
+    c = Call(kvq, heads=heads)
+    x, y = c.x(heads * 128, 128), c.x(heads * 128, 128, data=A + (1 << 44))
+    last = (2 ** 29 - 1) // heads
+    assert (c.write(x, y, last), c.write(x, y, last + 1)) == (OK, UNS)
+    assert (c.read(x, y, last), c.read(x, y, last + 1)) == (OK, UNS)
+    last = (2 ** 31 - 1) // heads
+    assert (c.attend(x, y, last), c.attend(x, y, last + 1)) == (OK, UNS)
+    last = (2 ** 31 - 1) // (80 * heads)
+    assert (Call(kvq, heads=heads, n_seqs=last).attend(x, y, 8), Call(kvq, heads=heads, n_seqs=last + 1).attend(x, y, 8)) == (WS, UNS)
+    assert c.write(x, y, 1 << 62) == UNS and c.attend(x, y, 1 << 62) == UNS
