@@ -359,7 +359,8 @@ enum { KVQ_F16 = 0, KVQ_BF16 = 1, KVQ_F32 = 2 };
  * data + r * row_stride + h * head_stride + c, strides in elements (so K, V
  * and queries may be slices of one fused projection).  data is 16-byte
  * aligned and the strides are multiples of 16 bytes; a stride may be 0 or
- * negative in an input, not in an output.
+ * negative in an input, not in an output.  From the first to the last element
+ * are at most 2^42 bytes (INVALID_ARG past that).
  */
 typedef struct {
     void* data;

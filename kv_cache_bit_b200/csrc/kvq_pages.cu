@@ -65,6 +65,10 @@ kvq_status check_paged(const kvq_config* cfg, const kvq_pages* p, const kvq_batc
     return KVQ_OK;
 }
 
+// From the first to the last element of a rows tensor at most: far above what
+// a GPU holds, and sums of its offsets are far from 64 bits.
+constexpr int64_t kMaxExtent = int64_t(1) << 42;
+
 // A rows tensor; strides of dimensions of one element are not looked at.
 kvq_status check_rows(const kvq_rows* x, int64_t rows, int heads, int d, bool output, bool f32) {
     if (x == nullptr || !ok_ptr(x->data) || x->reserved != 0) return KVQ_ERR_INVALID_ARG;
@@ -72,8 +76,10 @@ kvq_status check_rows(const kvq_rows* x, int64_t rows, int heads, int d, bool ou
     const int64_t unit = x->dtype == KVQ_F32 ? 4 : 8;  // elements of 16 bytes
     const int64_t rs = rows > 1 ? x->row_stride : 0, hs = heads > 1 ? x->head_stride : 0;
     if (rs % unit != 0 || hs % unit != 0) return KVQ_ERR_INVALID_ARG;
-    if (rs > (INT64_MAX >> 36) || rs < -(INT64_MAX >> 36) || hs > (INT64_MAX >> 36) || hs < -(INT64_MAX >> 36))
-        return KVQ_ERR_INVALID_ARG;
+    const int64_t most = kMaxExtent / (x->dtype == KVQ_F32 ? 4 : 2);  // elements
+    if (rs > most || rs < -most || hs > most || hs < -most) return KVQ_ERR_INVALID_ARG;
+    const __int128 span = (__int128)(rs < 0 ? -rs : rs) * (rows - 1) + (__int128)(hs < 0 ? -hs : hs) * (heads - 1) + d;
+    if (rows > 0 && span > most) return KVQ_ERR_INVALID_ARG;
     if (output) {  // no two elements in one place: rows inside heads or heads inside rows
         if ((rows > 1 && rs < d) || (heads > 1 && hs < d)) return KVQ_ERR_INVALID_ARG;
         if (rows > 1 && heads > 1 && rs < (heads - 1) * hs + d && hs < (rows - 1) * rs + d) return KVQ_ERR_INVALID_ARG;

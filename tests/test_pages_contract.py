@@ -75,3 +75,20 @@ def test_row_limits_are_the_documented_ones(kvq, heads):
     last = (2 ** 31 - 1) // (80 * heads)
     assert (Call(kvq, heads=heads, n_seqs=last).attend(x, y, 8), Call(kvq, heads=heads, n_seqs=last + 1).attend(x, y, 8)) == (WS, UNS)
     assert c.write(x, y, 1 << 62) == UNS and c.attend(x, y, 1 << 62) == UNS
+
+
+def test_strides_are_limited_by_where_they_reach(kvq):
+    """A head-major tensor of 2^20 rows and more is an ordinary one; from 2^42
+    bytes between its first and its last element on a tensor is refused."""
+    OK, INV = kvq.KVQ_OK, kvq.KVQ_ERR_INVALID_ARG
+    c = Call(kvq, heads=8)
+    for rows in (1 << 20, (1 << 20) + 1, 1 << 25):
+        x, y = c.x(128, rows * 128), c.x(128, rows * 128, data=A + (1 << 44))
+        assert (c.write(x, y, rows), c.read(x, y, rows), c.attend(x, y, rows)) == (OK, OK, OK), rows
+    most = 1 << 41  # elements of 2 bytes
+    for rs, hs, rows, over in (((most - 128) // 8, 0, 9, 0), ((most - 128 + 64) // 8, 0, 9, 1), (0, (most - 128) // 56 * 8, 5, 0),
+                               (0, (most - 128) // 56 * 8 + 8, 5, 1), (-((most - 128) // 8), 0, 9, 0), (1 << 62, 0, 2, 1),
+                               (-(1 << 62), 0, 2, 1), (0, 1 << 62, 2, 1), (1 << 40, 0, (1 << 29) // 8 - 1, 1),
+                               (1 << 62, 128, 1, 0), (most // 2, most // 14 // 8 * 8, 2, 1)):
+        x = c.x(rs // 8 * 8, hs)
+        assert c.write(x, x, rows) == (INV if over else OK), (rs, hs, rows)
