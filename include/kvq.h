@@ -332,7 +332,7 @@ typedef struct {
  *   len   int32 [n_seqs]      tokens of sequence s, those rows included
  *   table int32 [n_seqs][table_stride], of each row the first max_pages are
  *         used: token t of sequence s is slot t % page_tokens of page
- *         table[s][t / page_tokens]
+ *         table[s][t / page_tokens]; max_pages * page_tokens <= 2^31 - 256
  * Row start[s] + i is thus token len[s] - (start[s+1] - start[s]) + i.  Rows
  * whose token is negative (more rows than tokens) are padding, and so are
  * rows before start[0], from start[n_seqs] on, and past the call's `rows`.

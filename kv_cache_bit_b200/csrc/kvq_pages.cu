@@ -60,7 +60,8 @@ kvq_status check_paged(const kvq_config* cfg, const kvq_pages* p, const kvq_batc
     if (b->n_seqs > 0) {
         if (b->max_pages < 1 || b->table_stride < b->max_pages) return KVQ_ERR_INVALID_ARG;
         if (!ok_ints(b->start) || !ok_ints(b->len) || !ok_ints(b->table)) return KVQ_ERR_INVALID_ARG;
-        if ((int64_t)b->max_pages * t >= kMaxIndex) return KVQ_ERR_UNSUPPORTED;
+        // tokens are rounded up to units of 64 in 32 bits
+        if ((int64_t)b->max_pages * t > kMaxIndex - 256) return KVQ_ERR_UNSUPPORTED;
     }
     return KVQ_OK;
 }

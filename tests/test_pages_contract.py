@@ -92,3 +92,18 @@ def test_strides_are_limited_by_where_they_reach(kvq):
                                (1 << 62, 128, 1, 0), (most // 2, most // 14 // 8 * 8, 2, 1)):
         x = c.x(rs // 8 * 8, hs)
         assert c.write(x, x, rows) == (INV if over else OK), (rs, hs, rows)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_a_table_leaves_room_to_round_its_last_token_up(kvq, page):
+    """Tokens are counted in 32 bits and rounded up to whole units of 32 or 64:
+    a table may not reach the last of them."""
+    UNS, WS = kvq.KVQ_ERR_UNSUPPORTED, kvq.KVQ_ERR_WORKSPACE
+    most = (2 ** 31 - 256) // page
+    for pages, want in ((most, WS), (most + 1, UNS), ((2 ** 31 - 1) // page, UNS)):
+        c = Call(kvq, page=page, pages=pages, n_seqs=2)
+        x, y = c.x(256, 128), c.x(256, 128, data=A + (1 << 30))
+        assert c.attend(x, y, 8) == want, pages
+        if want == UNS:
+            assert c.write(x, y, 8) == UNS and c.read(x, y, 8) == UNS
+    assert (most * page + 63) < 2 ** 31
