@@ -410,7 +410,9 @@ size_t kvq_pages_attention_workspace_bytes(const kvq_config* cfg, const kvq_page
  * `window` of these.  The rows' own tokens are written before (kvq_pages_write).
  *   q     fp16 or bf16, `rows` rows of q_heads heads, q_heads a multiple of kv_heads
  *   scale softmax scale; <= 0 selects 1/sqrt(head_dim)
- *   out   the type of q (fp16 saturates at +-65504); must not overlap q
+ *   out   the type of q (fp16 saturates at +-65504); must not overlap q (other
+ *         slices of one buffer may interleave with it if their strides are
+ *         equal; of tensors of different strides the address ranges may not)
  *   lse   fp32 [rows][q_heads], the natural logarithm of the sum of
  *         exp(scale * q . k_hat), or NULL
  * A row that sees no token gives zeros and lse -inf: one of an empty sequence,

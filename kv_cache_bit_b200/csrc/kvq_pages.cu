@@ -97,6 +97,32 @@ void extent(const kvq_rows* x, int64_t rows, int heads, int d, intptr_t* lo, int
     *hi = at + size * ((r > 0 ? r : 0) + (h > 0 ? h : 0) + d);
 }
 
+// Whether queries x and outputs y share an element.  Slices of one buffer (of
+// the same strides) are looked at element by element, others by their extents.
+bool overlap(const kvq_rows* x, const kvq_rows* y, int64_t rows, int heads, int d) {
+    intptr_t xl, xh, yl, yh;
+    extent(x, rows, heads, d, &xl, &xh);
+    extent(y, rows, heads, d, &yl, &yh);
+    if (xl >= yh || yl >= xh) return false;
+    const int64_t rs = rows > 1 ? y->row_stride : 0, hs = heads > 1 ? y->head_stride : 0;  // of an output: positive
+    if ((rows > 1 && x->row_stride != rs) || (heads > 1 && x->head_stride != hs)) return true;
+    // vectors u rows and w heads apart share one iff |at + u rs| < d
+    const int64_t size = x->dtype == KVQ_F32 ? 4 : 2;
+    const int64_t delta = (reinterpret_cast<intptr_t>(y->data) - reinterpret_cast<intptr_t>(x->data)) / size;
+    for (int64_t w = 1 - (int64_t)heads; w < heads; ++w) {
+        const int64_t at = delta + w * hs;
+        int64_t u = 0, rest = at;  // rest = at + u rs, the last below rs
+        if (rs > 0) {
+            u = -(at / rs);
+            rest = at % rs;
+            if (rest < 0) rest += rs, ++u;
+        }
+        const auto hit = [&](int64_t n, int64_t v) { return n > -rows && n < rows && v < d && v > -d; };
+        if (hit(u, rest) || (rs > 0 && hit(u - 1, rest - rs))) return true;
+    }
+    return false;
+}
+
 Batch batch_of(const kvq_batch* b) {
     return Batch{b->start, b->len, b->table, b->n_seqs, b->max_pages, b->table_stride};
 }
@@ -430,10 +456,7 @@ kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, co
     if (lse != nullptr && !ok_ints(lse)) return KVQ_ERR_INVALID_ARG;
     if (!(scale <= 2.0e38f)) return KVQ_ERR_INVALID_ARG;  // infinite or NaN, or times log2 e infinite
     if (rows == 0 || batch->n_seqs == 0) return KVQ_OK;
-    intptr_t ql, qh, ol, oh;
-    extent(q, rows, q_heads, d, &ql, &qh);
-    extent(out, rows, q_heads, d, &ol, &oh);
-    if (ql < oh && ol < qh) return KVQ_ERR_INVALID_ARG;
+    if (overlap(q, out, rows, q_heads, d)) return KVQ_ERR_INVALID_ARG;
     const size_t need = kvq_pages_attention_workspace_bytes(cfg, pages, batch, rows, q_heads);
     if (!ok_ptr(ws) || ws_bytes < need) return KVQ_ERR_WORKSPACE;
     const int sms = sm_count();

@@ -107,3 +107,28 @@ def test_a_table_leaves_room_to_round_its_last_token_up(kvq, page):
         if want == UNS:
             assert c.write(x, y, 8) == UNS and c.read(x, y, 8) == UNS
     assert (most * page + 63) < 2 ** 31
+
+
+def test_queries_and_outputs_may_be_slices_of_one_buffer(kvq):
+    """Refused are outputs that share an element with the queries, by counting
+    all elements of small tensors; interleaved slices are not."""
+    INV, WS = kvq.KVQ_ERR_INVALID_ARG, kvq.KVQ_ERR_WORKSPACE
+    d, seen = 64, set()
+    for heads in (1, 2, 3):
+        c = Call(kvq, d=d, heads=heads, n_seqs=2)
+        for rows in (1, 2, 4):
+            wide = heads * d
+            for rs, hs in ((wide, d), (2 * wide, d), (2 * wide, 2 * d), (2 * wide + 64, d), (d, rows * d), (2 * d, 2 * rows * d),
+                           (d, 2 * rows * d), (3 * wide, 3 * d)):
+                for off in [8 * k * s for k in (1, 3, 7, 8, 9, 16, 24, 40) for s in (1, -1)] + [wide, -wide, rows * d, 2 * wide + 56]:
+                    if off % 8:
+                        continue
+                    other = {r * rs + h * hs + off + e for r in range(rows) for h in range(heads) for e in range(0, d, 8)}
+                    full = {r * rs + h * hs + e for r in range(rows) for h in range(heads) for e in range(0, d, 8)}
+                    got = c.attend(c.x(rs, hs), c.x(rs, hs, data=A + 2 * off), rows)
+                    assert got == (INV if other & full else WS), (heads, rows, rs, hs, off)
+                    seen.add((got, rows > 1 and heads > 1))
+    assert len(seen) == 4
+    c = Call(kvq, d=d, heads=2, n_seqs=2)
+    assert c.attend(c.x(128, 64), c.x(256, 64, data=A + 128), 8) == INV   # other strides: by extent
+    assert c.attend(c.x(0, 64), c.x(128, 64, data=A + (1 << 20)), 8) == WS
