@@ -385,7 +385,8 @@ kvq_status kvq_pages_write(const kvq_config* cfg, const kvq_pages* pages, const 
 /*
  * Rebuild the rows' K and V from the cache: sigma q, or R^T (sigma q) under
  * KVQ_HADAMARD, in fp32, rounded once to the output's type (fp16 saturates at
- * +-65504).  k_out or v_out may be NULL.  Rows start[s] .. are the sequence's
+ * +-65504).  k_out or v_out may be NULL; they must not share an element (of
+ * equal strides that is checked).  Rows start[s] .. are the sequence's
  * last tokens, so start = the running sum of len reads whole sequences, and a
  * smaller len ends the range earlier.  Rows whose token is negative, or whose page is
  * refused, become zeros; rows before start[0] and from start[n_seqs] on are left as they were.

@@ -97,15 +97,16 @@ void extent(const kvq_rows* x, int64_t rows, int heads, int d, intptr_t* lo, int
     *hi = at + size * ((r > 0 ? r : 0) + (h > 0 ? h : 0) + d);
 }
 
-// Whether queries x and outputs y share an element.  Slices of one buffer (of
-// the same strides) are looked at element by element, others by their extents.
-bool overlap(const kvq_rows* x, const kvq_rows* y, int64_t rows, int heads, int d) {
+// Whether x and outputs y share an element.  Slices of one buffer (of the same
+// strides) are looked at element by element; what others are taken for, where
+// their extents meet, is the caller's choice.
+bool overlap(const kvq_rows* x, const kvq_rows* y, int64_t rows, int heads, int d, bool others) {
     intptr_t xl, xh, yl, yh;
     extent(x, rows, heads, d, &xl, &xh);
     extent(y, rows, heads, d, &yl, &yh);
     if (xl >= yh || yl >= xh) return false;
     const int64_t rs = rows > 1 ? y->row_stride : 0, hs = heads > 1 ? y->head_stride : 0;  // of an output: positive
-    if ((rows > 1 && x->row_stride != rs) || (heads > 1 && x->head_stride != hs)) return true;
+    if ((rows > 1 && x->row_stride != rs) || (heads > 1 && x->head_stride != hs)) return others;
     // vectors u rows and w heads apart share one iff |at + u rs| < d
     const int64_t size = x->dtype == KVQ_F32 ? 4 : 2;
     const int64_t delta = (reinterpret_cast<intptr_t>(y->data) - reinterpret_cast<intptr_t>(x->data)) / size;
@@ -414,6 +415,7 @@ kvq_status kvq_pages_read(const kvq_config* cfg, const kvq_pages* pages, const k
     if (k_out != nullptr && v_out != nullptr && (k_out->dtype != v_out->dtype || k_out->data == v_out->data))
         return KVQ_ERR_INVALID_ARG;
     if (rows == 0 || batch->n_seqs == 0) return KVQ_OK;
+    if (k_out != nullptr && v_out != nullptr && overlap(k_out, v_out, rows, H, d, false)) return KVQ_ERR_INVALID_ARG;
     ReadLaunch L;
     L.a.b = batch_of(batch);
     L.a.p = pool_of(pages);
@@ -456,7 +458,7 @@ kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, co
     if (lse != nullptr && !ok_ints(lse)) return KVQ_ERR_INVALID_ARG;
     if (!(scale <= 2.0e38f)) return KVQ_ERR_INVALID_ARG;  // infinite or NaN, or times log2 e infinite
     if (rows == 0 || batch->n_seqs == 0) return KVQ_OK;
-    if (overlap(q, out, rows, q_heads, d)) return KVQ_ERR_INVALID_ARG;
+    if (overlap(q, out, rows, q_heads, d, true)) return KVQ_ERR_INVALID_ARG;
     const size_t need = kvq_pages_attention_workspace_bytes(cfg, pages, batch, rows, q_heads);
     if (!ok_ptr(ws) || ws_bytes < need) return KVQ_ERR_WORKSPACE;
     const int sms = sm_count();

@@ -132,3 +132,12 @@ def test_queries_and_outputs_may_be_slices_of_one_buffer(kvq):
     c = Call(kvq, d=d, heads=2, n_seqs=2)
     assert c.attend(c.x(128, 64), c.x(256, 64, data=A + 128), 8) == INV   # other strides: by extent
     assert c.attend(c.x(0, 64), c.x(128, 64, data=A + (1 << 20)), 8) == WS
+
+
+def test_read_outputs_that_share_elements_are_refused(kvq):
+    """A K output that begins inside the V output: what it holds afterwards
+    would be a race."""
+    INV = kvq.KVQ_ERR_INVALID_ARG
+    c = Call(kvq, d=64, heads=2, n_seqs=2)
+    for rs, hs, off in ((128, 64, 64), (128, 64, -8 * 64), (256, 64, 64), (256, 128, 128), (64, 8 * 64, 8 * 64 - 64)):
+        assert c.read(c.x(rs, hs), c.x(rs, hs, data=A + 2 * off), 8) == INV, (rs, hs, off)
