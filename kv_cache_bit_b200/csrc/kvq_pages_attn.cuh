@@ -71,11 +71,6 @@ __device__ __forceinline__ float lg2(float x) {
     return r;
 }
 
-__device__ __forceinline__ float load16(const void* p, long long at, int bf16) {
-    const uint16_t u = static_cast<const uint16_t*>(p)[at];
-    return bf16 ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
-}
-
 // 2^k with k such that m 2^k is in [2^14, 2^15); for infinite or NaN m, NaN
 // (the row's result is then NaN whatever its codes are).
 __device__ __forceinline__ float query_scale(float m) {
