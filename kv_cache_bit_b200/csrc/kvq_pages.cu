@@ -142,11 +142,28 @@ Pool pool_of(const kvq_pages* p) {
 
 float rsqd_of(int d) { return (float)(1.0 / std::sqrt((double)d)); }
 
+// SMs of the current device.
+int sm_count() {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        cudaGetLastError();
+        return 148;
+    }
+    if ((n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        return 148;
+    }
+    known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 // Heads of a row that a quad of lanes takes in turn: one while that leaves quads for every SM's schedulers
 // (a generation step), eight at most.
 int heads_a_quad(int64_t rows, int H) {
     int per = 1;
-    while (per < 8 && per * 2 <= H && rows * H >= (int64_t)per * 2 * 148 * 128) per *= 2;
+    while (per < 8 && per * 2 <= H && rows * H >= (int64_t)per * 2 * sm_count() * 128) per *= 2;
     return per;
 }
 
@@ -228,23 +245,6 @@ bool allow_smem(int bytes, int regs = 0) {
     }
     done.fetch_or(bit, std::memory_order_release);
     return true;
-}
-
-// SMs of the current device.
-int sm_count() {
-    static std::atomic<int> known[64];
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
-        cudaGetLastError();
-        return 148;
-    }
-    if ((n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
-        cudaGetLastError();
-        return 148;
-    }
-    known[dev].store(n, std::memory_order_relaxed);
-    return n;
 }
 
 // Generation-step kernel: CTAs of a single wave, and query rows an item.
