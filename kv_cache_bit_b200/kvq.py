@@ -267,6 +267,8 @@ def _on(pages: "PagedCache", stream, call: str, fn, *args):
     """fn(*args, stream) with the cache's device current; stream None: the
     current stream of that device."""
     global _torch
+    if pages.device.type != "cuda":
+        raise KvqError(KVQ_ERR_INVALID_ARG, call + ": a cache on a GPU")
     if _torch is None:
         import torch
         torch.cuda.init()
@@ -291,7 +293,7 @@ def kvq_pages_write(cfg: "Config", pages: "PagedCache", batch: "Batch", k, v, st
     head strides of whole 16 bytes) into their slots; see include/kvq.h."""
     name = "kvq_pages_write"
     rows = _paged(name, cfg, pages, batch, (k, pages.c.kv_heads), (v, pages.c.kv_heads))
-    _on(pages, stream, name, lib.kvq_pages_write, cfg.c, pages.c, batch.c, _rows(k, name), _rows(v, name), rows)
+    _on(pages, stream, name, lib.kvq_pages_write, cfg.c, pages.c, batch.c, _rows(k, name), _rows(v, name), rows or 0)
 
 
 def kvq_pages_read(cfg: "Config", pages: "PagedCache", batch: "Batch", k_out, v_out, stream=None):
@@ -316,6 +318,8 @@ def kvq_pages_attention(cfg: "Config", pages: "PagedCache", batch: "Batch", q, o
     into out (q's type and shape) and, if given, lse fp32 [rows, q_heads].
     ws: uint8 tensor of kvq_pages_attention_workspace_bytes()."""
     name = "kvq_pages_attention"
+    if q is None or out is None:
+        raise KvqError(KVQ_ERR_INVALID_ARG, name + ": q and out")
     rows = _paged(name, cfg, pages, batch, (q, 0), (out, 0))
     heads = q.shape[1]
     if out.shape[1] != heads or ws is None or ws.device != pages.device or not ws.is_contiguous():

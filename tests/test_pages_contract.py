@@ -141,3 +141,20 @@ def test_read_outputs_that_share_elements_are_refused(kvq):
     c = Call(kvq, d=64, heads=2, n_seqs=2)
     for rs, hs, off in ((128, 64, 64), (128, 64, -8 * 64), (256, 64, 64), (256, 128, 128), (64, 8 * 64, 8 * 64 - 64)):
         assert c.read(c.x(rs, hs), c.x(rs, hs, data=A + 2 * off), 8) == INV, (rs, hs, off)
+
+
+def test_binding_refuses_missing_tensors_and_caches_on_the_host(kvq):
+    import torch
+    c = kvq.Config(64, 4, 0, None, device="cpu")
+    p = kvq.PagedCache.allocate(c, 5, 2, 32, device="cpu")
+    i = lambda *x: torch.zeros(x, dtype=torch.int32)  # noqa: E731
+    b = kvq.Batch(i(3), i(2), i(2, 4))
+    x, ws = torch.zeros(6, 2, 64, dtype=torch.float16), torch.zeros(64, dtype=torch.uint8)
+    for call in (lambda: kvq.kvq_pages_write(c, p, b, None, None), lambda: kvq.kvq_pages_write(c, p, b, x, None),
+                 lambda: kvq.kvq_pages_read(c, p, b, None, None), lambda: kvq.kvq_pages_attention(c, p, b, None, x, ws=ws),
+                 lambda: kvq.kvq_pages_attention(c, p, b, x, None, ws=ws), lambda: kvq.kvq_pages_write(c, p, b, x, x),
+                 lambda: kvq.kvq_pages_read(c, p, b, x, None),
+                 lambda: kvq.kvq_pages_attention(c, p, b, x, x.clone(), ws=ws)):
+        with pytest.raises(kvq.KvqError) as e:
+            call()
+        assert e.value.status == kvq.KVQ_ERR_INVALID_ARG
