@@ -422,9 +422,8 @@ size_t kvq_pages_attention_workspace_bytes(const kvq_config* cfg, const kvq_page
  * sequence are left as they were.
  * Scores, softmax statistics and sums are fp32; the rotated query is kept to
  * 22 bits and a token's probability times its value scale is rounded to fp16
- * (for sequences of many rows, more than 48 query rows a kv head at head_dim
- * 128 or 80 at 64, numbers below 2^-14 of the largest to 2^-31 of the largest
- * value scale that the row sees).
+ * (for sequences of more than 32 query rows a kv head, numbers below 2^-14 of
+ * the largest to 2^-31 of the largest value scale that the row sees).
  * A row's result depends on its own sequence only.  Runs of one call give the
  * same bits; other batches, hints or devices may sum in another order.
  * Errors: INVALID_ARG; WORKSPACE; UNSUPPORTED (flags, bits, head_dim,

@@ -22,11 +22,17 @@ namespace {
 constexpr int64_t kMaxIndex = int64_t(1) << 31;
 constexpr int64_t kMaxVectors = int64_t(1) << 29;  // rows x heads of a write or read: lanes, four each, are counted in 32 bits
 constexpr int kMaxGroup = 256;  // query heads per kv head
-// Sequences of more query rows a kv head than this go to the tile kernel.  The generation-step kernel reads the
-// cache once for 16 rows (28 query heads over 4 kv heads, 16 x 300 .. 3001 tokens, D = 128: 48 us at 35 rows, 62
-// at 63, 99 at 98; 32 over 8, D = 64: 44, 65 and 90), the tile kernel once for 256 (57, 58, 60; 78, 79, 78).
-constexpr int many_rows(int d) { return d == 128 ? 48 : 80; }
-constexpr int kManyMost = 80;
+// Which of the two kernels a sequence goes to, by its query rows a kv head.  The generation-step kernel reads the
+// cache once for 16 of them at most (four or eight where the call's single rows ask for no more), the tile kernel
+// once for 256, with half the multiprocessor idle below 129.
+//   A call whose sequences all have up to kFewRows is the step kernel's alone.  Step and tile kernel, us, at about
+//   64, 80 and 112 rows, rotated, 16 x 300 .. 3001 tokens: 28 over 4 heads, D = 128: 48 62, 64 62, 83 63; 32 over 32:
+//   302 394, 370 388, 504 386; 32 over 8, D = 64: 72 82, 78 82, 102 83; 64 x 500 .. 4000, 32 over 8, D = 64: 234 300,
+//   291 301, 394 301.
+//   Beside sequences of more, and where the host does not know, those of up to kFewBeside: two of 500 rows and 14 of
+//   24, 32 and 48 rows, 600 .. 3001 tokens, D = 128, 32 over 8: 140 144, 151 145, 174 147; of 32 x 2000 .. 4000 four and
+//   28 of these: 332 369, 367 370, 438 369; D = 64: 264 325, 287 323, 336 325.
+constexpr int kFewRows = 80, kFewBeside = 32;
 
 struct NvtxRange {
     explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
@@ -255,16 +261,16 @@ struct StepShape {
 
 // Which kernels a call needs, from what the host knows of it.
 struct AttnPlan {
-    bool tiles;        // some sequence may have more than many_rows() query rows a kv head
-    int stretch;       // with tiles: rows of a sequence that has not
+    bool tiles;        // some sequence may have more than kFewRows query rows a kv head
+    int stretch;       // with tiles: rows of a sequence of up to kFewBeside
     long long places;  // rows that the step kernel's queries are prepared for
     long long queries; // query rows a kv head of the sequences that are the step kernel's
 };
-AttnPlan attn_plan(const kvq_batch* b, long long rows, int G, int d) {
+AttnPlan attn_plan(const kvq_batch* b, long long rows, int G) {
     AttnPlan p;
     const long long most = (long long)G * b->max_rows;
-    p.tiles = b->max_rows == 0 || most > many_rows(d);
-    p.stretch = p.tiles ? many_rows(d) / G : 0;
+    p.tiles = b->max_rows == 0 || most > kFewRows;
+    p.stretch = p.tiles ? kFewBeside / G : 0;
     p.places = p.tiles ? (long long)b->n_seqs * p.stretch : rows;
     p.queries = p.tiles ? G : most;
     return p;
@@ -309,8 +315,9 @@ AttnWorkspace attn_workspace(const AttnPlan& p, int sms, int d, bool had, int q_
 }
 
 // Caches of up to this many tokens (by the table's width) are taken whole where there is a CTA for every item.
-// In ranges with a merge, and whole, us: 1 sequence of 256 tokens, 8 heads, D = 64: 9.9 and 7.9; 4 of 256, 32
-// over 8 heads, D = 128: 11.6 and 9.2; 8 of 100 .. 512: 12.4 and 11.2; 1 of 512, 28 over 4 heads: 12.6 and 13.0.
+// In ranges with a merge, and whole, us, at tables of 256, 512 and 768 tokens: 1 sequence, 8 heads, D = 64: 9.0 7.3,
+// 9.1 8.8, 9.4 9.8; 4 of a quarter of that up to it, 32 over 8 heads, D = 128: 10.8 8.2, 11.3 9.8, 11.4 11.8; 1
+// sequence, 28 over 4 heads: 11.2 9.8, 11.9 12.0, 12.1 13.9; 12, 28 over 4: 12.9 10.1, 13.1 12.1, 13.6 13.9.
 constexpr long long kWholeTokens = 512;
 
 template <int D, int NQ, bool HAD>
@@ -360,7 +367,7 @@ kvq_status check_attention(const kvq_config* cfg, const kvq_pages* p, const kvq_
     if (s != KVQ_OK) return s;
     if (q_heads < p->kv_heads || q_heads % p->kv_heads != 0) return KVQ_ERR_INVALID_ARG;
     if (q_heads / p->kv_heads > kMaxGroup || q_heads > 65535 || reaches(rows, q_heads, kMaxIndex) ||
-        reaches(b->n_seqs, kManyMost * (int64_t)q_heads, kMaxIndex))  // prepared queries are counted in 32 bits
+        reaches(b->n_seqs, kFewRows * (int64_t)q_heads, kMaxIndex))  // prepared queries are counted in 32 bits
         return KVQ_ERR_UNSUPPORTED;
     return KVQ_OK;
 }
@@ -440,7 +447,7 @@ kvq_status kvq_pages_read(const kvq_config* cfg, const kvq_pages* pages, const k
 size_t kvq_pages_attention_workspace_bytes(const kvq_config* cfg, const kvq_pages* pages, const kvq_batch* batch,
                                            int64_t rows, int32_t q_heads) {
     if (check_attention(cfg, pages, batch, rows, q_heads) != KVQ_OK) return 0;
-    const AttnPlan p = attn_plan(batch, rows, q_heads / pages->kv_heads, cfg->head_dim);
+    const AttnPlan p = attn_plan(batch, rows, q_heads / pages->kv_heads);
     return attn_workspace(p, sm_count(), cfg->head_dim, cfg->flags == KVQ_HADAMARD, q_heads, batch->n_seqs).bytes;
 }
 
@@ -463,7 +470,7 @@ kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, co
     if (!ok_ptr(ws) || ws_bytes < need) return KVQ_ERR_WORKSPACE;
     const int sms = sm_count();
     const bool had = cfg->flags == KVQ_HADAMARD;
-    const AttnPlan p = attn_plan(batch, rows, q_heads / pages->kv_heads, cfg->head_dim);
+    const AttnPlan p = attn_plan(batch, rows, q_heads / pages->kv_heads);
     const AttnWorkspace w = attn_workspace(p, sms, d, had, q_heads, batch->n_seqs);
     uint8_t* base = static_cast<uint8_t*>(ws);
     StepArgs g;
@@ -490,7 +497,7 @@ kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, co
     a.ml = reinterpret_cast<float*>(base + w.ml);
     a.part = reinterpret_cast<float*>(base + w.part);
     a.left = reinterpret_cast<float*>(base + w.left);
-    g.many = p.tiles ? many_rows(d) : 0;
+    g.many = p.tiles ? kFewBeside : 0;
     g.stretch = p.stretch;
     g.whole = 0;
     g.frag = reinterpret_cast<__half*>(base + w.frag);
@@ -500,7 +507,7 @@ kvq_status kvq_pages_attention(const kvq_config* cfg, const kvq_pages* pages, co
     t.a.meta = reinterpret_cast<int4*>(base + w.tile_meta);
     t.a.ml = reinterpret_cast<float*>(base + w.tile_ml);
     t.a.part = reinterpret_cast<float*>(base + w.tile_part);
-    t.many = many_rows(d);
+    t.many = kFewBeside;
     t.plan = reinterpret_cast<int4*>(base + w.plan);
     t.seq_cost = reinterpret_cast<long long*>(base + w.seq_cost);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
