@@ -71,6 +71,40 @@ def test_ordinary_batches(d, G, dtype, rotated, rows):
         want[at], want_lse[at] = prec.exact(q[at], *prec.stored(s, i, n), s.signs, np.arange(n - m, n), np.full(m, n))
     assert not prec.faults(out, lse, want, want_lse, dtype)
 
+@pytest.mark.parametrize("d,G,rotated,dtype", [(128, 16, True, "fp16"), (64, 16, False, "fp16"), (128, 33, False, "bf16")])
+def test_nearly_equal_weights_of_many_rows_over_thousands_of_tokens(d, G, rotated, dtype):
+    """The same for the many-row kernel: 160 sequences of 10 rows are more than
+    8192 tokens a CTA."""
+    import torch
+    n, m, tokens = 160, 10, 8192
+    s = Setup([(tokens, 1)], d=d, H=1, page=64, rotated=rotated)
+    k, v = prec.stored(s, 0, tokens)
+    dev = lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda()  # noqa: E731
+    s.batch = s.kvq.Batch(dev(np.arange(n + 1, dtype=np.int32) * m), dev(np.full(n, tokens, np.int32)),
+                          s.batch.table.repeat(n, 1).contiguous(), max_rows=m)
+    s.rows = n * m
+    q = s.tensor(G, dtype, scale=0.1)
+    out, lse = s.attend(q)
+    assert s.kvq.kvq_pages_read_errors() == 0
+    want = prec.exact(q, k, v, s.signs, np.tile(np.arange(tokens - m, tokens), n), np.full(n * m, tokens))
+    assert not prec.faults(out, lse, *want, dtype)
+
+
+@pytest.mark.parametrize("n,H,tokens", [(64, 2, 500), (65, 2, 500), (200, 1, 512), (222, 2, 100), (400, 1, 33)])
+def test_many_short_sequences(n, H, tokens):
+    """Caches that CTAs take whole, for so many sequences that a block finds its
+    own by a search; some of them empty."""
+    import torch
+    counts = [((i * 37) % (tokens + 1), 1) for i in range(n - 1)] + [(tokens, 1)]
+    s = Setup(counts, H=H, d=64, page=16, max_rows=1)
+    q = s.tensor(2 * H, "fp16")
+    out, lse = s.attend(q)
+    rows = {0, 1, n // 2, n - 2, n - 1} | {int(r) for r in s.rng.integers(0, n, 40)}
+    s.check(q, out, lse, "fp16", only=rows)
+    empty = torch.tensor([c == 0 for c, _ in counts], device="cuda")
+    assert not out[empty].any() and bool(torch.isneginf(lse[empty]).all()) and bool(torch.isfinite(lse[~empty]).all())
+
+
 def values_of(s, mags, keep=None):
     """New stored values of the setup's only sequence, of magnitudes mags
     [tokens]; `keep`: tokens whose values stay."""
