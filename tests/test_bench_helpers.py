@@ -95,3 +95,11 @@ def test_sampled_parity_of_the_bench(bench):
     flat[row // w.S, row % w.S] = oracle.pack_rows(q, bits)[0]
     res = bench.sampled_parity(w, bits, state, cache, pairs)
     assert res["code_mismatches"] == 1 and res["non_half_point_mismatches"] == 1 and res["half_point_cases"] == 0
+
+
+def test_the_committed_traffic_capture_is_of_the_committed_sources():
+    """A change of the decode kernels' sources, a comment's too, takes the
+    figure out of the bench's line until the capture is taken again."""
+    import importlib
+    import bench
+    assert importlib.reload(bench).decode_traffic() is not None
