@@ -336,6 +336,8 @@ typedef struct {
  * Row start[s] + i is thus token len[s] - (start[s+1] - start[s]) + i.  Rows
  * whose token is negative (more rows than tokens) are padding, and so are
  * rows before start[0], from start[n_seqs] on, and past the call's `rows`.
+ * start may name rows that the tensors do not hold, below 0 or from `rows` on
+ * (a part of a batch's rows: start moved down by the part's first row).
  * A generation step has one row a sequence, a prompt or a part of one many;
  * both may be in one batch, and a sequence may have no rows.
  * max_rows (host): the most rows one sequence has; 0 = not known.  It only

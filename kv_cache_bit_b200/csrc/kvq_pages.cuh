@@ -10,8 +10,8 @@
 // sequence and page, about as many instructions as half a vector, is then made
 // once for them.
 //
-// A warp's instructions for eight vectors (D = 128, rotated): 518 writing, in
-// packed fp32 pairs, 66 of them shuffles; 410 reading, whose butterflies are
+// A warp's instructions for eight vectors (D = 128, rotated): 517 writing, in
+// packed fp32 pairs, 66 of them shuffles; 387 reading, whose butterflies are
 // exact in fp16 pairs (sums of codes stay below 1024).  32 x 4096 rows, 8 kv
 // heads: 177 us to write (HBM would take 103), 126 us to read back (103).
 #pragma once
