@@ -26,8 +26,10 @@ def sources():
 
 TEST_LIB = os.path.join(OUT_DIR, "libkvq_waittest.so")
 
+# Not --split-compile: it halves the time, but takes registers and spills by chance, so that one source gave the
+# 8192-token prompt of the paged attention 1040 or 1165 us from build to build (1002 without it).
 _FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
-          "-I", os.path.join(ROOT, "include"), "--expt-relaxed-constexpr", "--split-compile=0"]
+          "-I", os.path.join(ROOT, "include"), "--expt-relaxed-constexpr"]
 
 
 def _deps(unit):

@@ -33,7 +33,7 @@
 // O stays in tensor memory; a row whose maximum rose by more than 2^kSlack
 // scales it there, once the step before is in it.
 // Measured (8192 rows and tokens, 32 query heads over 8, rotated, D = 128):
-// 1040 us, 530 TFLOP/s of 4 D a (row, token, head); the products and their
+// 1000 us, 550 TFLOP/s of 4 D a (row, token, head); the products and their
 // reads of shared memory (a 64-token product of 128 rows reads 6 KB in the 32
 // cycles that it computes) are busy 60% of it, the exponentials a third.
 #pragma once

@@ -158,3 +158,10 @@ def test_binding_refuses_missing_tensors_and_caches_on_the_host(kvq):
         with pytest.raises(kvq.KvqError) as e:
             call()
         assert e.value.status == kvq.KVQ_ERR_INVALID_ARG
+
+
+def test_one_source_is_one_program():
+    """nvcc's split compilation shares registers out by chance: the same source
+    built twice had kernels of 138 and 168 registers."""
+    from kv_cache_bit_b200 import build
+    assert not any("split-compile" in flag for flag in build._FLAGS)
