@@ -34,8 +34,8 @@
 //           tensor core aligns products by their exponent fields and drops what
 //           falls below: errors of 7e-4 of the values.)
 // Measured at 64 x 500 .. 8192 tokens, 32 query heads over 8, rotated, D = 128:
-// 298 warp instructions a 16-token tile, set-up and merging included (the
-// block cache's kernel: 332), 80 us; the loop itself reads at 5.8 TB/s.
+// 303 warp instructions a 16-token tile, set-up and merging included (the
+// block cache's kernel: 332), 81 us; the loop itself reads at 5.8 TB/s.
 #pragma once
 
 #include "kvq_pages_attn.cuh"
